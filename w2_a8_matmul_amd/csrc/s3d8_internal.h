@@ -8,6 +8,10 @@ namespace s3d8 {
 int fail(int code, const char *msg);
 // Clear the calling thread's last error (called by successful entry points).
 void clear_error();
+// The current device is a gfx950 GPU (checked once per device); its CU count.
+int check_device(int *num_cus);
+// The status of the launches just made (hipGetLastError).
+int launch_status();
 }  // namespace s3d8
 
 #endif
