@@ -414,6 +414,157 @@ int32_t s3d8_linear_unfused_ex(const int8_t *xq, const float *xs, int64_t M, int
 int32_t s3d8_dequant_ex(const uint8_t *packed, const void *table, int32_t format, int64_t N, int64_t K, int8_t *w,
                         void *stream);
 
+/* ------------------------------------------------ 4-bit weights, group scales */
+
+/* A second weight format beside S3D8: plain 4-bit integers with one scale per
+ * group of consecutive input columns (the block-scaled integer format that
+ * [PAPER] Sec. 4 sets beside S3D8), with the same per-token INT8
+ * activations, so that matrices of both formats can stand in one model.
+ *
+ * Format ("W4", canonical layout): for W [N][K] and a group of `group` input
+ * columns (a positive multiple of 32; the last group of a row may be shorter),
+ * G = ceil(K/group):
+ *     packed   uint8 [N][K/2], row-major: byte (n, j) holds the codes of input
+ *              columns 2j (low nibble) and 2j + 1 (high nibble), 0..15;
+ *     scales   uint16 [N][G]: bfloat16 bit patterns, finite;
+ *     zeros    uint8 [N][G], entries 0..15, or absent: every zero point is 8.
+ *   Weight: w_nk = scales[n][k / group] * (q_nk - z[n][k / group]).
+ * Linear:
+ *   acc_mng = sum over the columns k of group g of xq_mk * (q_nk - z_ng)
+ *             (exact INT32),
+ *   y_mn    = s_m * sum_g scales_ng * float(acc_mng)   (fp32 sums, in an order
+ *             that depends on the shape alone, so repeated calls give the
+ *             same bits). */
+
+/* Encode a matrix to W4 on the host.  Per group, in fp32 (IEEE division, round
+ * half to even):
+ *   zeros NULL:  a = max |w|, s = bf16(a / 7), q = clamp(rne(w / s), -8, 7) + 8;
+ *   otherwise:   lo = min(0, min w), hi = max(0, max w), s = bf16((hi - lo) / 15),
+ *                z = clamp(rne(-lo / s), 0, 15), q = clamp(rne(w / s) + z, 0, 15).
+ * A group whose scale is 0 has every code at its zero point (z = 8 there).
+ *   W            host fp32 [N][K], row-major, finite.
+ *   group        columns per scale, a positive multiple of 32.
+ *   num_threads  as for s3d8_pack; the result does not depend on it.
+ *   packed       out, host uint8 [N][K/2].
+ *   scales_bf16  out, host uint16 [N][ceil(K/group)].
+ *   zeros        out, host uint8 [N][ceil(K/group)], or NULL (see above).
+ * Synchronous; touches no GPU.  Errors: INVALID_ARG, SHAPE, NOMEM. */
+int32_t s3d8_w4_encode(const float *W, int64_t N, int64_t K, int64_t group, int32_t num_threads, uint8_t *packed,
+                       uint16_t *scales_bf16, uint8_t *zeros);
+
+/* Bytes of the tiled device layout of a W4 matrix (see s3d8_w4_tile):
+ * ceil(N/16) * ceil(K/128) * (1024 + 32 p + 16 p if it has zero points), with
+ * p scales per 128 columns: 1 if group is a multiple of 128 or at least K,
+ * else 2 if a multiple of 64, else 4.  -1 on bad sizes. */
+int64_t s3d8_w4_tiled_bytes(int64_t N, int64_t K, int64_t group, int32_t has_zeros);
+
+/* Re-lay a W4 matrix into the tiled device layout read by s3d8_w4_linear,
+ * once, before the weights are used: fragments of 16 channels x 128 columns
+ * (1 KiB, one 16-byte piece per lane of a wave, in the operand order of the
+ * INT8 matrix instructions), then the scales and the zero points, p per
+ * channel and 128 columns, in the same order.  (The layout is internal to
+ * the library.)
+ *   packed, scales_bf16, zeros   device, canonical layout; zeros may be NULL;
+ *                scales_bf16 2-B aligned.
+ *   tiled        out, device, 16-B aligned, s3d8_w4_tiled_bytes(N, K, group,
+ *                zeros != NULL) bytes.
+ * Errors: INVALID_ARG, SHAPE (group not a multiple of 32, or over 2^31 tiled
+ * bytes), ALIGN, DEVICE, HIP. */
+int32_t s3d8_w4_tile(const uint8_t *packed, const uint16_t *scales_bf16, const uint8_t *zeros, int64_t N, int64_t K,
+                     int64_t group, uint8_t *tiled, void *stream);
+
+/* The linear layer on a W4 matrix and pre-quantised activations.
+ *   xq           device int8 [M][K], 16-B aligned (from s3d8_quant_act,
+ *                s3d8_block_norm or s3d8_glu_act).
+ *   xs           device fp32 [M].
+ *   tiled        device, from s3d8_w4_tile, 16-B aligned.
+ *   tiled_bytes  its size: exactly s3d8_w4_tiled_bytes(N, K, group, has_zeros),
+ *                so that a matrix laid out for other arguments is refused.
+ *   group, has_zeros   as the matrix was laid out.
+ *   y            out, device [M][N] of fp32 or bf16 (per out_type).
+ *   out_type     S3D8_OUT_F32 or S3D8_OUT_BF16.
+ * Errors: INVALID_ARG (also tiled_bytes), SHAPE, ALIGN, DEVICE, HIP. */
+int32_t s3d8_w4_linear(const int8_t *xq, const float *xs, int64_t M, int64_t K, int64_t N, const uint8_t *tiled,
+                       int64_t tiled_bytes, int64_t group, int32_t has_zeros, void *y, int32_t out_type, void *stream);
+
+/* s3d8_quant_act followed by s3d8_w4_linear, from fp32 activations.
+ *   x, xq, xs    as for s3d8_forward (xq and xs are outputs).
+ *   the rest     as for s3d8_w4_linear.
+ * Errors: as s3d8_w4_linear. */
+int32_t s3d8_w4_forward(const float *x, int64_t M, int64_t K, int64_t N, const uint8_t *tiled, int64_t tiled_bytes,
+                        int64_t group, int32_t has_zeros, void *y, int32_t out_type, int8_t *xq, float *xs,
+                        void *stream);
+
+/* -------------------------------------------- between the linears of a block */
+
+/* Types of a [M][K] row matrix.  Inputs are F32 or BF16; outputs may also be
+ * CODES: int8 [M][K] with fp32 [M] scales, as s3d8_quant_act leaves them. */
+#define S3D8_ROWS_F32 0
+#define S3D8_ROWS_BF16 1
+#define S3D8_ROWS_CODES 2
+
+#define S3D8_NORM_RMS 0
+#define S3D8_NORM_LAYER 1
+
+/* Arguments of s3d8_block_norm.  Every pointer is device memory. */
+typedef struct s3d8_block_norm_args {
+    const void *h;            /* [M][K], h_type: the residual stream                    */
+    const void *branch;       /* [M][K], branch_type: a block's output, or NULL         */
+    const float *post_weight; /* [K]: the norm after the block, or NULL (none)          */
+    const float *post_bias;   /* [K] or NULL (LAYER with post_weight only)              */
+    const float *gate;        /* [1], or [K] with gate_channels, or NULL (1)            */
+    const float *weight;      /* [K]: the norm before the next block                    */
+    const float *bias;        /* [K] or NULL (LAYER only)                               */
+    void *h_out;              /* out, [M][K], h_type; may be h; NULL iff branch is NULL */
+    void *rows;               /* out, [M][K], out_type F32 or BF16; NULL for CODES      */
+    int8_t *xq;               /* out, int8 [M][K] for CODES, else NULL                  */
+    float *xs;                /* out, fp32 [M] for CODES, else NULL                     */
+    int64_t M, K;
+    float residual_scale, eps;
+    int32_t kind;             /* S3D8_NORM_RMS or S3D8_NORM_LAYER, for both norms       */
+    int32_t h_type, branch_type, out_type;
+    int32_t gate_channels;    /* gate is [K] rather than [1]                            */
+    int32_t gate_tanh;        /* the gate's factor is tanh(gate)                        */
+} s3d8_block_norm_args;
+
+/* What stands between two blocks of a decoder or encoder layer, in one launch:
+ * the norm after a block, its gate, the scaled residual sum, the norm before
+ * the next block, and the next linear's activation quantisation.  Per row:
+ *   t   = gamma * (post_weight ? N(branch; post_weight, post_bias) : branch),
+ *         gamma = gate or tanh(gate) (computed in 64 bits, rounded to fp32);
+ *   h'  = residual_scale * h + t, rounded to h_type, stored in h_out
+ *         (h' = h when branch is NULL);
+ *   u   = N(h'; weight, bias);
+ *   out = u as fp32, rounded to bf16, or as the codes and scale that
+ *         s3d8_quant_act makes of u.
+ *   RMS:    N(v; w)    = (v * r) * w,             r = 1 / sqrt(sum(v^2) / K + eps)
+ *   LAYER:  N(v; w, b) = ((v - mu) * r) * w + b,  mu = sum(v) / K,
+ *                                                 r = 1 / sqrt(sum((v - mu)^2) / K + eps)
+ * The sums, mu and r are computed in 64 bits and then rounded to fp32; every
+ * other operation is one IEEE fp32 operation.  (The codes are whole numbers:
+ * sums in 64 bits keep them from depending on the order of summation.)
+ * K is a positive multiple of 16, at most 65536.  Row matrices must be 16-B
+ * aligned, fp32 vectors [K] as well; values finite, eps > 0.  Outputs other
+ * than h_out = h must not overlap inputs.
+ * Errors: INVALID_ARG, SHAPE, ALIGN, DEVICE, HIP. */
+int32_t s3d8_block_norm(const s3d8_block_norm_args *args, void *stream);
+
+/* The gated activation between the two halves of an MLP: a = SiLU(gate) * up,
+ * SiLU(g) = g / (1 + exp(-g)), computed in 64 bits and rounded once to fp32, then
+ * output as fp32, rounded to bf16, or as the codes and scale that
+ * s3d8_quant_act makes of it.
+ *   gate, up     device [M] rows of K values of in_type (S3D8_ROWS_F32 or
+ *                S3D8_ROWS_BF16), finite.
+ *   ld_gate, ld_up   elements between rows (at least K, multiples of 4), e.g. 2K for
+ *                the halves of one [M][2K] matrix.  gate and up aligned to 4
+ *                elements.
+ *   rows         out, device [M][K] for out_type F32 or BF16, 16-B aligned, else NULL.
+ *   xq, xs       out, int8 [M][K] (16-B aligned) and fp32 [M] for CODES, else NULL.
+ * K is a positive multiple of 16, at most 65536.
+ * Errors: INVALID_ARG, SHAPE, ALIGN, DEVICE, HIP. */
+int32_t s3d8_glu_act(const void *gate, int64_t ld_gate, const void *up, int64_t ld_up, int64_t M, int64_t K,
+                     int32_t in_type, int32_t out_type, void *rows, int8_t *xq, float *xs, void *stream);
+
 /* Matrix-core rate probe: a measurement utility for reading the GEMM's
  * INT8 rate against what the matrix cores sustain, not part of the method.
  * `workgroups` workgroups of 256 threads (4 waves) each run `iters` rounds

@@ -1,0 +1,316 @@
+"""The block norm and the gated activation on the GPU, bit for bit against
+their definitions in numpy, and a run of a whole MLP block."""
+import numpy as np
+import pytest
+
+import block_reference as ref
+import oracle
+import workloads
+from parity_inputs import random_format
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+s3d8 = pytest.importorskip("w2_a8_matmul_amd")
+
+F = np.float32
+
+
+def rng(*words):
+    return np.random.Generator(np.random.PCG64(np.random.SeedSequence(list(words))))
+
+
+def rows(g, M, K, bf16, scale=1.0):
+    x = (g.standard_normal((M, K)) * scale * np.where(g.random((M, K)) < 0.01, 20, 1)).astype(F)
+    return ref.round_bf16(x) if bf16 else x
+
+
+def dev(x, gpu, bf16=False):
+    t = torch.from_numpy(np.ascontiguousarray(x)).to(gpu)
+    return t.to(torch.bfloat16) if bf16 else t
+
+
+def same(t, x):
+    """Bit for bit (bf16 tensors as the fp32 values they hold); -0 and 0 differ."""
+    got = t.float().cpu().numpy() if t.dtype == torch.bfloat16 else t.cpu().numpy()
+    if got.dtype == F:
+        assert np.array_equal(got.view(np.uint32), np.asarray(x, F).view(np.uint32)), np.abs(got - x).max()
+    else:
+        assert np.array_equal(got, x)
+
+
+def check_rows(out, got, u):
+    if out == "codes":
+        codes, xs = ref.quantise(u)
+        same(got[0], codes)
+        same(got[1], xs)
+    else:
+        same(got, ref.round_bf16(u) if out == "bf16" else u)
+
+
+def norm_case(gpu, M, K, kind="rms", h_bf=False, b_bf=False, branch=True, post=False, post_bias=False, bias=False,
+              gate=None, rs=1.0, out="codes", eps=1e-5, in_place=False, seed=0):
+    g = rng(7300, M, K, seed)
+    h = rows(g, M, K, h_bf)
+    w = (1 + 0.1 * g.standard_normal(K)).astype(F)
+    vec = lambda: (0.1 * g.standard_normal(K)).astype(F)  # noqa: E731
+    b = vec() if bias else None
+    br = rows(g, M, K, b_bf, 0.5) if branch else None
+    pw = vec() + F(1) if post else None
+    pb = vec() if post_bias else None
+    gt = None if gate is None else g.standard_normal(K if "channel" in gate else 1).astype(F)
+    tanh = gate is not None and "tanh" in gate
+    h_r, u_r = ref.block_norm(h, w, b, br, pw, pb, gt, tanh, rs, eps, kind, h_bf)
+    to = lambda x: None if x is None else dev(x, gpu)  # noqa: E731
+    dh = dev(h, gpu, h_bf)
+    got = s3d8.block_norm(dh, to(w), to(b), branch=None if br is None else dev(br, gpu, b_bf), post_weight=to(pw),
+                          post_bias=to(pb), gate=to(gt), tanh_gate=tanh, residual_scale=rs, eps=eps, kind=kind, out=out,
+                          h_out=dh if in_place else None)
+    if branch:
+        assert (got[0] is dh) == in_place
+        same(got[0], h_r)
+        got = got[1:] if out == "codes" else got[1]
+        if not in_place:
+            same(dh, h)
+    check_rows(out, got, u_r)
+
+
+@pytest.mark.parametrize("out", ["codes", "f32", "bf16"])
+@pytest.mark.parametrize("h_bf,b_bf", [(False, False), (True, False), (False, True), (True, True)])
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+def test_norm_types(gpu, kind, h_bf, b_bf, out):
+    for post in (False, True):
+        norm_case(gpu, 5, 656, kind, h_bf, b_bf, post=post, post_bias=post and kind == "layer", bias=kind == "layer",
+                  out=out, rs=0.5)
+
+
+@pytest.mark.parametrize("gate", [None, "scalar", "tanh", "channel", "channel tanh"])
+@pytest.mark.parametrize("kind,post", [("rms", False), ("rms", True), ("layer", False), ("layer", True)])
+def test_norm_gates(gpu, kind, post, gate):
+    norm_case(gpu, 3, 1280, kind, b_bf=True, post=post, post_bias=kind == "layer" and post, gate=gate, rs=1.25)
+    norm_case(gpu, 2, 48, kind, h_bf=True, post=post, gate=gate, in_place=True, bias=kind == "layer")
+
+
+# widths at and around every thread-count and register step
+@pytest.mark.parametrize("K", [16, 32, 240, 1024, 1040, 2048, 2064, 4080, 4096, 4112, 8192, 8208, 14336, 16384, 16400,
+                               32768, 65536])
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+def test_norm_widths(gpu, kind, K):
+    norm_case(gpu, 2, K, kind, post=True, gate="tanh", bias=kind == "layer")
+    norm_case(gpu, 1, K, kind, h_bf=True, b_bf=True, out="f32")
+    norm_case(gpu, 3, K, kind, branch=False)
+
+
+@pytest.mark.parametrize("M", [1, 2, 7, 64, 511, 2048, 5000])
+def test_norm_rows(gpu, M):
+    norm_case(gpu, M, 512, h_bf=True, b_bf=True, post=True, seed=1)
+    norm_case(gpu, M, 1280, "layer", gate="tanh", out="bf16", seed=2)
+
+
+def test_norm_edge_rows(gpu):
+    """Zero rows (codes and scale 0), a single value, a constant row under LAYER, tiny and large values."""
+    K = 256
+    h = np.zeros((7, K), F)
+    h[1, 17] = -3.5
+    h[2] = 4.25
+    h[3] = 1e-30 * np.arange(1, K + 1, dtype=F)
+    h[4] = 1e15
+    h[4, 3] = -3e15
+    h[5] = 1e-42
+    h[6, ::2], h[6, 1::2] = 1.0, -1.0
+    w = np.ones(K, F)
+    w[5] = -2.0
+    w[7] = 0.0
+    for kind in ("rms", "layer"):
+        for br in (None, np.zeros_like(h), h * F(0.5)):
+            for out in ("codes", "f32"):
+                h_r, u_r = ref.block_norm(h, w, None, br, kind=kind)
+                got = s3d8.block_norm(dev(h, gpu), dev(w, gpu), branch=None if br is None else dev(br, gpu), kind=kind,
+                                      out=out)
+                if br is not None:
+                    same(got[0], h_r)
+                    got = got[1:] if out == "codes" else got[1]
+                check_rows(out, got, u_r)
+
+
+def test_norm_leaves_its_neighbours(gpu):
+    M, K = 3, 272
+    g = rng(7301)
+    h, br, w = rows(g, M, K, True), rows(g, M, K, True), np.ones(K, F)
+    pad = 1024
+    hb = torch.full((M * K + 2 * pad,), 5.0, dtype=torch.bfloat16, device=gpu)
+    qb = torch.full((M * K + 2 * pad,), 9, dtype=torch.int8, device=gpu)
+    sb = torch.full((M + 16,), 3.0, device=gpu)
+    s3d8.block_norm(dev(h, gpu, True), dev(w, gpu), branch=dev(br, gpu, True), h_out=hb[pad:pad + M * K].view(M, K),
+                    xq=qb[pad:pad + M * K].view(M, K), xs=sb[8:8 + M])
+    h_r, u_r = ref.block_norm(h, w, None, br, h_bf16=True)
+    same(hb[pad:pad + M * K].view(M, K), h_r)
+    check_rows("codes", (qb[pad:pad + M * K].view(M, K), sb[8:8 + M]), u_r)
+    for t, v in ((hb, 5), (qb, 9)):
+        assert (t[:pad] == v).all() and (t[pad + M * K:] == v).all()
+    assert (sb[:8] == 3).all() and (sb[8 + M:] == 3).all()
+
+
+# ------------------------------------------------------------------ gated activation
+@pytest.mark.parametrize("out", ["codes", "f32", "bf16"])
+@pytest.mark.parametrize("bf", [False, True])
+@pytest.mark.parametrize("fused", [False, True])
+@pytest.mark.parametrize("M,K", [(1, 16), (1, 4096), (1, 14336), (5, 1744), (33, 4112), (130, 8192), (700, 1040),
+                                 (2, 16400), (2, 65536), (1, 32768)])
+def test_glu(gpu, M, K, fused, bf, out):
+    g = rng(7302, M, K)
+    both = rows(g, M, 2 * K, bf, 2.0)
+    gate, up = both[:, :K], both[:, K:]
+    d = dev(both, gpu, bf)
+    dg, du = (d[:, :K], d[:, K:]) if fused else (d[:, :K].contiguous(), d[:, K:].contiguous())
+    check_rows(out, s3d8.glu_act(dg, du, out=out), ref.glu(gate, up))
+
+
+def test_glu_values(gpu):
+    """Every magnitude: far negative gates (the result underflows to -0), far positive ones, zeros, subnormals."""
+    K = 4096
+    mag = np.concatenate([np.geomspace(1e-44, 3e38, K // 2 - 2), [0.0, 1.0]]).astype(F)
+    gate = np.stack([np.concatenate([mag, -mag]), np.linspace(-110, 110, K).astype(F),
+                     np.linspace(-800, -80, K).astype(F), np.linspace(-1e-3, 1e-3, K).astype(F),
+                     np.zeros(K, F), np.full(K, -2000, F)])
+    up = np.stack([np.ones(K, F), np.full(K, -1.5, F), np.full(K, 1e30, F), np.linspace(-2, 2, K).astype(F),
+                   np.ones(K, F), np.full(K, 3e38, F)])
+    a = ref.glu(gate, up)
+    assert np.isfinite(a).all()
+    for out in ("f32", "codes"):
+        check_rows(out, s3d8.glu_act(dev(gate, gpu), dev(up, gpu), out=out), a)
+
+
+def test_glu_rounding_borders(gpu):
+    """Rows whose quotients x / s lie on and one fp32 step around k + 1/2."""
+    K = 2048
+    g = rng(7303)
+    gate = np.full((8, K), 60.0, F)  # SiLU(60) = 60 to the last bit
+    up = np.zeros((8, K), F)
+    for r in range(8):
+        top = F(127) * F(2.0 ** (r - 4))
+        v = ((g.integers(-126, 126, K) + 0.5) * 2.0 ** (r - 4)).astype(F)
+        v = np.where(np.arange(K) % 3 == 0, np.nextafter(v, F(np.inf)), np.where(np.arange(K) % 3 == 1, v, np.nextafter(v, F(-np.inf))))
+        up[r] = v / F(60)
+        up[r, 0] = top / F(60)
+    check_rows("codes", s3d8.glu_act(dev(gate, gpu), dev(up, gpu)), ref.glu(gate, up))
+
+
+def test_refusals(gpu):
+    h, w = torch.zeros((2, 64), device=gpu), torch.ones(64, device=gpu)
+    with pytest.raises(TypeError):
+        s3d8.block_norm(h.half(), w)
+    with pytest.raises(TypeError):
+        s3d8.block_norm(h, w.bfloat16())
+    with pytest.raises(ValueError):
+        s3d8.block_norm(h, w[:32])
+    with pytest.raises(ValueError):
+        s3d8.block_norm(h.t(), w[:2])
+    with pytest.raises(ValueError):
+        s3d8.block_norm(h, w, branch=h[:1])
+    with pytest.raises(ValueError):
+        s3d8.block_norm(h, w, branch=h, gate=torch.ones(3, device=gpu))
+    with pytest.raises(ValueError):
+        s3d8.block_norm(h, w, h_out=h)
+    with pytest.raises(ValueError):
+        s3d8.block_norm(h, w, kind="batch")
+    with pytest.raises(ValueError):
+        s3d8.block_norm(h, w, out="int8")
+    with pytest.raises(ValueError):
+        s3d8.block_norm(h, w, rows=torch.empty_like(h))
+    with pytest.raises(ValueError):
+        s3d8.block_norm(h, w, out="f32", xs=torch.empty(2, device=gpu))
+    with pytest.raises(TypeError):
+        s3d8.block_norm(h, w, out="bf16", rows=torch.empty_like(h))
+    with pytest.raises(s3d8.S3D8Error):
+        s3d8.block_norm(h, w, gate=torch.ones(1, device=gpu))  # no branch
+    with pytest.raises(s3d8.S3D8Error):
+        s3d8.block_norm(h, w, w)  # RMS takes no bias
+    with pytest.raises(s3d8.S3D8Error):
+        s3d8.block_norm(h[:, :40].contiguous(), w[:40].contiguous())
+    with pytest.raises(ValueError):
+        s3d8.glu_act(h, h[:1])
+    with pytest.raises(ValueError):
+        s3d8.glu_act(h.t(), h.t())
+    with pytest.raises(TypeError):
+        s3d8.glu_act(h.half(), h.half())
+    with pytest.raises(ValueError):
+        s3d8.glu_act(h, h.bfloat16())
+    with pytest.raises(s3d8.S3D8Error):
+        s3d8.glu_act(torch.zeros((2, 66), device=gpu)[:, 1:65], h)  # rows not aligned to 4 elements
+    torch.cuda.synchronize()
+
+
+# ------------------------------------------------------------------ together
+class Block:
+    """An MLP block: norm -> gate and up (one W4 matrix) -> gated activation -> down (S3D8) -> residual and next norm."""
+
+    def __init__(self, gpu, M, K, I, seed):
+        g = rng(7304, M, K, I, seed)
+        self.M, self.K, self.I = M, K, I
+        self.h, self.attn = rows(g, M, K, True), rows(g, M, K, False, 0.3)
+        self.w1, self.w2 = ((1 + 0.1 * g.standard_normal(K)).astype(F) for _ in range(2))
+        self.q = g.integers(0, 16, (2 * I, K), dtype=np.uint8)
+        self.scales = ref.bf16_bits(g.lognormal(-5, 0.3, (2 * I, -(-K // 64))).astype(F))
+        self.C, self.alpha, self.packed = random_format([7305, K, I], K, I)
+        self.lin = s3d8.W4Linear(ref.pack(self.q), self.scales, 64, device=gpu)
+        self.tiled = s3d8.tile(dev(self.packed, gpu), K)
+        self.dC, self.dalpha = dev(self.C, gpu), dev(self.alpha.view(np.int16), gpu)
+        self.dh, self.dattn, self.dw1, self.dw2 = dev(self.h, gpu, True), dev(self.attn, gpu), dev(self.w1, gpu), dev(self.w2, gpu)
+
+    def run(self):
+        h1, xq, xs = s3d8.block_norm(self.dh, self.dw1, branch=self.dattn)
+        both = self.lin.linear(xq, xs)
+        aq, as_ = s3d8.glu_act(both[:, :self.I], both[:, self.I:])
+        down = s3d8.linear(aq, as_, self.tiled, self.dC, self.dalpha, self.K)
+        h2, nq, ns = s3d8.block_norm(h1, self.dw2, branch=down, residual_scale=0.5)
+        return h1, xq, xs, both, aq, as_, down, h2, nq, ns
+
+    def check(self, out):
+        """Every stage against its definition on the inputs that the stage had."""
+        h1, xq, xs, both, aq, as_, down, h2, nq, ns = (t.float().cpu().numpy() if t.dtype == torch.bfloat16
+                                                       else t.cpu().numpy() for t in out)
+        h_r, u = ref.block_norm(self.h, self.w1, None, self.attn, h_bf16=True)
+        codes, s = ref.quantise(u)
+        assert np.array_equal(h1, h_r) and np.array_equal(xq, codes) and np.array_equal(xs, s)
+        y, size = ref.w4_linear(xq, xs, self.q, self.scales, None, 64)
+        assert (np.abs(both - y) <= ref.w4_tolerance(y, size, self.K, False)).all()
+        codes, s = ref.quantise(ref.glu(both[:, :self.I], both[:, self.I:]))
+        assert np.array_equal(aq, codes) and np.array_equal(as_, s)
+        w = oracle.decode(self.packed, self.C, self.K, self.I)
+        acc = aq.astype(np.int64) @ w.astype(np.int64).T
+        y = (as_[:, None] * acc.astype(F)) * ref.bf16_value(self.alpha[:self.K])[None, :]
+        assert np.array_equal(down, y)
+        h_r, u = ref.block_norm(h1, self.w2, None, down, residual_scale=0.5, h_bf16=True)
+        codes, s = ref.quantise(u)
+        assert np.array_equal(h2, h_r) and np.array_equal(nq, codes) and np.array_equal(ns, s)
+
+
+@pytest.mark.parametrize("M,K,I", [(1, 256, 768), (6, 1040, 656), (40, 512, 1296)])
+def test_mlp_block(gpu, M, K, I):
+    b = Block(gpu, M, K, I, 0)
+    b.check(b.run())
+
+
+@pytest.mark.parametrize("M", [1, 24])
+def test_mlp_block_in_a_graph(gpu, M):
+    """Captured once and replayed, with eager work and new inputs between the replays."""
+    b, other = Block(gpu, M, 512, 768, 1), Block(gpu, M, 512, 768, 2)
+    b.run()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream(gpu)
+    side.wait_stream(torch.cuda.current_stream(gpu))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        out = b.run()
+    for seed in (3, 4, 5):
+        g = rng(7306, seed)
+        b.h, b.attn = rows(g, M, 512, True), rows(g, M, 512, False, 0.3)
+        b.dh.copy_(dev(b.h, gpu, True))
+        b.dattn.copy_(dev(b.attn, gpu))
+        graph.replay()
+        other.check(other.run())
+        torch.cuda.synchronize()
+        b.check(out)
+        for e, r in zip(b.run(), out):
+            assert torch.equal(e, r)

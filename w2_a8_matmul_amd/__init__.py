@@ -12,6 +12,11 @@ Quantization of VLMs" (Sec. 3.4, Eq. 1) with the byte layout of the blog
 take 3D8 weights (``fmt="3d8"``: the table is int8 [256][3] signed
 centroids indexed by the whole byte, the format the blog sets beside S3D8)
 and write bf16 outputs (``out="bf16"``, as the blog's fused kernel does).
+
+Beside it: the same linear layer on plain 4-bit weights with group scales
+(``w4_linear``, ``W4Linear``), and what stands between the linears of a block,
+ending in the INT8 codes they read: ``block_norm`` (norms around a block, gate,
+residual sum) and ``glu_act`` (SiLU-gated activation).
 """
 from __future__ import annotations
 
@@ -26,6 +31,7 @@ __all__ = [
     "tile", "quant_act", "linear", "linear_unfused", "unfused_workspace_bytes", "forward", "dequant",
     "PackedLinear", "hbm_read_probe", "mfma_rate_probe", "encode_device", "forward_batch",
     "linear_splitk", "splitk_auto", "splitk_workspace_bytes",
+    "w4_encode", "w4_tiled_bytes", "w4_tile", "w4_linear", "w4_forward", "W4Linear", "block_norm", "glu_act",
 ]
 
 
@@ -467,3 +473,222 @@ class PackedLinear:
 
     def __call__(self, x):
         return forward(x, self.tiled, self.centroids, self.scales, self.N)
+
+
+# ------------------------------------------------------------------ 4-bit weights, group scales
+def w4_tiled_bytes(N: int, K: int, group: int, zeros: bool = False) -> int:
+    return int(lib().s3d8_w4_tiled_bytes(N, K, group, int(zeros)))
+
+
+def w4_encode(W, group: int = 64, zeros: bool = False, num_threads: int = 0):
+    """Encode W (fp32 [N][K], host) to 4-bit codes with a bf16 scale per
+    ``group`` columns, with zero points if ``zeros``: (packed uint8 [N][K/2],
+    scales_bf16 uint16 [N][ceil(K/group)], zeros uint8 of that shape or None)."""
+    W = np.ascontiguousarray(W, dtype=np.float32)
+    N, K = W.shape
+    shape = (N, -(-K // max(group, 1)))
+    packed = np.empty((N, K // 2), np.uint8)
+    scales = np.empty(shape, np.uint16)
+    z = np.empty(shape, np.uint8) if zeros else None
+    call("s3d8_w4_encode", _np_ptr(W), N, K, group, num_threads, _np_ptr(packed), _np_ptr(scales),
+         _np_ptr(z) if zeros else None)
+    return packed, scales, z
+
+
+def w4_tile(packed, scales, group: int, zeros=None, tiled=None):
+    """Re-lay a device W4 matrix (packed [N][K/2], scales and optionally zeros
+    [N][ceil(K/group)]) into the layout read by w4_linear (done once per
+    matrix)."""
+    torch = _torch()
+    _dev_check(packed, torch.uint8, "packed")
+    N, K = packed.shape[0], 2 * packed.shape[1]
+    scales = _scales_view(scales)
+    groups = N * -(-K // max(group, 1))
+    _dev_check(scales, torch.int16, "scales", packed.device, numel=groups)
+    if zeros is not None:
+        _dev_check(zeros, torch.uint8, "zeros", packed.device, numel=groups)
+    nbytes = max(w4_tiled_bytes(N, K, group, zeros is not None), 0)
+    if tiled is None:
+        tiled = torch.empty((nbytes,), dtype=torch.uint8, device=packed.device)
+    _dev_check(tiled, torch.uint8, "tiled", packed.device, numel=nbytes)
+    with torch.cuda.device(packed.device):
+        call("s3d8_w4_tile", packed.data_ptr(), scales.data_ptr(), zeros.data_ptr() if zeros is not None else None,
+             N, K, group, tiled.data_ptr(), _stream(packed))
+    return tiled
+
+
+def w4_linear(xq, xs, tiled, N: int, group: int, zeros: bool = False, y=None, out: str = "f32"):
+    """Linear layer on a tiled W4 matrix and pre-quantised activations: y [M][N],
+    fp32 or bf16.  ``group`` and ``zeros`` (whether the matrix has zero points)
+    as it was laid out."""
+    torch = _torch()
+    _, o = _variant("s3d8", out)
+    _dev_check(xq, torch.int8, "xq")
+    dev = xq.device
+    M, K = xq.shape
+    _dev_check(xs, torch.float32, "xs", dev, min_numel=M)
+    _dev_check(tiled, torch.uint8, "tiled", dev)
+    y = _y_out(y, M, N, out, dev)
+    with torch.cuda.device(dev):
+        call("s3d8_w4_linear", xq.data_ptr(), xs.data_ptr(), M, K, N, tiled.data_ptr(), tiled.numel(), group,
+             int(zeros), y.data_ptr(), o, _stream(xq))
+    return y
+
+
+def w4_forward(x, tiled, N: int, group: int, zeros: bool = False, y=None, xq=None, xs=None, return_all: bool = False,
+               out: str = "f32"):
+    """The whole path from fp32 x [M][K]: quantise, then w4_linear.  Returns y,
+    or (y, xq, xs) with ``return_all``."""
+    torch = _torch()
+    _, o = _variant("s3d8", out)
+    _dev_check(x, torch.float32, "x")
+    dev = x.device
+    M, K = x.shape
+    _dev_check(tiled, torch.uint8, "tiled", dev)
+    y = _y_out(y, M, N, out, dev)
+    xq, xs = _codes_out(xq, xs, M, K, dev)
+    with torch.cuda.device(dev):
+        call("s3d8_w4_forward", x.data_ptr(), M, K, N, tiled.data_ptr(), tiled.numel(), group, int(zeros),
+             y.data_ptr(), o, xq.data_ptr(), xs.data_ptr(), _stream(x))
+    return (y, xq, xs) if return_all else y
+
+
+class W4Linear:
+    """A W4 weight matrix resident in device memory, in the tiled layout
+    (``packed``, ``scales``, ``zeros``: numpy arrays or device tensors)."""
+
+    def __init__(self, packed, scales, group: int, zeros=None, device="cuda"):
+        torch = _torch()
+
+        def resident(a, kind):
+            if isinstance(a, torch.Tensor):
+                return a.to(device).contiguous()
+            return torch.as_tensor(np.ascontiguousarray(a, kind).view(np.int16 if kind == np.uint16 else kind)).to(device)
+
+        packed = resident(packed, np.uint8)
+        self.N, self.K, self.group, self.zeros = packed.shape[0], 2 * packed.shape[1], int(group), zeros is not None
+        self.tiled = w4_tile(packed, resident(scales, np.uint16), self.group,
+                             resident(zeros, np.uint8) if self.zeros else None)
+
+    @classmethod
+    def from_weights(cls, W, group: int = 64, zeros: bool = False, device="cuda"):
+        packed, scales, z = w4_encode(W, group, zeros)
+        return cls(packed, scales, group, z, device)
+
+    def linear(self, xq, xs, y=None, out: str = "f32"):
+        return w4_linear(xq, xs, self.tiled, self.N, self.group, self.zeros, y, out)
+
+    def __call__(self, x, out: str = "f32"):
+        return w4_forward(x, self.tiled, self.N, self.group, self.zeros, out=out)
+
+
+# ------------------------------------------------------------------ between the linears of a block
+_ROWS = {"f32": 0, "bf16": 1, "codes": 2}
+_KINDS = {"rms": 0, "layer": 1}
+
+
+def _row_type(t, name):
+    torch = _torch()
+    if t.dtype == torch.float32:
+        return 0
+    if t.dtype == torch.bfloat16:
+        return 1
+    raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+
+
+def _rows_out(out, rows, xq, xs, M, K, device):
+    """The outputs of block_norm / glu_act: (rows, None, None) or (None, xq, xs)."""
+    torch = _torch()
+    if out not in _ROWS:
+        raise ValueError(f"out must be one of {list(_ROWS)}")
+    if out == "codes":
+        if rows is not None:
+            raise ValueError("rows goes with out='f32' or 'bf16'")
+        return (None, *_codes_out(xq, xs, M, K, device))
+    if xq is not None or xs is not None:
+        raise ValueError("xq and xs go with out='codes'")
+    dtype = torch.float32 if out == "f32" else torch.bfloat16
+    if rows is None:
+        rows = torch.empty((M, K), dtype=dtype, device=device)
+    else:
+        _dev_check(rows, dtype, "rows", device, numel=M * K)
+    return rows, None, None
+
+
+def _ptr(t):
+    return t.data_ptr() if t is not None else None
+
+
+def block_norm(h, weight, bias=None, *, branch=None, post_weight=None, post_bias=None, gate=None,
+               tanh_gate: bool = False, residual_scale: float = 1.0, eps: float = 1e-5, kind: str = "rms",
+               out: str = "codes", h_out=None, rows=None, xq=None, xs=None):
+    """Norm after a block, gate, residual sum, norm before the next block and its
+    activation quantisation, in one launch (see s3d8_block_norm):
+
+      h' = residual_scale * h + gate * N(branch; post_weight, post_bias),  u = N(h'; weight, bias)
+
+    ``h``, ``branch``: fp32 or bf16 [M][K]; ``weight``, ``bias``, ``post_weight``,
+    ``post_bias``: fp32 [K] (no post norm without ``post_weight``); ``gate``: fp32
+    [1] or [K], used as tanh(gate) with ``tanh_gate``; ``kind``: "rms" or "layer".
+    ``h_out`` may be ``h``.  Without ``branch``, u is the norm of h.
+
+    Returns (h', xq, xs) for ``out="codes"`` and (h', u) for "f32" / "bf16";
+    without ``branch``, (xq, xs) or u."""
+    torch = _torch()
+    if kind not in _KINDS:
+        raise ValueError(f"kind must be one of {list(_KINDS)}")
+    ht = _row_type(h, "h")
+    _dev_check(h, h.dtype, "h")
+    M, K = h.shape
+    dev = h.device
+    bt = 0
+    if branch is not None:
+        bt = _row_type(branch, "branch")
+        _dev_check(branch, branch.dtype, "branch", dev, numel=M * K)
+        if h_out is None:
+            h_out = torch.empty_like(h)
+        else:
+            _dev_check(h_out, h.dtype, "h_out", dev, numel=M * K)
+    elif h_out is not None:
+        raise ValueError("h_out goes with branch")
+    for name, v in (("weight", weight), ("bias", bias), ("post_weight", post_weight), ("post_bias", post_bias)):
+        if v is not None:
+            _dev_check(v, torch.float32, name, dev, numel=K)
+    channels = 0
+    if gate is not None:
+        channels = int(gate.numel() != 1)
+        _dev_check(gate, torch.float32, "gate", dev, numel=K if channels else 1)
+    rows, xq, xs = _rows_out(out, rows, xq, xs, M, K, dev)
+    args = _lib.BlockNormArgs(h.data_ptr(), _ptr(branch), _ptr(post_weight), _ptr(post_bias), _ptr(gate),
+                              weight.data_ptr(), _ptr(bias), _ptr(h_out), _ptr(rows), _ptr(xq), _ptr(xs), M, K,
+                              residual_scale, eps, _KINDS[kind], ht, bt, _ROWS[out], channels, int(tanh_gate))
+    with torch.cuda.device(dev):
+        call("s3d8_block_norm", ctypes.addressof(args), _stream(h))
+    u = (xq, xs) if rows is None else (rows,)
+    if branch is not None:
+        return (h_out, *u)
+    return u if rows is None else rows
+
+
+def glu_act(gate, up, out: str = "codes", rows=None, xq=None, xs=None):
+    """SiLU(gate) * up, and its activation quantisation, in one launch (see
+    s3d8_glu_act).  ``gate``, ``up``: fp32 or bf16 [M][K], rows contiguous (any row
+    stride that is a multiple of 4, e.g. the halves of one [M][2K] matrix).
+
+    Returns (xq, xs) for ``out="codes"``, the rows for "f32" / "bf16"."""
+    torch = _torch()
+    t = _row_type(gate, "gate")
+    for name, v in (("gate", gate), ("up", up)):
+        if not isinstance(v, torch.Tensor) or v.device.type != "cuda":
+            raise TypeError(f"{name} must be a CUDA/HIP torch tensor")
+        if v.dim() != 2 or v.stride(1) != 1:
+            raise ValueError(f"{name} must be [M][K] with contiguous rows")
+    if up.dtype != gate.dtype or up.shape != gate.shape or up.device != gate.device:
+        raise ValueError("gate and up must have one type, shape and device")
+    M, K = gate.shape
+    dev = gate.device
+    rows, xq, xs = _rows_out(out, rows, xq, xs, M, K, dev)
+    with torch.cuda.device(dev):
+        call("s3d8_glu_act", gate.data_ptr(), gate.stride(0) if M > 1 else K, up.data_ptr(),
+             up.stride(0) if M > 1 else K, M, K, t, _ROWS[out], _ptr(rows), _ptr(xq), _ptr(xs), _stream(gate))
+    return (xq, xs) if rows is None else rows

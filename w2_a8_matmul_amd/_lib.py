@@ -54,6 +54,13 @@ SIGNATURES = {
     "s3d8_linear_unfused_noalloc": (_I32, [_P, _P, _I64, _I64, _I64, _P, _I64, _P, _P, _P, _P, _P]),
     "s3d8_linear_splitk": (_I32, [_P, _P, _I64, _I64, _I64, _P, _I64, _P, _I32, _P, _P, _I32, _P, _I32, _P, _I64,
                                   _P]),
+    "s3d8_w4_encode": (_I32, [_P, _I64, _I64, _I64, _I32, _P, _P, _P]),
+    "s3d8_w4_tiled_bytes": (_I64, [_I64, _I64, _I64, _I32]),
+    "s3d8_w4_tile": (_I32, [_P, _P, _P, _I64, _I64, _I64, _P, _P]),
+    "s3d8_w4_linear": (_I32, [_P, _P, _I64, _I64, _I64, _P, _I64, _I64, _I32, _P, _I32, _P]),
+    "s3d8_w4_forward": (_I32, [_P, _I64, _I64, _I64, _P, _I64, _I64, _I32, _P, _I32, _P, _P, _P]),
+    "s3d8_block_norm": (_I32, [_P, _P]),
+    "s3d8_glu_act": (_I32, [_P, _I64, _P, _I64, _I64, _I64, _I32, _I32, _P, _P, _P, _P]),
     "s3d8_splitk_auto": (_I32, [_I64, _I64, _I64, _I32]),
     "s3d8_splitk_workspace_bytes": (_I64, [_I64, _I64, _I64, _I32]),
 }
@@ -63,6 +70,15 @@ class ForwardItem(ctypes.Structure):
     """s3d8_forward_item of include/s3d8.h (all members 8 bytes wide)."""
     _fields_ = [("x", _P), ("M", _I64), ("K", _I64), ("N", _I64), ("tiled", _P), ("tiled_bytes", _I64),
                 ("centroids", _P), ("scales_bf16", _P), ("y", _P), ("xq", _P), ("xs", _P), ("acc_out", _P)]
+
+
+class BlockNormArgs(ctypes.Structure):
+    """s3d8_block_norm_args of include/s3d8.h."""
+    _fields_ = [(f, _P) for f in ("h", "branch", "post_weight", "post_bias", "gate", "weight", "bias", "h_out", "rows",
+                                  "xq", "xs")]
+    _fields_ += [("M", _I64), ("K", _I64), ("residual_scale", ctypes.c_float), ("eps", ctypes.c_float)]
+    _fields_ += [(f, _I32) for f in ("kind", "h_type", "branch_type", "out_type", "gate_channels", "gate_tanh")]
+
 
 _lib = None
 

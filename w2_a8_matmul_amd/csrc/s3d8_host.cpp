@@ -58,7 +58,11 @@ void parallel_chunks(int64_t nchunks, int nthreads, const std::function<void(int
     };
     std::vector<std::thread> pool;
     pool.reserve(nt - 1);
-    for (int i = 0; i < nt - 1; ++i) pool.emplace_back(worker);
+    try {
+        for (int i = 0; i < nt - 1; ++i) pool.emplace_back(worker);
+    } catch (...) {
+        // no more threads to be had: those that started, and this one, do the work
+    }
     worker();
     for (auto &t : pool) t.join();
 }
@@ -315,6 +319,24 @@ void encode_bytes(const float *W, int64_t N, int64_t K, const Vectors &V, const 
     });
 }
 
+// One group of n columns (n even) of a W4 row: its scale, zero point and the
+// n / 2 bytes of codes.  Everything in fp32: IEEE division, rounding half to
+// even.
+void encode_group(const float *w, int64_t n, bool affine, uint16_t *scale, uint8_t *zero, uint8_t *packed) {
+    float lo = 0.0f, hi = 0.0f;
+    for (int64_t j = 0; j < n; ++j) {
+        lo = std::min(lo, w[j]);
+        hi = std::max(hi, w[j]);
+    }
+    *scale = bf16_from_f32(affine ? (hi - lo) / 15.0f : std::max(hi, -lo) / 7.0f);
+    const float s = f32_from_bf16(*scale);
+    auto clamped = [](float v) { return std::min(15.0f, std::max(0.0f, v)); };
+    *zero = affine && s != 0.0f ? (uint8_t)clamped(std::nearbyint(-lo / s)) : 8;
+    const float z = (float)*zero;
+    auto code = [&](float v) { return s == 0.0f ? 8u : (uint32_t)clamped(std::nearbyint(v / s) + z); };
+    for (int64_t j = 0; j < n; j += 2) packed[j / 2] = (uint8_t)(code(w[j]) | (code(w[j + 1]) << 4));
+}
+
 }  // namespace
 
 namespace s3d8 {
@@ -327,7 +349,7 @@ void clear_error() { g_last_error.clear(); }
 
 extern "C" {
 
-int32_t s3d8_version(void) { return 20100; }
+int32_t s3d8_version(void) { return 20200; }
 
 int64_t s3d8_num_triples(int64_t N) { return N > 0 ? (N + 2) / 3 : -1; }
 
@@ -424,6 +446,32 @@ int32_t s3d8_pack(const float *W, int64_t N, int64_t K, uint64_t seed, int32_t m
             rc_cent[e] = r;
         }
         encode_bytes(W, N, K, V, rc_cent, nt, packed);
+    } catch (const std::bad_alloc &) {
+        return s3d8::fail(S3D8_ERR_NOMEM, "host allocation failed");
+    } catch (...) {
+        return s3d8::fail(S3D8_ERR_INVALID_ARG, "unexpected host exception");
+    }
+    s3d8::clear_error();
+    return S3D8_OK;
+}
+
+int32_t s3d8_w4_encode(const float *W, int64_t N, int64_t K, int64_t group, int32_t num_threads, uint8_t *packed,
+                       uint16_t *scales_bf16, uint8_t *zeros) {
+    int rc = validate_host(W, N, K, packed, scales_bf16, packed);
+    if (rc) return rc;
+    if (group <= 0) return s3d8::fail(S3D8_ERR_INVALID_ARG, "group must be positive");
+    if (group % 32 != 0) return s3d8::fail(S3D8_ERR_SHAPE, "group must be a multiple of 32");
+    try {
+        const int64_t G = (K - 1) / group + 1;
+        parallel_chunks(N, resolve_threads(num_threads), [&](int64_t n) {
+            for (int64_t g = 0; g < G; ++g) {
+                const int64_t k0 = g * group, len = std::min(group, K - k0);
+                uint8_t z;
+                encode_group(W + n * K + k0, len, zeros != nullptr, &scales_bf16[n * G + g], &z,
+                             packed + (n * K + k0) / 2);
+                if (zeros) zeros[n * G + g] = z;
+            }
+        });
     } catch (const std::bad_alloc &) {
         return s3d8::fail(S3D8_ERR_NOMEM, "host allocation failed");
     } catch (...) {

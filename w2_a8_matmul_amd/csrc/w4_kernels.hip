@@ -1,0 +1,451 @@
+// The linear layer with 4-bit weights and group scales ("W4") for gfx950:
+// tiled weight layout, the product kernel for few token rows, entry points.
+//
+// Mathematics: y[m][n] = xs[m] * sum_g s[n][g] * sum_{k in g} xq[m][k] * (q[n][k] - z[n][g]).
+// The inner sums are exact INT32 products on the INT8 matrix instructions;
+// only the outer sum over the groups is fp32.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "s3d8.h"
+#include "s3d8_device.h"
+#include "s3d8_internal.h"
+
+namespace {
+
+// --------------------------------------------------------------- tiled layout
+
+// Fragment (tile t of 16 channels, block b of 128 columns) is 1 KiB at
+// (t * KB + b) * 1024, KB = ceil(K/128).  Lane L = n + 16 g of a wave owns 16
+// bytes of it, those of channel 16 t + n; byte i holds the code of column
+// 128 b + c(g, i) in its low nibble and of column 128 b + 64 + c(g, i) in its
+// high one.  The low nibbles of a fragment are thus one B operand of the INT8
+// products over columns 0..63 of the block, and the high ones one over
+// 64..127, each after one mask.  c(g, i) is 16 g + i (v_mfma_i32_16x16x64_i8
+// on activations read 16 bytes at a time), or, with 4 scales a block,
+// 32 (i / 8) + 8 g + i % 8: each half of 8 bytes is then an operand of
+// v_mfma_i32_16x16x32_i8, whose sum stays inside one 32-column group.
+// Without zero points the nibbles are q - 8 in two's complement: masked into
+// the high half of a byte they are 16 (q - 8), an INT8 operand in one or two
+// instructions for four weights, and the factor 16 is taken out of the fp32
+// sum (exactly).  With zero points the nibbles are q.
+//
+// The scales follow the fragments: P = 1, 2 or 4 per channel and block (the
+// group size a multiple of 128, of 64 or of 32; larger groups repeat theirs),
+// [t][b][n][P] bf16, then the zero points in the same order, a byte each.
+constexpr int kBlk = 128;
+
+int per_block(int64_t K, int64_t group) {
+    if (group % 128 == 0 || group >= K) return 1;
+    return group % 64 == 0 ? 2 : 4;
+}
+
+int64_t w4_bytes(int64_t N, int64_t K, int64_t group, bool zeros) {
+    const int64_t frags = ((N + 15) / 16) * ((K + kBlk - 1) / kBlk);
+    return frags * (1024 + per_block(K, group) * (zeros ? 48 : 32));
+}
+
+__host__ __device__ constexpr int frag_column(int P, int g, int i) {
+    return P == 4 ? 32 * (i >> 3) + 8 * g + (i & 7) : 16 * g + i;
+}
+
+constexpr int kTileThreads = 256;
+
+// One thread per 16-byte piece, then one per (channel, block) of the scales.
+__global__ __launch_bounds__(kTileThreads) void w4_tile_kernel(const uint8_t *__restrict__ packed,
+                                                               const uint16_t *__restrict__ scales,
+                                                               const uint8_t *__restrict__ zeros, int N, int K,
+                                                               int64_t group, int G, int P, int64_t frags,
+                                                               uint8_t *__restrict__ tiled) {
+    const int KB = (K + kBlk - 1) / kBlk;
+    uint16_t *sc = reinterpret_cast<uint16_t *>(tiled + frags * 1024);
+    uint8_t *zp = tiled + frags * (1024 + 32 * P);
+    const int64_t pieces = frags * 64, total = pieces + frags * 16;
+    for (int64_t c = (int64_t)blockIdx.x * kTileThreads + threadIdx.x; c < total;
+         c += (int64_t)gridDim.x * kTileThreads) {
+        const bool piece = c < pieces;
+        const int64_t f = piece ? c >> 6 : (c - pieces) >> 4;
+        const int l = piece ? (int)(c & 63) : (int)((c - pieces) & 15);
+        const int64_t tile = f / KB;
+        const int64_t n = tile * 16 + (l & 15);
+        const int k0 = (int)(f - tile * KB) * kBlk;
+        if (piece) {
+            auto code = [&](int k) -> uint32_t {
+                if (n >= N || k >= K) return 0u;
+                const uint32_t q = (packed[n * (K / 2) + k / 2] >> (4 * (k & 1))) & 15u;
+                return zeros ? q : q ^ 8u;
+            };
+            uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int k = k0 + frag_column(P, l >> 4, i);
+                w[i >> 2] |= (code(k) | (code(k + 64) << 4)) << (8 * (i & 3));
+            }
+            *reinterpret_cast<uint4 *>(tiled + c * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+            for (int p = 0; p < P; ++p) {
+                const int k = k0 + p * (kBlk / P);
+                const bool ok = n < N && k < K;
+                const int64_t at = ok ? n * G + k / group : 0;
+                sc[(f * 16 + l) * P + p] = ok ? scales[at] : (uint16_t)0;
+                if (zeros) zp[(f * 16 + l) * P + p] = ok ? zeros[at] : (uint8_t)0;
+            }
+        }
+    }
+}
+
+// --------------------------------------------------------------- decode
+
+// INT8 B operand dwords of the low (h = 0) or high (h = 1) nibbles of packed
+// dword w.  Without zero points: 16 (q - 8) per byte.  With: q - z, where zrep
+// holds z in every byte (the set top bit keeps each byte's difference from
+// borrowing out of it; clearing it by exclusive or leaves q - z).
+template <bool kZeros>
+__device__ __forceinline__ int32_t nibbles(uint32_t w, int h, uint32_t zrep) {
+    if constexpr (kZeros) {
+        const uint32_t q = (h ? w >> 4 : w) & 0x0F0F0F0Fu;
+        return (int32_t)(((q | 0x80808080u) - zrep) ^ 0x80808080u);
+    } else {
+        return (int32_t)((h ? w : w << 4) & 0xF0F0F0F0u);
+    }
+}
+
+// --------------------------------------------------------------- product, few rows
+
+// Token rows 16 R at a time against NT tiles of 16 channels, the columns split
+// over the waves.  A workgroup's W waves form W / KS teams; a team takes a
+// group of NT tiles at a time, its KS waves every KS-th block of 128 columns.
+// Both operands go straight from memory to registers in operand order (lane
+// L = n + 16 g: B column n; A row n, 16-byte piece g), kDepth blocks ahead;
+// nothing passes through LDS but the waves' partial sums, which a team adds in
+// wave order.
+//
+// A row r of a row tile is token 4 (r % 4) + r / 4, so that result register i
+// of lane group g belongs to token 4 i + g: with up to 4 tokens only register
+// 0 of every result is converted and scaled, with up to 8 two (Q registers).
+template <int R, int NT, int Q, int P, bool kZeros, int W>
+__global__ __launch_bounds__(W * 64) void w4_rows_kernel(const int8_t *__restrict__ xq, const float *__restrict__ xs,
+                                                         const uint8_t *__restrict__ tiled, int M, int K, int N,
+                                                         int KS, int rounds, int wgs, void *__restrict__ y, int obf) {
+    constexpr int kDepth = 2;
+    __shared__ float red[W * NT * R * Q * 64];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int n = lane & 15, g = lane >> 4;
+    const int KB = (K + kBlk - 1) / kBlk, tiles = (N + 15) >> 4;
+    const int teams = W / KS, team = wave / KS, part = wave - team * KS;
+    const int bm = (int)blockIdx.x / wgs, bc = (int)blockIdx.x - bm * wgs;  // row tile, place among its wgs workgroups
+    const int m0 = bm * 16 * R;
+    const uint32_t frags = (uint32_t)tiles * (uint32_t)KB;
+    const auto rx = make_rsrc(xq, (uint32_t)M * (uint32_t)K);
+    const auto rw = make_rsrc(tiled, frags * 1024u);
+    const auto rs = make_rsrc(tiled + (int64_t)frags * 1024, frags * (32u * P));
+    const auto rz = make_rsrc(tiled + (int64_t)frags * (1024 + 32 * P), kZeros ? frags * (16u * P) : 0u);
+
+    struct Stage {
+        uint4 w[NT];
+        uint32_t s[NT][P == 4 ? 2 : 1], z[NT];
+        uint4 a[R][2];
+    };
+    const int steps_tile = (KB - part + KS - 1) / KS;  // this wave's blocks of a tile group
+    int group = bc * teams + team;        // of the next step to load
+    const int stride = wgs * teams;
+    uint32_t arow[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int tok = m0 + 16 * r + 4 * (n & 3) + (n >> 2);
+        arow[r] = tok < M ? (uint32_t)tok * (uint32_t)K : kOOB;
+    }
+    auto load = [&](Stage &st, int grp, int step) {
+        const int kb = part + KS * step;
+        const bool live = step < steps_tile;
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if constexpr (P == 4) {
+                    // the columns of byte halves 0..7 and 8..15 of the fragment's lane
+                    const int k = kb * kBlk + 64 * h + 8 * g;
+                    const uint32_t o0 = live && arow[r] != kOOB && k < K ? arow[r] + (uint32_t)k : kOOB;
+                    const uint32_t o1 = live && arow[r] != kOOB && k + 32 < K ? arow[r] + (uint32_t)k + 32u : kOOB;
+                    const auto lo = __builtin_amdgcn_raw_buffer_load_b64(rx, o0, 0, 0);
+                    const auto hi = __builtin_amdgcn_raw_buffer_load_b64(rx, o1, 0, 0);
+                    st.a[r][h] = make_uint4(lo[0], lo[1], hi[0], hi[1]);
+                } else {
+                    const int k = kb * kBlk + 64 * h + 16 * g;
+                    st.a[r][h] = bload16(rx, live && arow[r] != kOOB && k < K ? arow[r] + (uint32_t)k : kOOB);
+                }
+            }
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const int tile = grp * NT + t;
+            const uint32_t f = (uint32_t)tile * (uint32_t)KB + (uint32_t)kb;
+            const bool ok = live && tile < tiles;
+            st.w[t] = bload16(rw, ok ? f * 1024u + 16u * (uint32_t)lane : kOOB);
+            const uint32_t so = ok ? (f * 16u + (uint32_t)n) * (2u * P) : kOOB;
+            if constexpr (P == 1) {
+                st.s[t][0] = __builtin_amdgcn_raw_buffer_load_b16(rs, so, 0, 0);
+            } else if constexpr (P == 2) {
+                st.s[t][0] = __builtin_amdgcn_raw_buffer_load_b32(rs, so, 0, 0);
+            } else {
+                const auto v = __builtin_amdgcn_raw_buffer_load_b64(rs, so, 0, 0);
+                st.s[t][0] = v[0];
+                st.s[t][1] = v[1];
+            }
+            if constexpr (kZeros) {
+                const uint32_t zo = ok ? (f * 16u + (uint32_t)n) * (uint32_t)P : kOOB;
+                if constexpr (P == 1) st.z[t] = __builtin_amdgcn_raw_buffer_load_b8(rz, zo, 0, 0);
+                if constexpr (P == 2) st.z[t] = __builtin_amdgcn_raw_buffer_load_b16(rz, zo, 0, 0);
+                if constexpr (P == 4) st.z[t] = __builtin_amdgcn_raw_buffer_load_b32(rz, zo, 0, 0);
+            }
+        }
+    };
+    float sum[NT][R][Q];
+    auto consume = [&](const Stage &st) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const uint32_t wv[4] = {st.w[t].x, st.w[t].y, st.w[t].z, st.w[t].w};
+            v4i acc[R];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                v4i b;
+#pragma unroll
+                for (int d = 0; d < 4; ++d) {
+                    const int p = P == 1 ? 0 : P == 2 ? h : 2 * h + (d >> 1);
+                    const uint32_t zrep = kZeros ? ((st.z[t] >> (8 * p)) & 0xFFu) * 0x01010101u : 0u;
+                    b[d] = nibbles<kZeros>(wv[d], h, zrep);
+                }
+                auto add = [&](const v4i &c, int r, uint32_t sbits) {
+                    const float s = __uint_as_float(sbits << 16);
+#pragma unroll
+                    for (int i = 0; i < Q; ++i) sum[t][r][i] = __builtin_fmaf(s, (float)c[i], sum[t][r][i]);
+                };
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const uint4 av = st.a[r][h];
+                    const v4i a = {(int)av.x, (int)av.y, (int)av.z, (int)av.w}, zero = {0, 0, 0, 0};
+                    if constexpr (P == 4) {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const long al = (long)((uint64_t)(uint32_t)a[2 * e] | (uint64_t)(uint32_t)a[2 * e + 1] << 32);
+                            const long bl = (long)((uint64_t)(uint32_t)b[2 * e] | (uint64_t)(uint32_t)b[2 * e + 1] << 32);
+                            const v4i c = __builtin_amdgcn_mfma_i32_16x16x32_i8(al, bl, zero, 0, 0, 0);
+                            add(c, r, e ? st.s[t][h] >> 16 : st.s[t][h]);
+                        }
+                    } else if constexpr (P == 2) {
+                        const v4i c = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, zero, 0, 0, 0);
+                        add(c, r, h ? st.s[t][0] >> 16 : st.s[t][0]);
+                    } else {
+                        acc[r] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, h ? acc[r] : zero, 0, 0, 0);
+                        if (h) add(acc[r], r, st.s[t][0]);
+                    }
+                }
+            }
+        }
+    };
+
+    Stage ring[kDepth];
+    // (group, step) of the next load; every wave of a team loads and consumes
+    // in the same order, blocks past its share are predicated off
+    int ld_group = group, ld_step = 0;
+    const int steps_max = (KB + KS - 1) / KS;  // of any wave, so that barriers line up
+    auto load_next = [&](Stage &st) {
+        load(st, ld_group, ld_step);
+        if (++ld_step == steps_max) {
+            ld_step = 0;
+            ld_group += stride;
+        }
+    };
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) load_next(ring[d]);
+
+    const float post = kZeros ? 1.0f : 0.0625f;
+    auto clear = [&]() {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int i = 0; i < Q; ++i) sum[t][r][i] = 0.0f;
+    };
+    clear();
+    int step = 0;
+    const int total = rounds * steps_max;
+#pragma unroll 1
+    for (int st0 = 0; st0 < total; st0 += kDepth) {
+#pragma unroll
+        for (int u = 0; u < kDepth; ++u) {
+            if (st0 + u >= total) break;  // uniform
+            consume(ring[u]);
+            load_next(ring[u]);
+            if (++step < steps_max) continue;
+            // the team's partial sums of this tile group, added in wave order
+            step = 0;
+            float *mine = red + wave * (NT * R * Q * 64);
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int i = 0; i < Q; ++i) mine[((t * R + r) * Q + i) * 64 + lane] = sum[t][r][i];
+            clear();
+            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            const float *from = red + team * KS * (NT * R * Q * 64);
+            for (int o = part * 64 + lane; o < NT * R * Q * 64; o += KS * 64) {
+                // o = ((r Q + i) 4 + g') (16 NT) + channel
+                const int ch = o % (16 * NT), tk = o / (16 * NT);
+                const int gg = tk & 3, ri = tk >> 2, i = ri % Q, r = ri / Q;
+                const int m = m0 + 16 * r + 4 * i + gg, c = group * (16 * NT) + ch;
+                const float *at = from + (((ch >> 4) * R + r) * Q + i) * 64 + (ch & 15) + 16 * gg;
+                float v = 0.0f;
+                for (int w = 0; w < KS; ++w) v += at[w * (NT * R * Q * 64)];
+                if (m < M && c < N) {
+                    v = xs[m] * (v * post);
+                    if (obf)
+                        static_cast<uint16_t *>(y)[(int64_t)m * N + c] = f32_to_bf16_rne(v);
+                    else
+                        static_cast<float *>(y)[(int64_t)m * N + c] = v;
+                }
+            }
+            group += stride;
+            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        }
+    }
+}
+
+// --------------------------------------------------------------- launches
+
+struct W4Args {
+    const int8_t *xq;
+    const float *xs;
+    const uint8_t *tiled;
+    int M, K, N;
+    void *y;
+    int obf;
+};
+
+template <int R, int NT, int Q, int W>
+void launch_rows(const W4Args &a, int P, bool zeros, int cus, hipStream_t stream) {
+    const int KB = (a.K + kBlk - 1) / kBlk, groups = ((a.N + 15) / 16 + NT - 1) / NT;
+    // as many waves on one group's columns as it has blocks, until the groups
+    // fill the waves of every CU
+    int KS = W;
+    while (KS > 1 && (KS / 2 >= KB || (int64_t)groups * KS > (int64_t)cus * W * 2)) KS /= 2;
+    const int teams = W / KS;
+    const int wgs = std::min((groups + teams - 1) / teams, cus);
+    const int rounds = (groups + wgs * teams - 1) / (wgs * teams);
+    typedef void (*Fn)(const int8_t *, const float *, const uint8_t *, int, int, int, int, int, int, void *, int);
+    static const Fn fns[3][2] = {
+        {w4_rows_kernel<R, NT, Q, 1, false, W>, w4_rows_kernel<R, NT, Q, 1, true, W>},
+        {w4_rows_kernel<R, NT, Q, 2, false, W>, w4_rows_kernel<R, NT, Q, 2, true, W>},
+        {w4_rows_kernel<R, NT, Q, 4, false, W>, w4_rows_kernel<R, NT, Q, 4, true, W>},
+    };
+    hipLaunchKernelGGL(fns[P == 4 ? 2 : P - 1][zeros], dim3(wgs * ((a.M + 16 * R - 1) / (16 * R))), dim3(W * 64), 0,
+                       stream, a.xq, a.xs, a.tiled, a.M, a.K, a.N, KS, rounds, wgs, a.y, a.obf);
+}
+
+// Token rows of one call: keeps every launch under 2^32 threads.
+constexpr int64_t kMaxRows = 1 << 19;
+
+int check_w4(int64_t M, int64_t K, int64_t N, int64_t group, bool zeros) {
+    if (M <= 0 || K <= 0 || N <= 0 || group <= 0)
+        return s3d8::fail(S3D8_ERR_INVALID_ARG, "sizes and group must be positive");
+    if (K % 16 != 0) return s3d8::fail(S3D8_ERR_SHAPE, "K must be a multiple of 16");
+    if (group % 32 != 0) return s3d8::fail(S3D8_ERR_SHAPE, "group must be a multiple of 32");
+    const int64_t lim = (int64_t(1) << 31) - 1;
+    if (M > kMaxRows || K > lim - kBlk || N > lim - 64 || M > lim / K || M > lim / N || (N + 15) / 16 > lim / (K + kBlk) ||
+        w4_bytes(N, K, group, zeros) > lim)
+        return s3d8::fail(S3D8_ERR_SHAPE, "tensor too large (more than 2^31 elements or tiled bytes, or 524288 rows)");
+    return S3D8_OK;
+}
+
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+int check_linear(const int8_t *xq, const float *xs, int64_t M, int64_t K, int64_t N, const uint8_t *tiled,
+                 int64_t tiled_bytes, int64_t group, int32_t has_zeros, const void *y, int32_t out_type) {
+    if (!xq || !xs || !tiled || !y) return s3d8::fail(S3D8_ERR_INVALID_ARG, "null pointer argument");
+    if (out_type != S3D8_OUT_F32 && out_type != S3D8_OUT_BF16)
+        return s3d8::fail(S3D8_ERR_INVALID_ARG, "unknown output type");
+    if (has_zeros != 0 && has_zeros != 1) return s3d8::fail(S3D8_ERR_INVALID_ARG, "has_zeros must be 0 or 1");
+    int rc = check_w4(M, K, N, group, has_zeros != 0);
+    if (rc) return rc;
+    if (tiled_bytes != w4_bytes(N, K, group, has_zeros != 0))
+        return s3d8::fail(S3D8_ERR_INVALID_ARG,
+                          "tiled_bytes is not s3d8_w4_tiled_bytes(N, K, group, has_zeros): pass the matrix as "
+                          "s3d8_w4_tile laid it out for these arguments");
+    if (!aligned16(xq) || !aligned16(tiled))
+        return s3d8::fail(S3D8_ERR_ALIGN, "xq and the tiled weights must be 16-byte aligned");
+    if (reinterpret_cast<uintptr_t>(xs) & 3u || reinterpret_cast<uintptr_t>(y) & (out_type == S3D8_OUT_F32 ? 3u : 1u))
+        return s3d8::fail(S3D8_ERR_ALIGN, "xs and y must be aligned to their elements");
+    return S3D8_OK;
+}
+
+int launch_linear(const int8_t *xq, const float *xs, int64_t M, int64_t K, int64_t N, const uint8_t *tiled,
+                  int64_t group, bool zeros, void *y, int32_t out_type, int cus, hipStream_t stream) {
+    const W4Args a{xq, xs, tiled, (int)M, (int)K, (int)N, y, out_type == S3D8_OUT_BF16};
+    const int P = per_block(K, group);
+    if (M <= 4)
+        launch_rows<1, 1, 1, 16>(a, P, zeros, cus, stream);
+    else if (M <= 8)
+        launch_rows<1, 2, 2, 16>(a, P, zeros, cus, stream);
+    else if (M <= 16)
+        launch_rows<1, 2, 4, 16>(a, P, zeros, cus, stream);
+    else
+        launch_rows<2, 2, 4, 8>(a, P, zeros, cus, stream);
+    return s3d8::launch_status();
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t s3d8_w4_tiled_bytes(int64_t N, int64_t K, int64_t group, int32_t has_zeros) {
+    if (N <= 0 || K <= 0 || group <= 0 || group % 32 != 0) return -1;
+    const int64_t lim = (int64_t(1) << 31) - 1;
+    if (N > lim || K > lim || (N + 15) / 16 > (int64_t(1) << 50) / (K + kBlk)) return -1;
+    return w4_bytes(N, K, group, has_zeros != 0);
+}
+
+int32_t s3d8_w4_tile(const uint8_t *packed, const uint16_t *scales_bf16, const uint8_t *zeros, int64_t N, int64_t K,
+                     int64_t group, uint8_t *tiled, void *stream) {
+    if (!packed || !scales_bf16 || !tiled) return s3d8::fail(S3D8_ERR_INVALID_ARG, "null pointer argument");
+    int rc = check_w4(1, K, N, group, zeros != nullptr);
+    if (rc) return rc;
+    if (!aligned16(tiled)) return s3d8::fail(S3D8_ERR_ALIGN, "tiled must be 16-byte aligned");
+    if (reinterpret_cast<uintptr_t>(scales_bf16) & 1u)
+        return s3d8::fail(S3D8_ERR_ALIGN, "scales_bf16 must be 2-byte aligned");
+    int cus = 0;
+    rc = s3d8::check_device(&cus);
+    if (rc) return rc;
+    const int64_t frags = ((N + 15) / 16) * ((K + kBlk - 1) / kBlk);
+    const int64_t blocks = std::min<int64_t>((frags * 80 + kTileThreads - 1) / kTileThreads, (int64_t)cus * 8);
+    hipLaunchKernelGGL(w4_tile_kernel, dim3((unsigned)blocks), dim3(kTileThreads), 0, (hipStream_t)stream, packed,
+                       scales_bf16, zeros, (int)N, (int)K, group, (int)((K - 1) / group + 1), per_block(K, group),
+                       frags, tiled);
+    return s3d8::launch_status();
+}
+
+int32_t s3d8_w4_linear(const int8_t *xq, const float *xs, int64_t M, int64_t K, int64_t N, const uint8_t *tiled,
+                       int64_t tiled_bytes, int64_t group, int32_t has_zeros, void *y, int32_t out_type,
+                       void *stream) {
+    int rc = check_linear(xq, xs, M, K, N, tiled, tiled_bytes, group, has_zeros, y, out_type);
+    if (rc) return rc;
+    int cus = 0;
+    rc = s3d8::check_device(&cus);
+    if (rc) return rc;
+    return launch_linear(xq, xs, M, K, N, tiled, group, has_zeros != 0, y, out_type, cus, (hipStream_t)stream);
+}
+
+int32_t s3d8_w4_forward(const float *x, int64_t M, int64_t K, int64_t N, const uint8_t *tiled, int64_t tiled_bytes,
+                        int64_t group, int32_t has_zeros, void *y, int32_t out_type, int8_t *xq, float *xs,
+                        void *stream) {
+    int rc = check_linear(xq, xs, M, K, N, tiled, tiled_bytes, group, has_zeros, y, out_type);
+    if (rc) return rc;
+    rc = s3d8_quant_act(x, M, K, xq, xs, stream);
+    if (rc) return rc;
+    return s3d8_w4_linear(xq, xs, M, K, N, tiled, tiled_bytes, group, has_zeros, y, out_type, stream);
+}
+
+}  // extern "C"

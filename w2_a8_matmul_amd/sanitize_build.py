@@ -50,17 +50,19 @@ def build_sanitized(verbose: bool = False):
     """Build both sanitized libraries (skipped when newer than their sources);
     returns (library, oracle library)."""
     os.makedirs(SAN_DIR, exist_ok=True)
-    hip = os.path.join(_b.CSRC, "s3d8_kernels.hip")
+    hips = sorted(glob.glob(os.path.join(_b.CSRC, "*.hip")))
     cpp = os.path.join(_b.CSRC, "s3d8_host.cpp")
     hdrs = glob.glob(os.path.join(_b.CSRC, "*.h")) + glob.glob(os.path.join(_b.INCLUDE, "*.h"))
-    if _stale(SAN_LIB, [hip, cpp, *hdrs]):
-        k_o, h_o = os.path.join(SAN_DIR, "k.o"), os.path.join(SAN_DIR, "h.o")
+    if _stale(SAN_LIB, [*hips, cpp, *hdrs]):
+        h_o = os.path.join(SAN_DIR, "h.o")
+        k_os = [os.path.join(SAN_DIR, os.path.basename(h)[:-4] + ".o") for h in hips]
         dev_flags = [f for f in _b.HIP_FLAGS if f != "-O3"]
-        _b._run([_b.HIPCC, *dev_flags, "-O1", "-g", *_HOST_SAN, "-c", hip, "-o", k_o], verbose)
+        for hip, k_o in zip(hips, k_os):
+            _b._run([_b.HIPCC, *dev_flags, "-O1", "-g", *_HOST_SAN, "-c", hip, "-o", k_o], verbose)
         _b._run([CLANGXX, "-O1", "-g", "-fPIC", "-std=c++17", "-ffp-contract=off", "-pthread", *_SAN,
                  "-I", _b.INCLUDE, "-I", _b.CSRC, "-c", cpp, "-o", h_o], verbose)
         tmp = SAN_LIB + ".tmp%d" % os.getpid()
-        _b._run([CLANGXX, "-shared", "-fPIC", *_SAN, "-shared-libasan", "-o", tmp, k_o, h_o,
+        _b._run([CLANGXX, "-shared", "-fPIC", *_SAN, "-shared-libasan", "-o", tmp, *k_os, h_o,
                  "-L/opt/rocm/lib", "-lamdhip64", "-pthread", "-Wl,-rpath,/opt/rocm/lib"], verbose)
         os.replace(tmp, SAN_LIB)
     if _stale(SAN_ORACLE, [ORACLE_SRC]):
