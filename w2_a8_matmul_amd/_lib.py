@@ -7,6 +7,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 # S3D8_LIB selects another build of the library (e.g. the sanitizer build of
 # the host code, build.py --sanitize); by default the in-tree libs3d8.so
@@ -79,6 +80,10 @@ class BlockNormArgs(ctypes.Structure):
     _fields_ += [("M", _I64), ("K", _I64), ("residual_scale", ctypes.c_float), ("eps", ctypes.c_float)]
     _fields_ += [(f, _I32) for f in ("kind", "h_type", "branch_type", "out_type", "gate_channels", "gate_tanh")]
 
+
+# the same struct packed into bytes (0.6 us against 2.5 us for filling a Structure)
+BLOCK_NORM_ARGS = struct.Struct("11Q2q2f6i").pack
+assert struct.calcsize("11Q2q2f6i") == ctypes.sizeof(BlockNormArgs)
 
 _lib = None
 
