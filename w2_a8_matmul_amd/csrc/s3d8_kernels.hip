@@ -1435,55 +1435,11 @@ __global__ __launch_bounds__(1024) void gemv_codes_kernel(const int8_t *__restri
 constexpr int kGemmBF = 8;        // weight fragments (16 triples) per workgroup
 constexpr int kGemmSlots = 5;     // LDS ring slots
 constexpr int kGemmAhead = kGemmSlots - 1;  // blocks in flight ahead of use
-constexpr int kXcds = 8;
 // a workgroup's rows of fp32 output stay under 2^31 bytes (32-bit store offsets)
 constexpr int kGemmMaxRT = 5;     // most 32-row tiles per wave of any GEMM variant
 constexpr int64_t kGemmMaxN = (int64_t(1) << 31) / (4 * 32 * kGemmMaxRT) - 1;
 
 typedef int32_t v16i __attribute__((ext_vector_type(16)));
-
-// Tile of workgroup blockIdx.x.  Workgroup w runs on XCD w % 8; each XCD
-// takes a contiguous range of tile indices, and tile indices run over
-// groups of kGroupM row blocks, row block fastest within a group and
-// column block next: the ~32 workgroups resident on one XCD then cover
-// about 8 row blocks x 4 column blocks, so their activation and weight
-// tiles are shared through that XCD's L2 instead of each workgroup
-// streaming its own weight stripe.
-//
-// With the input columns split into `splits` ranges, the range index ks is
-// the slowest: an XCD's workgroups then share a k range as well.
-constexpr int kGroupM = 8;
-__device__ __forceinline__ bool gemm_tile(int nbm, int nbn, int splits, int &bm, int &bn, int &ks) {
-    const int nt = nbm * nbn;
-    const int nwg = nt * splits;
-    const int per_xcd = (nwg + kXcds - 1) / kXcds;
-    const int L0 = (int)(blockIdx.x % kXcds) * per_xcd + (int)(blockIdx.x / kXcds);
-    if (L0 >= nwg) return false;
-    ks = L0 / nt;
-    const int L = L0 - ks * nt;
-    const int group = L / (kGroupM * nbn), r = L - group * (kGroupM * nbn);
-    const int gm = min(kGroupM, nbm - group * kGroupM);
-    bm = group * kGroupM + r % gm;
-    bn = r / gm;
-    return true;
-}
-__device__ __forceinline__ bool gemm_tile(int nbm, int nbn, int &bm, int &bn) {
-    int ks;
-    return gemm_tile(nbm, nbn, 1, bm, bn, ks);
-}
-
-// s_waitcnt vmcnt(N) for the loads the compiler does not see (LDS-DMA), and
-// the same followed by lgkmcnt(0) and a workgroup barrier.
-template <int N>
-__device__ __forceinline__ void wait_vmcnt() {
-    static_assert(N >= 0 && N <= 63, "vmcnt is a 6-bit count");
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
-}
-template <int N>
-__device__ __forceinline__ void wait_vmcnt_barrier() {
-    static_assert(N >= 0 && N <= 63, "vmcnt is a 6-bit count");
-    asm volatile("s_waitcnt vmcnt(%0)\n\ts_waitcnt lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
-}
 
 __device__ __forceinline__ uint16_t bload2(__amdgpu_buffer_rsrc_t r, uint32_t off) {
     return __builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0);

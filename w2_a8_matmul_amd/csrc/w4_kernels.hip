@@ -315,6 +315,187 @@ __global__ __launch_bounds__(W * 64) void w4_rows_kernel(const int8_t *__restric
     }
 }
 
+// --------------------------------------------------------------- product, many rows
+
+// Workgroup tile of 16 TR WR token rows x 16 TC (8 / WR) channels on eight
+// waves, each with TR x TC results of 16 x 16.  The activations go through LDS
+// (an LDS-DMA ring of kGemmRing blocks of 128 columns, stored in A operand
+// order, so that every operand read is contiguous and free of bank
+// conflicts); a wave's weights are its own and go straight to registers, one
+// block ahead.
+template <int TR, int TC, int WR, int P, bool kZeros>
+__global__ __launch_bounds__(512) void w4_gemm_kernel(const int8_t *__restrict__ xq, const uint8_t *__restrict__ tiled,
+                                                      int M, int K, int N, int nbm, int nbn,
+                                                      const float *__restrict__ xs, void *__restrict__ y, int obf) {
+    constexpr int kGemmRing = 3;
+    constexpr int BM = 16 * TR * WR, WC = 8 / WR, BN = 16 * TC * WC;
+    constexpr int NA = BM / 64;                  // activation loads (1 KiB) per wave and block
+    constexpr int NB = TC * (kZeros ? 3 : 2);    // weight, scale and zero-point loads
+    static_assert(BM % 64 == 0, "eight waves share the activation loads evenly");
+    __shared__ __attribute__((aligned(16))) int8_t abuf[kGemmRing][BM * kBlk];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int n = lane & 15, g = lane >> 4;
+    const int KB = (K + kBlk - 1) / kBlk, tiles = (N + 15) >> 4;
+    int bm, bn;
+    if (!gemm_tile(nbm, nbn, bm, bn)) return;  // padding workgroup
+    const int row0 = bm * BM, wr = wave / WC, tile0 = bn * (BN / 16) + (wave - wr * WC) * TC;
+
+    const uint32_t frags = (uint32_t)tiles * (uint32_t)KB;
+    const v4i rx = rsrc_words(xq, (uint32_t)M * (uint32_t)K);
+    const auto rw = make_rsrc(tiled, frags * 1024u);
+    const auto rs = make_rsrc(tiled + (int64_t)frags * 1024, frags * (32u * P));
+    const auto rz = make_rsrc(tiled + (int64_t)frags * (1024 + 32 * P), kZeros ? frags * (16u * P) : 0u);
+
+    // activation load L = wave + 8 j: rows 16 (L / 2) .., columns 64 (L % 2) ..
+    // of a block, chunk g of row n at 16 lane of KiB L
+    uint32_t aoff[NA], atail[NA];
+#pragma unroll
+    for (int j = 0; j < NA; ++j) {
+        const int L = wave + 8 * j, row = row0 + 16 * (L >> 1) + n, col = 64 * (L & 1) + 16 * g;
+        aoff[j] = row < M ? (uint32_t)row * (uint32_t)K + (uint32_t)col : kOOB;
+        atail[j] = (KB - 1) * kBlk + col < K ? aoff[j] : kOOB;
+    }
+    auto issue = [&](int kb, int slot) {
+        const uint32_t base = S3D8_LDS_OFFSET(&abuf[0][0]) + (uint32_t)(BM * kBlk * slot) + 1024u * (uint32_t)wave;
+        const uint32_t so = kb < KB ? (uint32_t)(kb * kBlk) : 0u;
+#pragma unroll
+        for (int j = 0; j < NA; ++j)
+            load_to_lds16_so(base + 8192u * j, kb < KB - 1 ? aoff[j] : kb == KB - 1 ? atail[j] : kOOB, so, rx);
+    };
+    struct Raw {
+        uint4 w[TC];
+        uint32_t s[TC][P == 4 ? 2 : 1], z[TC];
+    };
+    auto load = [&](Raw &q, int kb) {
+#pragma unroll
+        for (int t = 0; t < TC; ++t) {
+            const bool ok = tile0 + t < tiles && kb < KB;
+            const uint32_t f = (uint32_t)(tile0 + t) * (uint32_t)KB + (uint32_t)kb;
+            q.w[t] = bload16(rw, ok ? f * 1024u + 16u * (uint32_t)lane : kOOB);
+            const uint32_t so = ok ? (f * 16u + (uint32_t)n) * (2u * P) : kOOB;
+            if constexpr (P == 1) q.s[t][0] = __builtin_amdgcn_raw_buffer_load_b16(rs, so, 0, 0);
+            if constexpr (P == 2) q.s[t][0] = __builtin_amdgcn_raw_buffer_load_b32(rs, so, 0, 0);
+            if constexpr (P == 4) {
+                const auto v = __builtin_amdgcn_raw_buffer_load_b64(rs, so, 0, 0);
+                q.s[t][0] = v[0];
+                q.s[t][1] = v[1];
+            }
+            if constexpr (kZeros) {
+                const uint32_t zo = ok ? (f * 16u + (uint32_t)n) * (uint32_t)P : kOOB;
+                if constexpr (P == 1) q.z[t] = __builtin_amdgcn_raw_buffer_load_b8(rz, zo, 0, 0);
+                if constexpr (P == 2) q.z[t] = __builtin_amdgcn_raw_buffer_load_b16(rz, zo, 0, 0);
+                if constexpr (P == 4) q.z[t] = __builtin_amdgcn_raw_buffer_load_b32(rz, zo, 0, 0);
+            }
+        }
+    };
+
+    float4 sum[TR][TC];
+#pragma unroll
+    for (int r = 0; r < TR; ++r)
+#pragma unroll
+        for (int t = 0; t < TC; ++t) sum[r][t] = make_float4(0, 0, 0, 0);
+    auto add = [&](float4 &o, const v4i &c, float s) {
+        o.x = __builtin_fmaf(s, (float)c[0], o.x);
+        o.y = __builtin_fmaf(s, (float)c[1], o.y);
+        o.z = __builtin_fmaf(s, (float)c[2], o.z);
+        o.w = __builtin_fmaf(s, (float)c[3], o.w);
+    };
+
+    Raw raw;
+    static_assert(kGemmRing == 3, "two blocks of activations in flight");
+    issue(0, 0);
+    issue(1, 1);
+    load(raw, 0);
+    int slot = 0;
+#pragma unroll 1
+    for (int kb = 0; kb < KB; ++kb) {
+        // this wave's loads of block kb have landed (younger: those of block
+        // kb + 1 and the weights of block kb), everyone's after the barrier,
+        // which also ends every read of block kb - 1's slot
+        wait_vmcnt_barrier<NA + NB>();
+        issue(kb + 2, slot == 0 ? 2 : slot - 1);
+        v4i b[2][TC];
+        float s[TC][P];
+#pragma unroll
+        for (int t = 0; t < TC; ++t) {
+            const uint32_t wv[4] = {raw.w[t].x, raw.w[t].y, raw.w[t].z, raw.w[t].w};
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int d = 0; d < 4; ++d) {
+                    const int p = P == 1 ? 0 : P == 2 ? h : 2 * h + (d >> 1);
+                    const uint32_t zrep = kZeros ? ((raw.z[t] >> (8 * p)) & 0xFFu) * 0x01010101u : 0u;
+                    b[h][t][d] = nibbles<kZeros>(wv[d], h, zrep);
+                }
+#pragma unroll
+            for (int p = 0; p < P; ++p)
+                s[t][p] = __uint_as_float(p & 1 ? raw.s[t][p >> 1] & 0xFFFF0000u : raw.s[t][p >> 1] << 16);
+        }
+        load(raw, kb + 1);
+        const int8_t *at = &abuf[slot][wr * TR * 2048];
+        const v4i zero = {0, 0, 0, 0};
+#pragma unroll
+        for (int r = 0; r < TR; ++r) {
+            if constexpr (P == 4) {
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    // columns 32 p + 8 g .. + 7 of the block: half g % 2 of chunk 2 (p % 2) + g / 2
+                    const long a = *reinterpret_cast<const long *>(at + 2048 * r + 1024 * (p >> 1) + 512 * (p & 1) +
+                                                                   256 * (g >> 1) + 16 * n + 8 * (g & 1));
+#pragma unroll
+                    for (int t = 0; t < TC; ++t) {
+                        const v4i &bv = b[p >> 1][t];
+                        const int e = 2 * (p & 1);
+                        const long bl = (long)((uint64_t)(uint32_t)bv[e] | (uint64_t)(uint32_t)bv[e + 1] << 32);
+                        add(sum[r][t], __builtin_amdgcn_mfma_i32_16x16x32_i8(a, bl, zero, 0, 0, 0), s[t][p]);
+                    }
+                }
+            } else {
+                const v4i a0 = *reinterpret_cast<const v4i *>(at + 2048 * r + 16 * lane);
+                const v4i a1 = *reinterpret_cast<const v4i *>(at + 2048 * r + 1024 + 16 * lane);
+#pragma unroll
+                for (int t = 0; t < TC; ++t) {
+                    v4i c = __builtin_amdgcn_mfma_i32_16x16x64_i8(a0, b[0][t], zero, 0, 0, 0);
+                    if constexpr (P == 2) add(sum[r][t], c, s[t][0]);
+                    c = __builtin_amdgcn_mfma_i32_16x16x64_i8(a1, b[1][t], P == 1 ? c : zero, 0, 0, 0);
+                    add(sum[r][t], c, s[t][P - 1]);
+                }
+            }
+        }
+        slot = slot == 2 ? 0 : slot + 1;
+    }
+    wait_vmcnt<0>();  // loads of blocks past the end
+
+    // result lane (n, g), element i: row 4 g + i of the row tile, channel n
+    const int wrow = row0 + 16 * TR * wr, nrows = min(M - wrow, 16 * TR);
+    if (nrows <= 0) return;
+    const uint32_t size = obf ? 2u : 4u, rowb = size * (uint32_t)N;
+    const auto ry = make_rsrc(static_cast<char *>(y) + (int64_t)wrow * N * size, rowb * (uint32_t)nrows);
+    const auto rxs = make_rsrc(xs + wrow, 4u * (uint32_t)nrows);
+    const float post = kZeros ? 1.0f : 0.0625f;
+#pragma unroll
+    for (int r = 0; r < TR; ++r) {
+        const uint4 sx = bload16(rxs, 64u * r + 16u * g);
+        const float sxv[4] = {__uint_as_float(sx.x), __uint_as_float(sx.y), __uint_as_float(sx.z), __uint_as_float(sx.w)};
+#pragma unroll
+        for (int t = 0; t < TC; ++t) {
+            const int ch = 16 * (tile0 + t) + n;
+            const float v[4] = {sum[r][t].x, sum[r][t].y, sum[r][t].z, sum[r][t].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = 16 * r + 4 * g + i;
+                const uint32_t off = row < nrows && ch < N ? (uint32_t)row * rowb + size * (uint32_t)ch : kOOB;
+                const float o = sxv[i] * (v[i] * post);
+                if (obf)
+                    __builtin_amdgcn_raw_buffer_store_b16(f32_to_bf16_rne(o), ry, off, 0, 0);
+                else
+                    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(o), ry, off, 0, 0);
+            }
+        }
+    }
+}
+
 // --------------------------------------------------------------- launches
 
 struct W4Args {
@@ -348,6 +529,23 @@ void launch_rows(const W4Args &a, int P, bool zeros, int cus, hipStream_t stream
 
 // Token rows of one call: keeps every launch under 2^32 threads.
 constexpr int64_t kMaxRows = 1 << 19;
+
+// a wave's rows of output stay under 2^31 bytes (32-bit store offsets)
+constexpr int64_t kGemmMaxN = (int64_t(1) << 31) / (4 * 128) - 1;
+
+template <int TR, int TC, int WR>
+void launch_gemm(const W4Args &a, int P, bool zeros, hipStream_t stream) {
+    constexpr int BM = 16 * TR * WR, BN = 16 * TC * (8 / WR);
+    const int nbm = (a.M + BM - 1) / BM, nbn = (a.N + BN - 1) / BN;
+    typedef void (*Fn)(const int8_t *, const uint8_t *, int, int, int, int, int, const float *, void *, int);
+    static const Fn fns[3][2] = {
+        {w4_gemm_kernel<TR, TC, WR, 1, false>, w4_gemm_kernel<TR, TC, WR, 1, true>},
+        {w4_gemm_kernel<TR, TC, WR, 2, false>, w4_gemm_kernel<TR, TC, WR, 2, true>},
+        {w4_gemm_kernel<TR, TC, WR, 4, false>, w4_gemm_kernel<TR, TC, WR, 4, true>},
+    };
+    hipLaunchKernelGGL(fns[P == 4 ? 2 : P - 1][zeros], dim3((nbm * nbn + kXcds - 1) / kXcds * kXcds), dim3(512), 0,
+                       stream, a.xq, a.tiled, a.M, a.K, a.N, nbm, nbn, a.xs, a.y, a.obf);
+}
 
 int check_w4(int64_t M, int64_t K, int64_t N, int64_t group, bool zeros) {
     if (M <= 0 || K <= 0 || N <= 0 || group <= 0)
@@ -392,8 +590,10 @@ int launch_linear(const int8_t *xq, const float *xs, int64_t M, int64_t K, int64
         launch_rows<1, 2, 2, 16>(a, P, zeros, cus, stream);
     else if (M <= 16)
         launch_rows<1, 2, 4, 16>(a, P, zeros, cus, stream);
-    else
+    else if (M <= 128 || N > kGemmMaxN)
         launch_rows<2, 2, 4, 8>(a, P, zeros, cus, stream);
+    else
+        launch_gemm<8, 2, 1>(a, P, zeros, stream);
     return s3d8::launch_status();
 }
 
