@@ -64,6 +64,20 @@ __device__ __forceinline__ void load_to_lds16_so(uint32_t lds, uint32_t voff, ui
         : "memory");
 }
 
+// The same with 4 bytes per lane, into LDS at lds + 4 * lane.
+__device__ __forceinline__ void load_to_lds4_so(uint32_t lds, uint32_t voff, uint32_t soff, v4i rsrc) {
+    uint32_t saved;
+    asm volatile(
+        "s_mov_b32 %0, m0\n\t"
+        "s_mov_b32 m0, %1\n\t"
+        "s_nop 0\n\t"
+        "buffer_load_dword %2, %3, %4 offen lds\n\t"
+        "s_mov_b32 m0, %0"
+        : "=&s"(saved)
+        : "s"(lds), "v"(voff), "s"(rsrc), "s"(soff)
+        : "memory");
+}
+
 // Maxima of non-negative floats (absolute values and their maxima, never
 // NaN): for x >= +0 the IEEE bit patterns order like the values, so the
 // reductions compare them as unsigned integers (0 is the identity, and the

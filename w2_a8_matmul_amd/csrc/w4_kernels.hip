@@ -318,76 +318,81 @@ __global__ __launch_bounds__(W * 64) void w4_rows_kernel(const int8_t *__restric
 // --------------------------------------------------------------- product, many rows
 
 // Workgroup tile of 16 TR WR token rows x 16 TC (8 / WR) channels on eight
-// waves, each with TR x TC results of 16 x 16.  The activations go through LDS
-// (an LDS-DMA ring of kGemmRing blocks of 128 columns, stored in A operand
-// order, so that every operand read is contiguous and free of bank
-// conflicts); a wave's weights are its own and go straight to registers, one
-// block ahead.
-template <int TR, int TC, int WR, int P, bool kZeros>
-__global__ __launch_bounds__(512) void w4_gemm_kernel(const int8_t *__restrict__ xq, const uint8_t *__restrict__ tiled,
-                                                      int M, int K, int N, int nbm, int nbn,
-                                                      const float *__restrict__ xs, void *__restrict__ y, int obf) {
-    constexpr int kGemmRing = 3;
-    constexpr int BM = 16 * TR * WR, WC = 8 / WR, BN = 16 * TC * WC;
-    constexpr int NA = BM / 64;                  // activation loads (1 KiB) per wave and block
-    constexpr int NB = TC * (kZeros ? 3 : 2);    // weight, scale and zero-point loads
-    static_assert(BM % 64 == 0, "eight waves share the activation loads evenly");
-    __shared__ __attribute__((aligned(16))) int8_t abuf[kGemmRing][BM * kBlk];
+// waves, each with TR x TC results of 16 x 16.  Everything a block of 128
+// columns needs is copied to LDS by LDS-DMA, S - 1 blocks ahead: the
+// activations, shared by the waves and stored in A operand order (every operand
+// read is contiguous, no bank conflicts), and each wave's own fragments,
+// scales and zero points.  (With the fragments loaded into registers instead,
+// the compiler's waits for them count only the loads it knows and so also wait
+// for younger activation copies.)
+template <int TR, int TC, int WR, int KP, int S, int P, bool kZeros>
+__global__ __launch_bounds__(512, TR * TC <= 16 ? 4 : 2) void w4_gemm_kernel(
+    const int8_t *__restrict__ xq, const uint8_t *__restrict__ tiled, int M, int K, int N, int nbm, int nbn,
+    const float *__restrict__ xs, void *__restrict__ y, int obf) {
+    constexpr int WP = 8 / KP;                     // waves of a column range
+    constexpr int BM = 16 * TR * WR, WC = WP / WR, BN = 16 * TC * WC;
+    constexpr int NA = BM / 8 / WP;                // activation loads (1 KiB) per wave and block
+    constexpr int NL = NA + TC + (kZeros ? 2 : 1);  // all loads per wave and block
+    static_assert(BM / 8 % WP == 0, "the waves of a range share its activation loads evenly");
+    static_assert(TC * 8 * P <= 64, "a wave's scales of a block are one load of 4 bytes per lane");
+    constexpr int kRangeBytes = BM * kBlk, kLds = KP * S * kRangeBytes;
+    constexpr int kSumBytes = KP > 1 ? 8 * TR * TC * 1024 : 0;  // partial sums, after the last block
+    __shared__ __attribute__((aligned(16))) int8_t abuf[kLds > kSumBytes ? kLds : kSumBytes];
+    __shared__ __attribute__((aligned(16))) uint8_t wbuf[S][8][TC * 1024];
+    __shared__ __attribute__((aligned(16))) uint8_t sbuf[S][8][256], zbuf[kZeros ? S : 1][8][256];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int n = lane & 15, g = lane >> 4;
     const int KB = (K + kBlk - 1) / kBlk, tiles = (N + 15) >> 4;
     int bm, bn;
     if (!gemm_tile(nbm, nbn, bm, bn)) return;  // padding workgroup
-    const int row0 = bm * BM, wr = wave / WC, tile0 = bn * (BN / 16) + (wave - wr * WC) * TC;
+    const int part = wave / WP, pw = wave - part * WP;  // column range, wave of it
+    const int row0 = bm * BM, wr = pw / WC, tile0 = bn * (BN / 16) + (pw - wr * WC) * TC;
+    const int steps = (KB + KP - 1) / KP;
 
     const uint32_t frags = (uint32_t)tiles * (uint32_t)KB;
     const v4i rx = rsrc_words(xq, (uint32_t)M * (uint32_t)K);
-    const auto rw = make_rsrc(tiled, frags * 1024u);
-    const auto rs = make_rsrc(tiled + (int64_t)frags * 1024, frags * (32u * P));
-    const auto rz = make_rsrc(tiled + (int64_t)frags * (1024 + 32 * P), kZeros ? frags * (16u * P) : 0u);
+    const v4i rw = rsrc_words(tiled, frags * 1024u);
+    const v4i rs = rsrc_words(tiled + (int64_t)frags * 1024, frags * (32u * P));
+    const v4i rz = rsrc_words(tiled + (int64_t)frags * (1024 + 32 * P), kZeros ? frags * (16u * P) : 0u);
 
-    // activation load L = wave + 8 j: rows 16 (L / 2) .., columns 64 (L % 2) ..
+    // activation load L = pw + WP j: rows 16 (L / 2) .., columns 64 (L % 2) ..
     // of a block, chunk g of row n at 16 lane of KiB L
     uint32_t aoff[NA], atail[NA];
 #pragma unroll
     for (int j = 0; j < NA; ++j) {
-        const int L = wave + 8 * j, row = row0 + 16 * (L >> 1) + n, col = 64 * (L & 1) + 16 * g;
+        const int L = pw + WP * j, row = row0 + 16 * (L >> 1) + n, col = 64 * (L & 1) + 16 * g;
         aoff[j] = row < M ? (uint32_t)row * (uint32_t)K + (uint32_t)col : kOOB;
         atail[j] = (KB - 1) * kBlk + col < K ? aoff[j] : kOOB;
     }
-    auto issue = [&](int kb, int slot) {
-        const uint32_t base = S3D8_LDS_OFFSET(&abuf[0][0]) + (uint32_t)(BM * kBlk * slot) + 1024u * (uint32_t)wave;
-        const uint32_t so = kb < KB ? (uint32_t)(kb * kBlk) : 0u;
+    // scale load: dword `lane` of the wave's TC tiles of 8 P dwords; zero
+    // points: of 4 P dwords.  (A tile past the last one re-reads that one: its
+    // channels are not stored.)
+    auto first = [&](int t) { return (uint32_t)min(tile0 + t, tiles - 1) * (uint32_t)KB; };
+    const uint32_t st = (uint32_t)lane / (8 * P), zt = (uint32_t)lane / (4 * P);
+    const uint32_t soff = st < TC ? first(st) * (32u * P) + 4u * (lane % (8 * P)) : kOOB;
+    const uint32_t zoff = zt < TC ? first(zt) * (16u * P) + 4u * (lane % (4 * P)) : kOOB;
+    uint32_t wfirst[TC];
+#pragma unroll
+    for (int t = 0; t < TC; ++t) wfirst[t] = __builtin_amdgcn_readfirstlane(first(t) * 1024u);
+    const uint32_t alds = S3D8_LDS_OFFSET(&abuf[0]) + (uint32_t)(kRangeBytes * part) + 1024u * (uint32_t)pw;
+    const uint32_t wlds = S3D8_LDS_OFFSET(&wbuf[0][wave][0]);
+    const uint32_t slds = S3D8_LDS_OFFSET(&sbuf[0][wave][0]), zlds = S3D8_LDS_OFFSET(&zbuf[0][wave][0]);
+    // step i of column range `part` is block part + KP i.  Past the last block
+    // the activations are zeros and the weights those of the last one, so
+    // that every wait counts the same and every range takes as many steps.
+    auto issue = [&](int i, int slot) {
+        const int kb = part + KP * i;
+        const uint32_t kbc = (uint32_t)min(kb, KB - 1);
 #pragma unroll
         for (int j = 0; j < NA; ++j)
-            load_to_lds16_so(base + 8192u * j, kb < KB - 1 ? aoff[j] : kb == KB - 1 ? atail[j] : kOOB, so, rx);
-    };
-    struct Raw {
-        uint4 w[TC];
-        uint32_t s[TC][P == 4 ? 2 : 1], z[TC];
-    };
-    auto load = [&](Raw &q, int kb) {
+            load_to_lds16_so(alds + (uint32_t)(KP * kRangeBytes) * slot + (uint32_t)(WP * 1024) * j,
+                             kb < KB - 1 ? aoff[j] : kb == KB - 1 ? atail[j] : kOOB, kbc * kBlk, rx);
 #pragma unroll
-        for (int t = 0; t < TC; ++t) {
-            const bool ok = tile0 + t < tiles && kb < KB;
-            const uint32_t f = (uint32_t)(tile0 + t) * (uint32_t)KB + (uint32_t)kb;
-            q.w[t] = bload16(rw, ok ? f * 1024u + 16u * (uint32_t)lane : kOOB);
-            const uint32_t so = ok ? (f * 16u + (uint32_t)n) * (2u * P) : kOOB;
-            if constexpr (P == 1) q.s[t][0] = __builtin_amdgcn_raw_buffer_load_b16(rs, so, 0, 0);
-            if constexpr (P == 2) q.s[t][0] = __builtin_amdgcn_raw_buffer_load_b32(rs, so, 0, 0);
-            if constexpr (P == 4) {
-                const auto v = __builtin_amdgcn_raw_buffer_load_b64(rs, so, 0, 0);
-                q.s[t][0] = v[0];
-                q.s[t][1] = v[1];
-            }
-            if constexpr (kZeros) {
-                const uint32_t zo = ok ? (f * 16u + (uint32_t)n) * (uint32_t)P : kOOB;
-                if constexpr (P == 1) q.z[t] = __builtin_amdgcn_raw_buffer_load_b8(rz, zo, 0, 0);
-                if constexpr (P == 2) q.z[t] = __builtin_amdgcn_raw_buffer_load_b16(rz, zo, 0, 0);
-                if constexpr (P == 4) q.z[t] = __builtin_amdgcn_raw_buffer_load_b32(rz, zo, 0, 0);
-            }
-        }
+        for (int t = 0; t < TC; ++t)
+            load_to_lds16_so(wlds + (8u * TC * 1024u) * slot + 1024u * t, 16u * lane, wfirst[t] + kbc * 1024u, rw);
+        load_to_lds4_so(slds + 2048u * slot, soff, kbc * (32u * P), rs);
+        if constexpr (kZeros) load_to_lds4_so(zlds + 2048u * slot, zoff, kbc * (16u * P), rz);
     };
 
     float4 sum[TR][TC];
@@ -395,6 +400,7 @@ __global__ __launch_bounds__(512) void w4_gemm_kernel(const int8_t *__restrict__
     for (int r = 0; r < TR; ++r)
 #pragma unroll
         for (int t = 0; t < TC; ++t) sum[r][t] = make_float4(0, 0, 0, 0);
+    typedef int32_t v2i __attribute__((ext_vector_type(2)));
     auto add = [&](float4 &o, const v4i &c, float s) {
         o.x = __builtin_fmaf(s, (float)c[0], o.x);
         o.y = __builtin_fmaf(s, (float)c[1], o.y);
@@ -402,90 +408,156 @@ __global__ __launch_bounds__(512) void w4_gemm_kernel(const int8_t *__restrict__
         o.w = __builtin_fmaf(s, (float)c[3], o.w);
     };
 
-    Raw raw;
-    static_assert(kGemmRing == 3, "two blocks of activations in flight");
-    issue(0, 0);
-    issue(1, 1);
-    load(raw, 0);
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) issue(i, i);
     int slot = 0;
 #pragma unroll 1
-    for (int kb = 0; kb < KB; ++kb) {
-        // this wave's loads of block kb have landed (younger: those of block
-        // kb + 1 and the weights of block kb), everyone's after the barrier,
-        // which also ends every read of block kb - 1's slot
-        wait_vmcnt_barrier<NA + NB>();
-        issue(kb + 2, slot == 0 ? 2 : slot - 1);
+    for (int i = 0; i < steps; ++i) {
+        // this wave's copies of step i have landed, everyone's after the
+        // barrier, which also ends every read of step i - 1's slot
+        wait_vmcnt_barrier<(S - 2) * NL>();
+        issue(i + S - 1, slot == 0 ? S - 1 : slot - 1);
         v4i b[2][TC];
         float s[TC][P];
 #pragma unroll
         for (int t = 0; t < TC; ++t) {
-            const uint32_t wv[4] = {raw.w[t].x, raw.w[t].y, raw.w[t].z, raw.w[t].w};
+            const uint4 w = *reinterpret_cast<const uint4 *>(&wbuf[slot][wave][1024 * t + 16 * lane]);
+            const uint32_t wv[4] = {w.x, w.y, w.z, w.w};
+            uint32_t sv[2] = {0, 0}, zv = 0;
+            const uint8_t *sp = &sbuf[slot][wave][32 * P * t + 2 * P * n], *zp = &zbuf[kZeros ? slot : 0][wave][16 * P * t + P * n];
+            if constexpr (P == 1) sv[0] = *reinterpret_cast<const uint16_t *>(sp);
+            if constexpr (P == 2) sv[0] = *reinterpret_cast<const uint32_t *>(sp);
+            if constexpr (P == 4) {
+                const uint2 v = *reinterpret_cast<const uint2 *>(sp);
+                sv[0] = v.x;
+                sv[1] = v.y;
+            }
+            if constexpr (kZeros) {
+                if constexpr (P == 1) zv = *zp;
+                if constexpr (P == 2) zv = *reinterpret_cast<const uint16_t *>(zp);
+                if constexpr (P == 4) zv = *reinterpret_cast<const uint32_t *>(zp);
+            }
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int d = 0; d < 4; ++d) {
                     const int p = P == 1 ? 0 : P == 2 ? h : 2 * h + (d >> 1);
-                    const uint32_t zrep = kZeros ? ((raw.z[t] >> (8 * p)) & 0xFFu) * 0x01010101u : 0u;
-                    b[h][t][d] = nibbles<kZeros>(wv[d], h, zrep);
+                    b[h][t][d] = nibbles<kZeros>(wv[d], h, kZeros ? ((zv >> (8 * p)) & 0xFFu) * 0x01010101u : 0u);
                 }
 #pragma unroll
-            for (int p = 0; p < P; ++p)
-                s[t][p] = __uint_as_float(p & 1 ? raw.s[t][p >> 1] & 0xFFFF0000u : raw.s[t][p >> 1] << 16);
+            for (int p = 0; p < P; ++p) s[t][p] = __uint_as_float(p & 1 ? sv[p >> 1] & 0xFFFF0000u : sv[p >> 1] << 16);
         }
-        load(raw, kb + 1);
-        const int8_t *at = &abuf[slot][wr * TR * 2048];
+        // The products in TR P steps of TC results each.  A step reads the
+        // next one's activations, issues its own products and scales the
+        // previous step's results, so that neither the reads nor the products
+        // are waited for.
+        const int8_t *at = &abuf[kRangeBytes * (KP * slot + part) + wr * TR * 2048];
         const v4i zero = {0, 0, 0, 0};
-#pragma unroll
-        for (int r = 0; r < TR; ++r) {
+        constexpr int kSteps = TR * P;
+        auto read_a = [&](int i, v4i (&a)[2]) {
+            const int r = i / P, p = i % P;
             if constexpr (P == 4) {
+                // columns 32 p + 8 g .. + 7 of the block: half g % 2 of chunk 2 (p % 2) + g / 2
+                const v2i v = *reinterpret_cast<const v2i *>(at + 2048 * r + 1024 * (p >> 1) + 512 * (p & 1) +
+                                                             256 * (g >> 1) + 16 * n + 8 * (g & 1));
+                a[0][0] = v[0];
+                a[0][1] = v[1];
+            } else {
+                a[0] = *reinterpret_cast<const v4i *>(at + 2048 * r + 1024 * p + 16 * lane);
+                if constexpr (P == 1) a[1] = *reinterpret_cast<const v4i *>(at + 2048 * r + 1024 + 16 * lane);
+            }
+        };
+        auto two = [](int lo, int hi) { return (long)((uint64_t)(uint32_t)lo | (uint64_t)(uint32_t)hi << 32); };
+        v4i a[2][2], c[2][TC];
+        read_a(0, a[0]);
 #pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    // columns 32 p + 8 g .. + 7 of the block: half g % 2 of chunk 2 (p % 2) + g / 2
-                    const long a = *reinterpret_cast<const long *>(at + 2048 * r + 1024 * (p >> 1) + 512 * (p & 1) +
-                                                                   256 * (g >> 1) + 16 * n + 8 * (g & 1));
+        for (int i = 0; i <= kSteps; ++i) {
+            const int p = i % P, now = i & 1;
+            if (i + 1 < kSteps) read_a(i + 1, a[now ^ 1]);
 #pragma unroll
-                    for (int t = 0; t < TC; ++t) {
+            for (int t = 0; t < TC; ++t) {
+                if (i < kSteps) {
+                    if constexpr (P == 4) {
                         const v4i &bv = b[p >> 1][t];
                         const int e = 2 * (p & 1);
-                        const long bl = (long)((uint64_t)(uint32_t)bv[e] | (uint64_t)(uint32_t)bv[e + 1] << 32);
-                        add(sum[r][t], __builtin_amdgcn_mfma_i32_16x16x32_i8(a, bl, zero, 0, 0, 0), s[t][p]);
+                        c[now][t] = __builtin_amdgcn_mfma_i32_16x16x32_i8(two(a[now][0][0], a[now][0][1]),
+                                                                          two(bv[e], bv[e + 1]), zero, 0, 0, 0);
+                    } else {
+                        c[now][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[now][0], b[p][t], zero, 0, 0, 0);
+                        if constexpr (P == 1)
+                            c[now][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[now][1], b[1][t], c[now][t], 0, 0, 0);
                     }
                 }
-            } else {
-                const v4i a0 = *reinterpret_cast<const v4i *>(at + 2048 * r + 16 * lane);
-                const v4i a1 = *reinterpret_cast<const v4i *>(at + 2048 * r + 1024 + 16 * lane);
-#pragma unroll
-                for (int t = 0; t < TC; ++t) {
-                    v4i c = __builtin_amdgcn_mfma_i32_16x16x64_i8(a0, b[0][t], zero, 0, 0, 0);
-                    if constexpr (P == 2) add(sum[r][t], c, s[t][0]);
-                    c = __builtin_amdgcn_mfma_i32_16x16x64_i8(a1, b[1][t], P == 1 ? c : zero, 0, 0, 0);
-                    add(sum[r][t], c, s[t][P - 1]);
-                }
+                if (i > 0) add(sum[(i - 1) / P][t], c[now ^ 1][t], s[t][(i - 1) % P]);
             }
+            __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);  // the reads
+#pragma unroll
+            for (int t = 0; t < TC; ++t) {
+                __builtin_amdgcn_sched_group_barrier(0x008, P == 1 ? 2 : 1, 0);  // a product
+                __builtin_amdgcn_sched_group_barrier(0x002, 8, 0);               // and the scaling of one
+            }
+            __builtin_amdgcn_sched_barrier(0);
         }
-        slot = slot == 2 ? 0 : slot + 1;
+        slot = slot == S - 1 ? 0 : slot + 1;
     }
     wait_vmcnt<0>();  // loads of blocks past the end
+    // the ranges' sums, added in their order; the waves of a range then store
+    // TR / KP row tiles each
+    constexpr int TO = TR / KP;
+    static_assert(TR % KP == 0, "the ranges share the row tiles evenly");
+    float4 out[TO][TC];
+    if constexpr (KP == 1) {
+#pragma unroll
+        for (int r = 0; r < TO; ++r)
+#pragma unroll
+            for (int t = 0; t < TC; ++t) out[r][t] = sum[r][t];
+    } else {
+        wait_vmcnt_barrier<0>();  // every wave has read its last block
+        float4 *red = reinterpret_cast<float4 *>(&abuf[0]);
+#pragma unroll
+        for (int r = 0; r < TR; ++r)
+#pragma unroll
+            for (int t = 0; t < TC; ++t) red[((part * WP + pw) * TR * TC + r * TC + t) * 64 + lane] = sum[r][t];
+        wait_vmcnt_barrier<0>();
+#pragma unroll
+        for (int r = 0; r < TO; ++r)
+#pragma unroll
+            for (int t = 0; t < TC; ++t) {
+                float4 v = make_float4(0, 0, 0, 0);
+#pragma unroll
+                for (int q = 0; q < KP; ++q) {
+                    const float4 u = red[((q * WP + pw) * TR * TC + (part * TO + r) * TC + t) * 64 + lane];
+                    v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
+                }
+                out[r][t] = v;
+            }
+    }
 
-    // result lane (n, g), element i: row 4 g + i of the row tile, channel n
-    const int wrow = row0 + 16 * TR * wr, nrows = min(M - wrow, 16 * TR);
+    // result lane (n, g), element i: row 4 g + i of the row tile, channel n.
+    // Rows past M lie past the end of the buffer and channels past N get an
+    // offset that does: those stores are dropped.
+    const int wrow = row0 + 16 * (TR * wr + TO * part), nrows = min(M - wrow, 16 * TO);
     if (nrows <= 0) return;
     const uint32_t size = obf ? 2u : 4u, rowb = size * (uint32_t)N;
     const auto ry = make_rsrc(static_cast<char *>(y) + (int64_t)wrow * N * size, rowb * (uint32_t)nrows);
     const auto rxs = make_rsrc(xs + wrow, 4u * (uint32_t)nrows);
     const float post = kZeros ? 1.0f : 0.0625f;
+    uint32_t base[TC];
 #pragma unroll
-    for (int r = 0; r < TR; ++r) {
+    for (int t = 0; t < TC; ++t) {
+        const int ch = 16 * (tile0 + t) + n;
+        base[t] = ch < N ? 4u * g * rowb + size * (uint32_t)ch : kOOB;
+    }
+#pragma unroll
+    for (int r = 0; r < TO; ++r) {
         const uint4 sx = bload16(rxs, 64u * r + 16u * g);
         const float sxv[4] = {__uint_as_float(sx.x), __uint_as_float(sx.y), __uint_as_float(sx.z), __uint_as_float(sx.w)};
 #pragma unroll
         for (int t = 0; t < TC; ++t) {
-            const int ch = 16 * (tile0 + t) + n;
-            const float v[4] = {sum[r][t].x, sum[r][t].y, sum[r][t].z, sum[r][t].w};
+            const float v[4] = {out[r][t].x, out[r][t].y, out[r][t].z, out[r][t].w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int row = 16 * r + 4 * g + i;
-                const uint32_t off = row < nrows && ch < N ? (uint32_t)row * rowb + size * (uint32_t)ch : kOOB;
+                const uint32_t off = base[t] + (uint32_t)(16 * r + i) * rowb;
                 const float o = sxv[i] * (v[i] * post);
                 if (obf)
                     __builtin_amdgcn_raw_buffer_store_b16(f32_to_bf16_rne(o), ry, off, 0, 0);
@@ -530,18 +602,48 @@ void launch_rows(const W4Args &a, int P, bool zeros, int cus, hipStream_t stream
 // Token rows of one call: keeps every launch under 2^32 threads.
 constexpr int64_t kMaxRows = 1 << 19;
 
+// Workgroup tiles of the GEMM: rows and channels, column ranges (waves split
+// between them), and the time of a step of `ranges` blocks and of everything
+// else, in ns, from K = 4096 with one workgroup on a CU (a second one beside
+// it gains little: a workgroup keeps its SIMDs' issue busy).
+struct GemmTile {
+    int rows, channels, ranges, step_ns, fixed_ns;
+};
+constexpr GemmTile kGemmTiles[] = {
+    {128, 256, 1, 1500, 3000}, {64, 256, 1, 920, 3000}, {64, 128, 2, 950, 3000},
+    {64, 64, 4, 1050, 3000},   {32, 128, 2, 620, 3000}, {64, 32, 4, 650, 3000},
+};
+
+// The tile with the least estimated time: rounds of workgroups on the CUs
+// times a workgroup's time.
+int gemm_tile_choice(int64_t M, int64_t K, int64_t N, int cus) {
+    const int64_t KB = (K + kBlk - 1) / kBlk;
+    int best = 0;
+    int64_t least = 0;
+    for (int i = 0; i < (int)(sizeof(kGemmTiles) / sizeof(kGemmTiles[0])); ++i) {
+        const GemmTile &t = kGemmTiles[i];
+        const int64_t wgs = ((M + t.rows - 1) / t.rows) * ((N + t.channels - 1) / t.channels);
+        const int64_t ns = ((wgs + cus - 1) / cus) * ((KB + t.ranges - 1) / t.ranges * t.step_ns + t.fixed_ns);
+        if (i == 0 || ns < least) {
+            least = ns;
+            best = i;
+        }
+    }
+    return best;
+}
+
 // a wave's rows of output stay under 2^31 bytes (32-bit store offsets)
 constexpr int64_t kGemmMaxN = (int64_t(1) << 31) / (4 * 128) - 1;
 
-template <int TR, int TC, int WR>
+template <int TR, int TC, int WR, int KP, int S>
 void launch_gemm(const W4Args &a, int P, bool zeros, hipStream_t stream) {
-    constexpr int BM = 16 * TR * WR, BN = 16 * TC * (8 / WR);
+    constexpr int BM = 16 * TR * WR, BN = 16 * TC * (8 / KP / WR);
     const int nbm = (a.M + BM - 1) / BM, nbn = (a.N + BN - 1) / BN;
     typedef void (*Fn)(const int8_t *, const uint8_t *, int, int, int, int, int, const float *, void *, int);
     static const Fn fns[3][2] = {
-        {w4_gemm_kernel<TR, TC, WR, 1, false>, w4_gemm_kernel<TR, TC, WR, 1, true>},
-        {w4_gemm_kernel<TR, TC, WR, 2, false>, w4_gemm_kernel<TR, TC, WR, 2, true>},
-        {w4_gemm_kernel<TR, TC, WR, 4, false>, w4_gemm_kernel<TR, TC, WR, 4, true>},
+        {w4_gemm_kernel<TR, TC, WR, KP, S, 1, false>, w4_gemm_kernel<TR, TC, WR, KP, S, 1, true>},
+        {w4_gemm_kernel<TR, TC, WR, KP, S, 2, false>, w4_gemm_kernel<TR, TC, WR, KP, S, 2, true>},
+        {w4_gemm_kernel<TR, TC, WR, KP, S, 4, false>, w4_gemm_kernel<TR, TC, WR, KP, S, 4, true>},
     };
     hipLaunchKernelGGL(fns[P == 4 ? 2 : P - 1][zeros], dim3((nbm * nbn + kXcds - 1) / kXcds * kXcds), dim3(512), 0,
                        stream, a.xq, a.tiled, a.M, a.K, a.N, nbm, nbn, a.xs, a.y, a.obf);
@@ -590,10 +692,17 @@ int launch_linear(const int8_t *xq, const float *xs, int64_t M, int64_t K, int64
         launch_rows<1, 2, 2, 16>(a, P, zeros, cus, stream);
     else if (M <= 16)
         launch_rows<1, 2, 4, 16>(a, P, zeros, cus, stream);
-    else if (M <= 128 || N > kGemmMaxN)
+    else if (N > kGemmMaxN)
         launch_rows<2, 2, 4, 8>(a, P, zeros, cus, stream);
     else
-        launch_gemm<8, 2, 1>(a, P, zeros, stream);
+        switch (gemm_tile_choice(M, K, N, cus)) {
+            case 0: launch_gemm<8, 2, 1, 1, 2>(a, P, zeros, stream); break;
+            case 1: launch_gemm<4, 2, 1, 1, 3>(a, P, zeros, stream); break;
+            case 2: launch_gemm<4, 2, 1, 2, 3>(a, P, zeros, stream); break;
+            case 3: launch_gemm<4, 2, 1, 4, 3>(a, P, zeros, stream); break;
+            case 4: launch_gemm<2, 2, 1, 2, 3>(a, P, zeros, stream); break;
+            default: launch_gemm<4, 1, 1, 4, 3>(a, P, zeros, stream); break;
+        }
     return s3d8::launch_status();
 }
 
