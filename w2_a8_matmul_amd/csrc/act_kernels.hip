@@ -14,18 +14,35 @@
 
 namespace {
 
-constexpr int kRowThreads = 1024;
-constexpr int64_t kMaxWidth = 65536;    // 16 float4 per thread
+constexpr int64_t kMaxWidth = 65536;    // 16 float4 per thread of 1024
 constexpr int64_t kMaxRows = 1 << 19;   // keeps a launch under 2^32 threads
 
-// Four consecutive values of an fp32 or bf16 row.
-__device__ __forceinline__ float4 load4(const void *p, int64_t at, bool bf) {
+__device__ __forceinline__ float4 bf16x4_values(uint2 u) {
+    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
+                       __uint_as_float(u.y & 0xFFFF0000u));
+}
+
+// A workgroup's share of a row of K fp32 or bf16 values from element `base`: thread
+// t of T takes float4 t, t + T, ... (zeros past the row).
+template <int T, int NV>
+__device__ __forceinline__ void load_row(float4 (&v)[NV], const void *p, int64_t base, int n4, bool bf) {
     if (bf) {
-        const uint2 u = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p) + at);
-        return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
-                           __uint_as_float(u.y & 0xFFFF0000u));
+        uint2 u[NV];
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int i = threadIdx.x + j * T;
+            u[j] = i < n4 ? reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p) + base)[i] : make_uint2(0, 0);
+        }
+#pragma unroll
+        for (int j = 0; j < NV; ++j) v[j] = bf16x4_values(u[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int i = threadIdx.x + j * T;
+            v[j] = i < n4 ? reinterpret_cast<const float4 *>(static_cast<const float *>(p) + base)[i]
+                          : make_float4(0, 0, 0, 0);
+        }
     }
-    return *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + at);
 }
 
 __device__ __forceinline__ uint2 bf16x4(float4 v) {
@@ -49,12 +66,34 @@ __device__ __forceinline__ float4 zip4(float4 a, float4 b, F f) {
     return make_float4(f(a.x, b.x), f(a.y, b.y), f(a.z, b.z), f(a.w, b.w));
 }
 
-// Sum over the workgroup's T threads, the same in every thread.  `slot` is LDS
-// not used by the previous reduction (one barrier per reduction).
+// v plus lane-permuted v, both halves of the double through DPP.
+template <int kCtrl>
+__device__ __forceinline__ double dpp_add(double v) {
+    const uint64_t b = (uint64_t)__double_as_longlong(v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, kCtrl, 0xF, 0xF, false);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), kCtrl, 0xF, 0xF, false);
+    return v + __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
+}
+__device__ __forceinline__ double lane_value(double v, int lane) {
+    const uint64_t b = (uint64_t)__double_as_longlong(v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, lane);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), lane);
+    return __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
+}
+// Sum over the wave, wave-uniform (the moves of row16_max: within pairs, within
+// quads, halves of 8 mirrored, the row of 16 mirrored, then the four rows).
+__device__ __forceinline__ double wave_sum(double v) {
+    v = dpp_add<0x140>(dpp_add<0x141>(dpp_add<0x4E>(dpp_add<0xB1>(v))));
+    return (lane_value(v, 0) + lane_value(v, 16)) + (lane_value(v, 32) + lane_value(v, 48));
+}
+
+// Sum and maximum over the workgroup's T threads, the same in every thread.
+// `slot` is LDS not used by the previous reduction (one barrier per reduction,
+// none for a workgroup of one wave).
 template <int T>
 __device__ __forceinline__ double block_sum(double v, double *slot) {
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
+    v = wave_sum(v);
+    if constexpr (T == 64) return v;
     if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = v;
     __syncthreads();
     v = slot[0];
@@ -66,6 +105,7 @@ __device__ __forceinline__ double block_sum(double v, double *slot) {
 template <int T>
 __device__ __forceinline__ float block_max(float v, float *slot) {
     v = wave_max(v);
+    if constexpr (T == 64) return v;
     if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = v;
     __syncthreads();
     v = slot[0];
@@ -95,15 +135,36 @@ __device__ __forceinline__ void row_out(const float4 (&v)[NV], int64_t row, int 
     a = block_max<T>(a, slot);
     const float s = a / 127.0f;
     if (threadIdx.x == 0) xs[row] = s;
-    auto code = [&](float x) {
-        return a == 0.0f ? 0u : (uint32_t)(uint8_t)(int8_t)fminf(127.0f, fmaxf(-127.0f, rintf(x / s)));
-    };
+    // The code is rne(fl(x / s)).  t = x fl(1 / s) differs from x / s by less than
+    // 127 2^-23, fl(x / s) by less than 127 2^-24: where t is further than 2^-15
+    // from a border k + 1/2, rne(t) is the code.  A thread with a value nearer
+    // than that (or with 1 / s infinite) divides.
+    const float rs = 1.0f / s;
+    bool divide = false;
+    uint32_t q[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const float x[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+        q[j] = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float t = x[e] * rs, k = rintf(t);
+            divide |= !(fabsf(t - k) <= 0.5f - 0x1p-15f);
+            q[j] |= (uint32_t)((int)k & 0xFF) << (8 * e);
+        }
+    }
+    if (divide) {
+        auto code = [&](float x) {
+            return a == 0.0f ? 0u : (uint32_t)(uint8_t)(int8_t)fminf(127.0f, fmaxf(-127.0f, rintf(x / s)));
+        };
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            q[j] = code(v[j].x) | code(v[j].y) << 8 | code(v[j].z) << 16 | code(v[j].w) << 24;
+    }
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const int i = threadIdx.x + j * T;
-        if (i < n4)
-            *reinterpret_cast<uint32_t *>(xq + row * K + 4 * i) =
-                code(v[j].x) | code(v[j].y) << 8 | code(v[j].z) << 16 | code(v[j].w) << 24;
+        if (i < n4) reinterpret_cast<uint32_t *>(xq + row * K)[i] = q[j];
     }
 }
 
@@ -154,18 +215,10 @@ __global__ __launch_bounds__(T) void block_norm_kernel(const s3d8_block_norm_arg
     const int K = (int)p.K, n4 = K >> 2;
     const bool layer = p.kind == S3D8_NORM_LAYER;
     float4 h[NV];
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int i = threadIdx.x + j * T;
-        h[j] = i < n4 ? load4(p.h, row * K + 4 * i, p.h_type == S3D8_ROWS_BF16) : make_float4(0, 0, 0, 0);
-    }
+    load_row<T, NV>(h, p.h, row * K, n4, p.h_type == S3D8_ROWS_BF16);
     if (p.branch) {
         float4 b[NV];
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int i = threadIdx.x + j * T;
-            b[j] = i < n4 ? load4(p.branch, row * K + 4 * i, p.branch_type == S3D8_ROWS_BF16) : make_float4(0, 0, 0, 0);
-        }
+        load_row<T, NV>(b, p.branch, row * K, n4, p.branch_type == S3D8_ROWS_BF16);
         if (p.post_weight) normalise<T, NV>(b, K, layer, p.eps, p.post_weight, p.post_bias, sums[0]);
         const float rs = p.residual_scale;
         auto factor = [&](float g) { return p.gate_tanh ? (float)tanh((double)g) : g; };
@@ -185,8 +238,7 @@ __global__ __launch_bounds__(T) void block_norm_kernel(const s3d8_block_norm_arg
                 // the norm reads the residual as it is stored
                 const uint2 u = bf16x4(h[j]);
                 *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.h_out) + row * K + 4 * i) = u;
-                h[j] = make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u),
-                                   __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xFFFF0000u));
+                h[j] = bf16x4_values(u);
             } else {
                 *reinterpret_cast<float4 *>(static_cast<float *>(p.h_out) + row * K + 4 * i) = h[j];
             }
@@ -196,9 +248,35 @@ __global__ __launch_bounds__(T) void block_norm_kernel(const s3d8_block_norm_arg
     row_out<T, NV>(h, row, K, p.out_type, p.rows, p.xq, p.xs, maxima);
 }
 
-// SiLU(g) * u in 64 bits, rounded once.
+// SiLU(g) * u = g u / (1 + exp(-g)) in 64 bits, rounded to fp32 once, to a
+// relative 2^-50 before that (so that it is the correctly rounded product but
+// for one value in some 2^25).  exp: -g = n ln 2 + r with ln 2 in two parts, a
+// degree-11 polynomial on |r| <= ln 2 / 2 (Chebyshev interpolation, relative
+// error 2^-55.7), 2^n by ldexp.  |g| is cut at 700, where the result is already
+// g u or, below 2^-149, a zero of its sign; the denominator stays finite.
+// The quotient: two Newton steps on the hardware reciprocal.
+// About 31 instructions against some 80 of the library's exp and division.
 __device__ __forceinline__ float gated(float g, float u) {
-    return (float)((double)g / (1.0 + exp(-(double)g)) * (double)u);
+    const double x = (double)-__builtin_amdgcn_fmed3f(g, -700.0f, 700.0f);
+    const double n = __builtin_rint(x * 0x1.71547652b82fep+0);
+    const double r = __builtin_fma(n, -0x1.a39ef35793c76p-33, __builtin_fma(n, -0x1.62e42fee00000p-1, x));
+    double e = 0x1.af631d203b4edp-26;
+    e = __builtin_fma(e, r, 0x1.28b405992d897p-22);
+    e = __builtin_fma(e, r, 0x1.71ddf5748bd71p-19);
+    e = __builtin_fma(e, r, 0x1.a01991ac6b2ddp-16);
+    e = __builtin_fma(e, r, 0x1.a01a01b1437f6p-13);
+    e = __builtin_fma(e, r, 0x1.6c16c187fbea9p-10);
+    e = __builtin_fma(e, r, 0x1.111111110f225p-7);
+    e = __builtin_fma(e, r, 0x1.555555554f0cep-5);
+    e = __builtin_fma(e, r, 0x1.555555555555ap-3);
+    e = __builtin_fma(e, r, 0x1.0000000000011p-1);
+    e = __builtin_fma(e, r, 1.0);
+    e = __builtin_fma(e, r, 1.0);
+    const double d = 1.0 + __builtin_amdgcn_ldexp(e, (int)n), a = (double)g * (double)u;
+    double q = __builtin_amdgcn_rcp(d);
+    q = __builtin_fma(q, __builtin_fma(-d, q, 1.0), q);
+    q = __builtin_fma(q, __builtin_fma(-d, q, 1.0), q);
+    return (float)(a * q);
 }
 
 template <int T, int NV>
@@ -209,18 +287,54 @@ __global__ __launch_bounds__(T) void glu_act_kernel(const void *__restrict__ gat
     __shared__ float maxima[T / 64];
     const int64_t row = blockIdx.x;
     const int n4 = K >> 2;
-    float4 v[NV];
+    float4 v[NV], u[NV];
+    load_row<T, NV>(v, gate, row * ldg, n4, in_bf);
+    load_row<T, NV>(u, up, row * ldu, n4, in_bf);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int i = threadIdx.x + j * T;
-        v[j] = make_float4(0, 0, 0, 0);
-        if (i < n4)
-            v[j] = zip4(load4(gate, row * ldg + 4 * i, in_bf), load4(up, row * ldu + 4 * i, in_bf), gated);
-    }
+    for (int j = 0; j < NV; ++j)
+        if ((int)threadIdx.x + j * T < n4) v[j] = zip4(v[j], u[j], gated);
     row_out<T, NV>(v, row, K, out_type, rows, xq, xs, maxima);
 }
 
 // --------------------------------------------------------------- host
+
+struct BlockNorm {
+    template <int T, int NV>
+    static constexpr auto kernel() { return &block_norm_kernel<T, NV>; }
+};
+struct GluAct {
+    template <int T, int NV>
+    static constexpr auto kernel() { return &glu_act_kernel<T, NV>; }
+};
+
+template <class Op, int T>
+auto row_kernel_of(int64_t nv) {
+    switch (nv) {
+        case 1: return Op::template kernel<T, 1>();
+        case 2: return Op::template kernel<T, 2>();
+        case 3: return Op::template kernel<T, 3>();
+        case 4: return Op::template kernel<T, 4>();
+        case 5: return Op::template kernel<T, 5>();
+        case 6: return Op::template kernel<T, 6>();
+        case 7: return Op::template kernel<T, 7>();
+        default: return Op::template kernel<T, 8>();
+    }
+}
+
+// The workgroup of a row: where there are rows for every CU, the fewest threads
+// that hold it in 8 float4 each (few waves to join, many rows on a CU); else as
+// many as it has float4 (short chains).
+template <class Op>
+auto row_kernel(int64_t M, int64_t K, int cus, int &threads) {
+    const int64_t n4 = K / 4;
+    auto nv = [&](int t) { return (n4 + t - 1) / t; };
+    const int64_t most = M >= 2 * cus ? 8 : 1;
+    if (nv(64) <= most) return threads = 64, row_kernel_of<Op, 64>(nv(64));
+    if (nv(256) <= most) return threads = 256, row_kernel_of<Op, 256>(nv(256));
+    if (nv(512) <= most) return threads = 512, row_kernel_of<Op, 512>(nv(512));
+    threads = 1024;
+    return nv(1024) <= 8 ? row_kernel_of<Op, 1024>(nv(1024)) : Op::template kernel<1024, 16>();
+}
 
 bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
@@ -273,15 +387,12 @@ int32_t s3d8_block_norm(const s3d8_block_norm_args *args, void *stream) {
         !aligned(a.bias, 16) || !aligned(a.post_weight, 16) || !aligned(a.post_bias, 16) ||
         !aligned(a.gate, a.gate_channels ? 16 : 4))
         return s3d8::fail(S3D8_ERR_ALIGN, "rows and [K] vectors must be 16-byte aligned");
-    rc = s3d8::check_device(nullptr);
+    int cus = 0;
+    rc = s3d8::check_device(&cus);
     if (rc) return rc;
-    const int64_t nv = (a.K / 4 + kRowThreads - 1) / kRowThreads;
-    void (*fn)(s3d8_block_norm_args) = nv <= 1   ? block_norm_kernel<kRowThreads, 1>
-                                       : nv <= 2 ? block_norm_kernel<kRowThreads, 2>
-                                       : nv <= 4 ? block_norm_kernel<kRowThreads, 4>
-                                       : nv <= 8 ? block_norm_kernel<kRowThreads, 8>
-                                                 : block_norm_kernel<kRowThreads, 16>;
-    hipLaunchKernelGGL(fn, dim3((unsigned)a.M), dim3(kRowThreads), 0, (hipStream_t)stream, a);
+    int threads = 0;
+    const auto fn = row_kernel<BlockNorm>(a.M, a.K, cus, threads);
+    hipLaunchKernelGGL(fn, dim3((unsigned)a.M), dim3(threads), 0, (hipStream_t)stream, a);
     return s3d8::launch_status();
 }
 
@@ -299,15 +410,12 @@ int32_t s3d8_glu_act(const void *gate, int64_t ld_gate, const void *up, int64_t 
     const uintptr_t four = in_type == S3D8_ROWS_F32 ? 16 : 8;
     if (ld_gate % 4 || ld_up % 4 || !aligned(gate, four) || !aligned(up, four))
         return s3d8::fail(S3D8_ERR_ALIGN, "gate and up rows must be aligned to 4 elements");
-    rc = s3d8::check_device(nullptr);
+    int cus = 0;
+    rc = s3d8::check_device(&cus);
     if (rc) return rc;
-    const int64_t nv = (K / 4 + kRowThreads - 1) / kRowThreads;
-    auto *fn = nv <= 1   ? glu_act_kernel<kRowThreads, 1>
-               : nv <= 2 ? glu_act_kernel<kRowThreads, 2>
-               : nv <= 4 ? glu_act_kernel<kRowThreads, 4>
-               : nv <= 8 ? glu_act_kernel<kRowThreads, 8>
-                         : glu_act_kernel<kRowThreads, 16>;
-    hipLaunchKernelGGL(fn, dim3((unsigned)M), dim3(kRowThreads), 0, (hipStream_t)stream, gate, ld_gate, up, ld_up,
+    int threads = 0;
+    const auto fn = row_kernel<GluAct>(M, K, cus, threads);
+    hipLaunchKernelGGL(fn, dim3((unsigned)M), dim3(threads), 0, (hipStream_t)stream, gate, ld_gate, up, ld_up,
                        (int)K, (int)(in_type == S3D8_ROWS_BF16), out_type, rows, xq, xs);
     return s3d8::launch_status();
 }
