@@ -6,7 +6,9 @@
 // workgroup through its reductions, and is written once.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "s3d8.h"
 #include "s3d8_device.h"
@@ -22,32 +24,32 @@ __device__ __forceinline__ float4 bf16x4_values(uint2 u) {
                        __uint_as_float(u.y & 0xFFFF0000u));
 }
 
-// A workgroup's share of a row of K fp32 or bf16 values from element `base`: thread
-// t of T takes float4 t, t + T, ... (zeros past the row).
-template <int T, int NV>
-__device__ __forceinline__ void load_row(float4 (&v)[NV], const void *p, int64_t base, int n4, bool bf) {
-    if (bf) {
-        uint2 u[NV];
+// A workgroup's share of a row of K fp32 or bf16 values from element `base`, as it
+// lies in memory: thread t of T takes four values at 4 (t + T j), j < NV (zeros
+// past the row).
+template <bool kBF>
+using Raw = std::conditional_t<kBF, uint2, float4>;
+__device__ __forceinline__ float4 values(float4 r) { return r; }
+__device__ __forceinline__ float4 values(uint2 r) { return bf16x4_values(r); }
+
+template <int T, int NV, bool kBF>
+__device__ __forceinline__ void load_row(Raw<kBF> (&r)[NV], const void *p, int64_t base, int n4) {
+    using E = std::conditional_t<kBF, uint16_t, float>;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int i = threadIdx.x + j * T;
-            u[j] = i < n4 ? reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p) + base)[i] : make_uint2(0, 0);
-        }
-#pragma unroll
-        for (int j = 0; j < NV; ++j) v[j] = bf16x4_values(u[j]);
-    } else {
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int i = threadIdx.x + j * T;
-            v[j] = i < n4 ? reinterpret_cast<const float4 *>(static_cast<const float *>(p) + base)[i]
-                          : make_float4(0, 0, 0, 0);
-        }
+    for (int j = 0; j < NV; ++j) {
+        const int i = threadIdx.x + j * T;
+        r[j] = i < n4 ? reinterpret_cast<const Raw<kBF> *>(static_cast<const E *>(p) + base)[i] : Raw<kBF>{};
     }
 }
 
+// Workgroup barrier for LDS alone: loads from memory stay in flight.
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// Four values rounded to bf16, to nearest even.
 __device__ __forceinline__ uint2 bf16x4(float4 v) {
-    return make_uint2(f32_to_bf16_rne(v.x) | (uint32_t)f32_to_bf16_rne(v.y) << 16,
-                      f32_to_bf16_rne(v.z) | (uint32_t)f32_to_bf16_rne(v.w) << 16);
+    typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+    const bf2 lo = {(__bf16)v.x, (__bf16)v.y}, hi = {(__bf16)v.z, (__bf16)v.w};  // v_cvt_pk_bf16_f32
+    return make_uint2(__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi));
 }
 
 __device__ __forceinline__ void store4(void *p, int64_t at, float4 v, bool bf) {
@@ -95,7 +97,7 @@ __device__ __forceinline__ double block_sum(double v, double *slot) {
     v = wave_sum(v);
     if constexpr (T == 64) return v;
     if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = v;
-    __syncthreads();
+    lds_barrier();
     v = slot[0];
 #pragma unroll
     for (int w = 1; w < T / 64; ++w) v += slot[w];
@@ -107,11 +109,26 @@ __device__ __forceinline__ float block_max(float v, float *slot) {
     v = wave_max(v);
     if constexpr (T == 64) return v;
     if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = v;
-    __syncthreads();
+    lds_barrier();
     v = slot[0];
 #pragma unroll
     for (int w = 1; w < T / 64; ++w) v = fmaxf(v, slot[w]);
     return v;
+}
+
+// Codes rne(x rs) of four values, |x rs| < 2^22, and in `far` the largest distance of
+// an x rs from its code.  Adding 1.5 2^23 rounds to an integer, whose low byte
+// is then the low byte of the sum.
+__device__ __forceinline__ uint32_t codes4(float4 x, float rs, float &far) {
+    constexpr float kRound = 12582912.0f;
+    const float m[4] = {__builtin_fmaf(x.x, rs, kRound), __builtin_fmaf(x.y, rs, kRound), __builtin_fmaf(x.z, rs, kRound),
+                        __builtin_fmaf(x.w, rs, kRound)};
+    const float d[4] = {__builtin_fmaf(x.x, rs, kRound - m[0]), __builtin_fmaf(x.y, rs, kRound - m[1]),
+                        __builtin_fmaf(x.z, rs, kRound - m[2]), __builtin_fmaf(x.w, rs, kRound - m[3])};
+    far = fmaxf(fmaxf(far, fmaxf(fabsf(d[0]), fabsf(d[1]))), fmaxf(fabsf(d[2]), fabsf(d[3])));
+    const uint32_t lo = __builtin_amdgcn_perm(__float_as_uint(m[1]), __float_as_uint(m[0]), 0x0C0C0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(__float_as_uint(m[3]), __float_as_uint(m[2]), 0x04000C0Cu);
+    return lo | hi;
 }
 
 // The row (NV float4 per thread, zeros past n4) out: fp32, bf16, or its codes
@@ -140,20 +157,11 @@ __device__ __forceinline__ void row_out(const float4 (&v)[NV], int64_t row, int 
     // from a border k + 1/2, rne(t) is the code.  A thread with a value nearer
     // than that (or with 1 / s infinite) divides.
     const float rs = 1.0f / s;
-    bool divide = false;
+    float far = 0.0f;
     uint32_t q[NV];
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const float x[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
-        q[j] = 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float t = x[e] * rs, k = rintf(t);
-            divide |= !(fabsf(t - k) <= 0.5f - 0x1p-15f);
-            q[j] |= (uint32_t)((int)k & 0xFF) << (8 * e);
-        }
-    }
-    if (divide) {
+    for (int j = 0; j < NV; ++j) q[j] = codes4(v[j], rs, far);
+    if (!(far <= 0.5f - 0x1p-15f && rs < INFINITY)) {
         auto code = [&](float x) {
             return a == 0.0f ? 0u : (uint32_t)(uint8_t)(int8_t)fminf(127.0f, fmaxf(-127.0f, rintf(x / s)));
         };
@@ -171,25 +179,29 @@ __device__ __forceinline__ void row_out(const float4 (&v)[NV], int64_t row, int 
 // N(v; w, b) of a row.  The statistics are sums of exact products in 64 bits,
 // rounded to fp32 once: an fp32 sum would depend on its order, and its last
 // bit moves codes across their rounding borders.
-template <int T, int NV>
-__device__ __forceinline__ void normalise(float4 (&v)[NV], int K, bool layer, float eps, const float *__restrict__ w,
+template <int T, int NV, bool kLayer>
+__device__ __forceinline__ void normalise(float4 (&v)[NV], int K, float eps, const float *__restrict__ w,
                                           const float *__restrict__ b, double *slot) {
     const int n4 = K >> 2;
-    double mu = 0.0;
-    if (layer) {
+    double mu = 0.0, q = 0.0;
+    if constexpr (kLayer) {
         double s = 0.0;
 #pragma unroll
         for (int j = 0; j < NV; ++j) s += ((double)v[j].x + (double)v[j].y) + ((double)v[j].z + (double)v[j].w);
         mu = block_sum<T>(s, slot) / (double)K;
         slot += T / 64;
     }
-    double q = 0.0;
+    auto square = [&](float x) {
+        const double y = kLayer ? (double)x - mu : (double)x;
+        q = __builtin_fma(y, y, q);
+    };
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        if ((int)threadIdx.x + j * T < n4) {  // (past the row v is 0, not mu)
-            const double x = v[j].x - mu, y = v[j].y - mu, z = v[j].z - mu, t = v[j].w - mu;
-            q += (x * x + y * y) + (z * z + t * t);
-        }
+        if (kLayer && (int)threadIdx.x + j * T >= n4) continue;  // (past the row v is 0, not mu)
+        square(v[j].x);
+        square(v[j].y);
+        square(v[j].z);
+        square(v[j].w);
     }
     const float r = (float)(1.0 / sqrt(block_sum<T>(q, slot) / (double)K + (double)eps));
     const float m = (float)mu;
@@ -198,66 +210,22 @@ __device__ __forceinline__ void normalise(float4 (&v)[NV], int K, bool layer, fl
         const int i = threadIdx.x + j * T;
         if (i >= n4) continue;
         float4 u = v[j];
-        if (layer) u = map4(u, [&](float x) { return x - m; });
+        if constexpr (kLayer) u = map4(u, [&](float x) { return x - m; });
         u = zip4(map4(u, [&](float x) { return x * r; }), reinterpret_cast<const float4 *>(w)[i],
                  [](float x, float y) { return x * y; });
-        if (b) u = zip4(u, reinterpret_cast<const float4 *>(b)[i], [](float x, float y) { return x + y; });
+        if constexpr (kLayer)
+            if (b) u = zip4(u, reinterpret_cast<const float4 *>(b)[i], [](float x, float y) { return x + y; });
         v[j] = u;
     }
 }
 
-// One workgroup per row.
-template <int T, int NV>
-__global__ __launch_bounds__(T) void block_norm_kernel(const s3d8_block_norm_args p) {
-    __shared__ double sums[4][T / 64];
-    __shared__ float maxima[T / 64];
-    const int64_t row = blockIdx.x;
-    const int K = (int)p.K, n4 = K >> 2;
-    const bool layer = p.kind == S3D8_NORM_LAYER;
-    float4 h[NV];
-    load_row<T, NV>(h, p.h, row * K, n4, p.h_type == S3D8_ROWS_BF16);
-    if (p.branch) {
-        float4 b[NV];
-        load_row<T, NV>(b, p.branch, row * K, n4, p.branch_type == S3D8_ROWS_BF16);
-        if (p.post_weight) normalise<T, NV>(b, K, layer, p.eps, p.post_weight, p.post_bias, sums[0]);
-        const float rs = p.residual_scale;
-        auto factor = [&](float g) { return p.gate_tanh ? (float)tanh((double)g) : g; };
-        const float g1 = p.gate && !p.gate_channels ? factor(*p.gate) : 1.0f;
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int i = threadIdx.x + j * T;
-            if (i >= n4) continue;
-            float4 t = b[j];
-            if (p.gate && p.gate_channels)
-                t = zip4(map4(reinterpret_cast<const float4 *>(p.gate)[i], factor), t,
-                         [](float g, float x) { return g * x; });
-            else
-                t = map4(t, [&](float x) { return g1 * x; });
-            h[j] = zip4(h[j], t, [&](float x, float y) { return rs * x + y; });
-            if (p.h_type == S3D8_ROWS_BF16) {
-                // the norm reads the residual as it is stored
-                const uint2 u = bf16x4(h[j]);
-                *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.h_out) + row * K + 4 * i) = u;
-                h[j] = bf16x4_values(u);
-            } else {
-                *reinterpret_cast<float4 *>(static_cast<float *>(p.h_out) + row * K + 4 * i) = h[j];
-            }
-        }
-    }
-    normalise<T, NV>(h, K, layer, p.eps, p.weight, p.bias, sums[2]);
-    row_out<T, NV>(h, row, K, p.out_type, p.rows, p.xq, p.xs, maxima);
-}
-
-// SiLU(g) * u = g u / (1 + exp(-g)) in 64 bits, rounded to fp32 once, to a
-// relative 2^-50 before that (so that it is the correctly rounded product but
-// for one value in some 2^25).  exp: -g = n ln 2 + r with ln 2 in two parts, a
-// degree-11 polynomial on |r| <= ln 2 / 2 (Chebyshev interpolation, relative
-// error 2^-55.7), 2^n by ldexp.  |g| is cut at 700, where the result is already
-// g u or, below 2^-149, a zero of its sign; the denominator stays finite.
-// The quotient: two Newton steps on the hardware reciprocal.
-// About 31 instructions against some 80 of the library's exp and division.
-__device__ __forceinline__ float gated(float g, float u) {
-    const double x = (double)-__builtin_amdgcn_fmed3f(g, -700.0f, 700.0f);
+// exp(x) - 1 = 2^n (p(r) - 1) + (2^n - 1) and its parts: x = n ln 2 + r with ln 2 in two
+// parts, p a polynomial of degree 11 on |r| <= ln 2 / 2 (Chebyshev interpolation,
+// relative error 2^-55.7).
+struct Exp {
+    double less_one, two_n;  // p(r) - 1, 2^n
+};
+__device__ __forceinline__ Exp exp_parts(double x) {
     const double n = __builtin_rint(x * 0x1.71547652b82fep+0);
     const double r = __builtin_fma(n, -0x1.a39ef35793c76p-33, __builtin_fma(n, -0x1.62e42fee00000p-1, x));
     double e = 0x1.af631d203b4edp-26;
@@ -271,69 +239,241 @@ __device__ __forceinline__ float gated(float g, float u) {
     e = __builtin_fma(e, r, 0x1.555555555555ap-3);
     e = __builtin_fma(e, r, 0x1.0000000000011p-1);
     e = __builtin_fma(e, r, 1.0);
-    e = __builtin_fma(e, r, 1.0);
-    const double d = 1.0 + __builtin_amdgcn_ldexp(e, (int)n), a = (double)g * (double)u;
+    return {e * r, __builtin_amdgcn_ldexp(1.0, (int)n)};
+}
+// 1 / d to a relative 2^-52: two Newton steps on the hardware reciprocal.
+__device__ __forceinline__ double reciprocal(double d) {
     double q = __builtin_amdgcn_rcp(d);
     q = __builtin_fma(q, __builtin_fma(-d, q, 1.0), q);
-    q = __builtin_fma(q, __builtin_fma(-d, q, 1.0), q);
-    return (float)(a * q);
+    return __builtin_fma(q, __builtin_fma(-d, q, 1.0), q);
 }
 
-template <int T, int NV>
-__global__ __launch_bounds__(T) void glu_act_kernel(const void *__restrict__ gate, int64_t ldg,
-                                                    const void *__restrict__ up, int64_t ldu, int K, int in_bf,
-                                                    int out_type, void *__restrict__ rows, int8_t *__restrict__ xq,
-                                                    float *__restrict__ xs) {
+// tanh(g) = (e^2g - 1) / (e^2g + 1) in 64 bits, rounded to fp32.
+__device__ __forceinline__ float tanh_rounded(float g) {
+    const Exp e = exp_parts(2.0 * (double)__builtin_amdgcn_fmed3f(g, -20.0f, 20.0f));
+    const double m = __builtin_fma(e.two_n, e.less_one, e.two_n - 1.0);
+    return __builtin_copysignf((float)(m * reciprocal(m + 2.0)), g);
+}
+
+// One workgroup per row.
+template <int T, int NV, bool kLayer>
+__global__ __launch_bounds__(T) void block_norm_kernel(const s3d8_block_norm_args p) {
+    __shared__ double sums[4][T / 64];
     __shared__ float maxima[T / 64];
     const int64_t row = blockIdx.x;
-    const int n4 = K >> 2;
-    float4 v[NV], u[NV];
-    load_row<T, NV>(v, gate, row * ldg, n4, in_bf);
-    load_row<T, NV>(u, up, row * ldu, n4, in_bf);
+    const int K = (int)p.K, n4 = K >> 2;
+    const int64_t base = row * K;
+    auto load = [&](float4 (&v)[NV], const void *x, bool bf) {
+        if (bf) {
+            Raw<true> r[NV];
+            load_row<T, NV, true>(r, x, base, n4);
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
-        if ((int)threadIdx.x + j * T < n4) v[j] = zip4(v[j], u[j], gated);
-    row_out<T, NV>(v, row, K, out_type, rows, xq, xs, maxima);
+            for (int j = 0; j < NV; ++j) v[j] = values(r[j]);
+        } else {
+            load_row<T, NV, false>(v, x, base, n4);
+        }
+    };
+    float4 h[NV];
+    load(h, p.h, p.h_type == S3D8_ROWS_BF16);
+    if (p.branch) {
+        float4 t[NV];
+        load(t, p.branch, p.branch_type == S3D8_ROWS_BF16);
+        if (p.post_weight) normalise<T, NV, kLayer>(t, K, p.eps, p.post_weight, p.post_bias, sums[0]);
+        if (p.gate) {
+            const bool one = !p.gate_channels, squash = p.gate_tanh;
+            const float g1 = one ? (squash ? tanh_rounded(*p.gate) : *p.gate) : 1.0f;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int i = threadIdx.x + j * T;
+                float4 g = make_float4(g1, g1, g1, g1);
+                if (!one && i < n4) {
+                    g = reinterpret_cast<const float4 *>(p.gate)[i];
+                    if (squash) g = map4(g, tanh_rounded);
+                }
+                t[j] = zip4(g, t[j], [](float x, float y) { return x * y; });
+            }
+        }
+        const float rs = p.residual_scale;
+        if (rs != 1.0f)
+#pragma unroll
+            for (int j = 0; j < NV; ++j) h[j] = map4(h[j], [&](float x) { return rs * x; });
+#pragma unroll
+        for (int j = 0; j < NV; ++j) h[j] = zip4(h[j], t[j], [](float x, float y) { return x + y; });
+        if (p.h_type == S3D8_ROWS_BF16) {
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int i = threadIdx.x + j * T;
+                const uint2 u = bf16x4(h[j]);
+                h[j] = bf16x4_values(u);  // the norm reads the residual as it is stored
+                if (i < n4) reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.h_out) + base)[i] = u;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int i = threadIdx.x + j * T;
+                if (i < n4) reinterpret_cast<float4 *>(static_cast<float *>(p.h_out) + base)[i] = h[j];
+            }
+        }
+    }
+    normalise<T, NV, kLayer>(h, K, p.eps, p.weight, p.bias, sums[2]);
+    row_out<T, NV>(h, row, K, p.out_type, p.rows, p.xq, p.xs, maxima);
+}
+
+// SiLU(g) * u = g u / (1 + exp(-g)) in 64 bits, rounded to fp32 once, to a
+// relative 2^-50 before that (so that it is the correctly rounded product but
+// for one value in some 2^25).  |g| is cut at 700, where the result is already
+// g u or, below 2^-149, a zero of its sign; the denominator stays finite.
+__device__ __forceinline__ float gated(float g, float u) {
+    const Exp e = exp_parts((double)-__builtin_amdgcn_fmed3f(g, -700.0f, 700.0f));
+    const double d = 1.0 + __builtin_fma(e.two_n, e.less_one, e.two_n);
+    return (float)((double)g * (double)u * reciprocal(d));
+}
+
+// The same in fp32, off by less than a relative 2^-20 while g >= -64 and g u is
+// neither infinite nor subnormal: exp2 and the reciprocal by at most an ulp
+// (2^-23) each, the exponent -g log2(e) in two parts by nothing that counts, and
+// five more roundings of 2^-24.
+__device__ __forceinline__ float gated_near(float g, float u) {
+    const float c = fminf(g, 200.0f);
+    const float h = c * -0x1.715476p+0f;
+    const float l = __builtin_fmaf(c, -0x1.4ae0c0p-26f, __builtin_fmaf(c, -0x1.715476p+0f, -h));
+    float e = __builtin_amdgcn_exp2f(h);
+    e = __builtin_fmaf(e, l * 0x1.62e430p-1f, e);
+    return g * u * __builtin_amdgcn_rcpf(1.0f + e);
+}
+
+// Codes and scale of a row, equal to what row_out makes of gated() of every element,
+// but with gated() (some 45 instructions) only where fp32 cannot tell:
+//   - the row's maximum is gated() of the elements whose gated_near() is
+//     within 2^-18 of the largest one (the true maximum's is within 2^-19);
+//   - t = near fl(1 / s) is off from x / s by less than 127 (2^-20 + 2^-22) < 2^-12.6,
+//     fl(x / s) by 127 2^-24: where t is further than 2^-12 from a border k + 1/2
+//     its nearest integer is the code (all but one value in 2^11).
+// Both kinds go through a list in LDS, so that the few of them take one pass of
+// the workgroup.  False where the row is outside gated_near()'s range or a list
+// overflows: nothing is then said about the row, whose codes may be partly
+// written.
+constexpr int kListed = 256;
+template <int T, int NV, bool kBF>
+__device__ __forceinline__ bool glu_codes(const Raw<kBF> (&g4)[NV], const Raw<kBF> (&u4)[NV], int64_t row, int K,
+                                          int8_t *xq, float *xs, float (*slots)[T / 64]) {
+    __shared__ int counts[2];
+    __shared__ int place[kListed];
+    __shared__ float4 gs[kListed], us[kListed];
+    const int n4 = K >> 2;
+    if (threadIdx.x < 2) counts[threadIdx.x] = 0;
+    float4 near[NV];
+    float lowest = 0.0f, most = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const float4 g = values(g4[j]);
+        near[j] = zip4(g, values(u4[j]), gated_near);
+        lowest = fminf(fminf(lowest, fminf(g.x, g.y)), fminf(g.z, g.w));
+        most = fmaxf(fmaxf(most, fmaxf(fabsf(near[j].x), fabsf(near[j].y))), fmaxf(fabsf(near[j].z), fabsf(near[j].w)));
+    }
+    const float top = block_max<T>(lowest < -64.0f ? INFINITY : most, slots[0]);
+    if (!(top >= 0x1p-100f && top < INFINITY)) return false;  // uniform
+    lds_barrier();  // (a workgroup of one wave has had none)
+    const float bar = top * (1.0f - 0x1p-18f);
+    auto list = [&](int j, int which) {
+        const int k = atomicAdd(&counts[which], 1);
+        if (k < kListed) {
+            place[k] = threadIdx.x + j * T;
+            gs[k] = values(g4[j]);
+            us[k] = values(u4[j]);
+        }
+    };
+    if (most >= bar) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            if (fmaxf(fmaxf(fabsf(near[j].x), fabsf(near[j].y)), fmaxf(fabsf(near[j].z), fabsf(near[j].w))) >= bar)
+                list(j, 0);
+    }
+    lds_barrier();
+    int listed = counts[0];
+    if (listed > kListed) return false;
+    float a = 0.0f;
+    const float *gl = reinterpret_cast<const float *>(gs), *ul = reinterpret_cast<const float *>(us);
+    for (int k = threadIdx.x; k < 4 * listed; k += T) a = fmaxf(a, fabsf(gated(gl[k], ul[k])));
+    a = block_max<T>(a, slots[1]);
+    lds_barrier();
+    const float s = a / 127.0f, rs = 1.0f / s;
+    if (threadIdx.x == 0) xs[row] = s;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int i = threadIdx.x + j * T;
+        float far = 0.0f;
+        const uint32_t q = codes4(near[j], rs, far);
+        if (far > 0.5f - 0x1p-12f)
+            list(j, 1);
+        else if (i < n4)
+            reinterpret_cast<uint32_t *>(xq + row * K)[i] = q;
+    }
+    lds_barrier();
+    listed = counts[1];
+    if (listed > kListed) return false;
+    for (int k = threadIdx.x; k < 4 * listed; k += T) {
+        const float x = fminf(127.0f, fmaxf(-127.0f, rintf(gated(gl[k], ul[k]) / s)));
+        const int at = 4 * place[k >> 2] + (k & 3);
+        if (at < K) xq[row * K + at] = (int8_t)x;
+    }
+    return true;
+}
+
+template <int T, int NV, bool kBF>
+__global__ __launch_bounds__(T) void glu_act_kernel(const void *__restrict__ gate, int64_t ldg,
+                                                    const void *__restrict__ up, int64_t ldu, int K, int out_type,
+                                                    void *__restrict__ rows, int8_t *__restrict__ xq,
+                                                    float *__restrict__ xs) {
+    __shared__ float maxima[3][T / 64];
+    const int64_t row = blockIdx.x;
+    const int n4 = K >> 2;
+    Raw<kBF> g4[NV], u4[NV];
+    load_row<T, NV, kBF>(g4, gate, row * ldg, n4);
+    load_row<T, NV, kBF>(u4, up, row * ldu, n4);
+    if (out_type == S3D8_ROWS_CODES && glu_codes<T, NV, kBF>(g4, u4, row, K, xq, xs, maxima)) return;
+    float4 v[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) v[j] = zip4(values(g4[j]), values(u4[j]), gated);
+    row_out<T, NV>(v, row, K, out_type, rows, xq, xs, maxima[2]);
 }
 
 // --------------------------------------------------------------- host
 
+// Kernels by workgroup and row width.
+template <bool kLayer>
 struct BlockNorm {
     template <int T, int NV>
-    static constexpr auto kernel() { return &block_norm_kernel<T, NV>; }
+    static constexpr auto kernel() { return &block_norm_kernel<T, NV, kLayer>; }
 };
+template <bool kBF>
 struct GluAct {
     template <int T, int NV>
-    static constexpr auto kernel() { return &glu_act_kernel<T, NV>; }
+    static constexpr auto kernel() { return &glu_act_kernel<T, NV, kBF>; }
 };
 
-template <class Op, int T>
-auto row_kernel_of(int64_t nv) {
-    switch (nv) {
-        case 1: return Op::template kernel<T, 1>();
-        case 2: return Op::template kernel<T, 2>();
-        case 3: return Op::template kernel<T, 3>();
-        case 4: return Op::template kernel<T, 4>();
-        case 5: return Op::template kernel<T, 5>();
-        case 6: return Op::template kernel<T, 6>();
-        case 7: return Op::template kernel<T, 7>();
-        default: return Op::template kernel<T, 8>();
-    }
-}
-
 // The workgroup of a row: where there are rows for every CU, the fewest threads
-// that hold it in 8 float4 each (few waves to join, many rows on a CU); else as
-// many as it has float4 (short chains).
+// that hold it in `most` float4 each (few waves to join, several rows on a CU at
+// once); else as many as it has float4 (short chains).
 template <class Op>
-auto row_kernel(int64_t M, int64_t K, int cus, int &threads) {
+auto row_kernel(int64_t M, int64_t K, int cus, int most, int &threads) {
     const int64_t n4 = K / 4;
-    auto nv = [&](int t) { return (n4 + t - 1) / t; };
-    const int64_t most = M >= 2 * cus ? 8 : 1;
-    if (nv(64) <= most) return threads = 64, row_kernel_of<Op, 64>(nv(64));
-    if (nv(256) <= most) return threads = 256, row_kernel_of<Op, 256>(nv(256));
-    if (nv(512) <= most) return threads = 512, row_kernel_of<Op, 512>(nv(512));
     threads = 1024;
-    return nv(1024) <= 8 ? row_kernel_of<Op, 1024>(nv(1024)) : Op::template kernel<1024, 16>();
+    for (int t : {512, 256, 64})
+        if (n4 <= t * (M >= 2 * cus ? most : 1)) threads = t;
+    const int64_t nv = (n4 + threads - 1) / threads;
+    auto pick = [&](auto t) {
+        constexpr int T = decltype(t)::value;
+        return nv <= 1   ? Op::template kernel<T, 1>()
+               : nv <= 2 ? Op::template kernel<T, 2>()
+               : nv <= 4 ? Op::template kernel<T, 4>()
+               : nv <= 5 ? Op::template kernel<T, 5>()
+                         : Op::template kernel<T, 7>();
+    };
+    if (threads == 64) return pick(std::integral_constant<int, 64>());
+    if (threads == 256) return pick(std::integral_constant<int, 256>());
+    if (threads == 512) return pick(std::integral_constant<int, 512>());
+    return nv > 7 ? Op::template kernel<1024, 16>() : pick(std::integral_constant<int, 1024>());
 }
 
 bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -391,7 +531,8 @@ int32_t s3d8_block_norm(const s3d8_block_norm_args *args, void *stream) {
     rc = s3d8::check_device(&cus);
     if (rc) return rc;
     int threads = 0;
-    const auto fn = row_kernel<BlockNorm>(a.M, a.K, cus, threads);
+    const auto fn = a.kind == S3D8_NORM_LAYER ? row_kernel<BlockNorm<true>>(a.M, a.K, cus, 7, threads)
+                                              : row_kernel<BlockNorm<false>>(a.M, a.K, cus, 7, threads);
     hipLaunchKernelGGL(fn, dim3((unsigned)a.M), dim3(threads), 0, (hipStream_t)stream, a);
     return s3d8::launch_status();
 }
@@ -414,9 +555,10 @@ int32_t s3d8_glu_act(const void *gate, int64_t ld_gate, const void *up, int64_t 
     rc = s3d8::check_device(&cus);
     if (rc) return rc;
     int threads = 0;
-    const auto fn = row_kernel<GluAct>(M, K, cus, threads);
+    const auto fn = in_type == S3D8_ROWS_BF16 ? row_kernel<GluAct<true>>(M, K, cus, 7, threads)
+                                              : row_kernel<GluAct<false>>(M, K, cus, 7, threads);
     hipLaunchKernelGGL(fn, dim3((unsigned)M), dim3(threads), 0, (hipStream_t)stream, gate, ld_gate, up, ld_up,
-                       (int)K, (int)(in_type == S3D8_ROWS_BF16), out_type, rows, xq, xs);
+                       (int)K, out_type, rows, xq, xs);
     return s3d8::launch_status();
 }
 
