@@ -483,6 +483,7 @@ int32_t s3d8_w4_tile(const uint8_t *packed, const uint16_t *scales_bf16, const u
  *   group, has_zeros   as the matrix was laid out.
  *   y            out, device [M][N] of fp32 or bf16 (per out_type).
  *   out_type     S3D8_OUT_F32 or S3D8_OUT_BF16.
+ * At most 524288 rows, and 4194303 channels when M > 16.
  * Errors: INVALID_ARG (also tiled_bytes), SHAPE, ALIGN, DEVICE, HIP. */
 int32_t s3d8_w4_linear(const int8_t *xq, const float *xs, int64_t M, int64_t K, int64_t N, const uint8_t *tiled,
                        int64_t tiled_bytes, int64_t group, int32_t has_zeros, void *y, int32_t out_type, void *stream);
@@ -543,7 +544,7 @@ typedef struct s3d8_block_norm_args {
  * The sums, mu and r are computed in 64 bits and then rounded to fp32; every
  * other operation is one IEEE fp32 operation.  (The codes are whole numbers:
  * sums in 64 bits keep them from depending on the order of summation.)
- * K is a positive multiple of 16, at most 65536.  Row matrices must be 16-B
+ * K is a positive multiple of 16, at most 65536; at most 524288 rows.  Row matrices must be 16-B
  * aligned, fp32 vectors [K] as well; values finite, eps > 0.  Outputs other
  * than h_out = h must not overlap inputs.
  * Errors: INVALID_ARG, SHAPE, ALIGN, DEVICE, HIP. */
@@ -560,7 +561,7 @@ int32_t s3d8_block_norm(const s3d8_block_norm_args *args, void *stream);
  *                elements.
  *   rows         out, device [M][K] for out_type F32 or BF16, 16-B aligned, else NULL.
  *   xq, xs       out, int8 [M][K] (16-B aligned) and fp32 [M] for CODES, else NULL.
- * K is a positive multiple of 16, at most 65536.
+ * K is a positive multiple of 16, at most 65536; at most 524288 rows.
  * Errors: INVALID_ARG, SHAPE, ALIGN, DEVICE, HIP. */
 int32_t s3d8_glu_act(const void *gate, int64_t ld_gate, const void *up, int64_t ld_up, int64_t M, int64_t K,
                      int32_t in_type, int32_t out_type, void *rows, int8_t *xq, float *xs, void *stream);

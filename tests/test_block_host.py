@@ -114,6 +114,7 @@ def test_linear_refusals(entry):
     assert call(o=2) == INVALID and call(z=2, tb=1) == INVALID
     assert call(K=120) == SHAPE and call(g=48) == SHAPE
     assert call(M=(1 << 19) + 1) == SHAPE and call(M=1 << 40) == SHAPE and call(N=1 << 40) == SHAPE
+    assert call(M=17, K=16, N=1 << 22) == SHAPE
     assert call(M=1 << 19, K=1 << 13) == SHAPE and call(M=1 << 18, N=1 << 13) == SHAPE
     # laid out for other arguments
     assert call(tb=16 * 64) == INVALID

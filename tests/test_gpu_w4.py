@@ -83,11 +83,12 @@ def test_larger_shapes(gpu, M, N, K, group, zeros, out):
     run(gpu, M, N, K, group, zeros, out)
 
 
-# each workgroup tile of the many-row kernel (128 x 256, 64 x 256, 64 x 128, 64 x 64,
-# 32 x 128, 64 x 32 rows x channels), with 1, 2 and 4 scales per 128 columns
+# each workgroup tile of the many-row kernel (128 x 256, also with a last round in
+# halves, 64 x 256, 64 x 128, 64 x 64, 32 x 128, 32 x 64 rows x channels), with 1, 2
+# and 4 scales per 128 columns
 @pytest.mark.parametrize("group,zeros", [(128, False), (64, False), (32, False), (128, True), (64, True), (32, True)])
-@pytest.mark.parametrize("M,N,K", [(2000, 7000, 400), (520, 7000, 656), (120, 14330, 1040), (50, 16000, 912),
-                                   (30, 14330, 592), (40, 1000, 1296)])
+@pytest.mark.parametrize("M,N,K", [(2000, 7000, 400), (1601, 5120, 272), (520, 7000, 656), (120, 14330, 1040), (50, 16000, 912),
+                                   (30, 30000, 592), (40, 1000, 1296)])
 def test_workgroup_tiles(gpu, M, N, K, group, zeros):
     run(gpu, M, N, K, group, zeros, "bf16" if zeros else "f32")
 

@@ -115,6 +115,12 @@ constexpr int kXcds = 8;
 // With the input columns split into `splits` ranges, the range index ks is
 // the slowest: an XCD's workgroups then share a k range as well.
 constexpr int kGroupM = 8;
+__device__ __forceinline__ void gemm_tile_at(int L, int nbm, int nbn, int &bm, int &bn) {
+    const int group = L / (kGroupM * nbn), r = L - group * (kGroupM * nbn);
+    const int gm = min(kGroupM, nbm - group * kGroupM);
+    bm = group * kGroupM + r % gm;
+    bn = r / gm;
+}
 __device__ __forceinline__ bool gemm_tile(int nbm, int nbn, int splits, int &bm, int &bn, int &ks) {
     const int nt = nbm * nbn;
     const int nwg = nt * splits;
@@ -122,11 +128,7 @@ __device__ __forceinline__ bool gemm_tile(int nbm, int nbn, int splits, int &bm,
     const int L0 = (int)(blockIdx.x % kXcds) * per_xcd + (int)(blockIdx.x / kXcds);
     if (L0 >= nwg) return false;
     ks = L0 / nt;
-    const int L = L0 - ks * nt;
-    const int group = L / (kGroupM * nbn), r = L - group * (kGroupM * nbn);
-    const int gm = min(kGroupM, nbm - group * kGroupM);
-    bm = group * kGroupM + r % gm;
-    bn = r / gm;
+    gemm_tile_at(L0 - ks * nt, nbm, nbn, bm, bn);
     return true;
 }
 __device__ __forceinline__ bool gemm_tile(int nbm, int nbn, int &bm, int &bn) {

@@ -114,30 +114,29 @@ __device__ __forceinline__ int32_t nibbles(uint32_t w, int h, uint32_t zrep) {
 
 // --------------------------------------------------------------- product, few rows
 
-// Token rows 16 R at a time against NT tiles of 16 channels, the columns split
-// over the waves.  A workgroup's W waves form W / KS teams; a team takes a
-// group of NT tiles at a time, its KS waves every KS-th block of 128 columns.
-// Both operands go straight from memory to registers in operand order (lane
-// L = n + 16 g: B column n; A row n, 16-byte piece g), kDepth blocks ahead;
-// nothing passes through LDS but the waves' partial sums, which a team adds in
-// wave order.
+// Up to 16 token rows: one read of the weights.  A workgroup's 16 waves form
+// 16 / KS teams; a team takes a group of NT tiles of 16 channels at a time, its KS
+// waves every KS-th block of 128 columns.  Both operands go straight from memory to
+// registers in operand order (lane L = n + 16 g: B column n; A row n, 16-byte
+// piece g), kDepth blocks ahead; nothing passes through LDS but the waves'
+// partial sums, which a team adds in wave order.
 //
-// A row r of a row tile is token 4 (r % 4) + r / 4, so that result register i
-// of lane group g belongs to token 4 i + g: with up to 4 tokens only register
-// 0 of every result is converted and scaled, with up to 8 two (Q registers).
-template <int R, int NT, int Q, int P, bool kZeros, int W>
-__global__ __launch_bounds__(W * 64) void w4_rows_kernel(const int8_t *__restrict__ xq, const float *__restrict__ xs,
-                                                         const uint8_t *__restrict__ tiled, int M, int K, int N,
-                                                         int KS, int rounds, int wgs, void *__restrict__ y, int obf) {
-    constexpr int kDepth = 2;
-    __shared__ float red[W * NT * R * Q * 64];
+// A row r is token 4 (r % 4) + r / 4, so that result register i of lane group g
+// belongs to token 4 i + g: with up to 4 tokens only register 0 of every result is
+// converted and scaled, with up to 8 two (Q registers).
+constexpr int kRowWaves = 16;
+
+template <int NT, int Q, int P, bool kZeros>
+__global__ __launch_bounds__(kRowWaves * 64) void w4_rows_kernel(
+    const int8_t *__restrict__ xq, const uint8_t *__restrict__ tiled, int M, int K, int N, int KS, int rounds, int wgs,
+    const float *__restrict__ xs, void *__restrict__ y, int obf) {
+    constexpr int kDepth = 2;  // (three and four measured 1 to 8% slower)
+    __shared__ float red[kRowWaves * NT * Q * 64];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int n = lane & 15, g = lane >> 4;
     const int KB = (K + kBlk - 1) / kBlk, tiles = (N + 15) >> 4;
-    const int teams = W / KS, team = wave / KS, part = wave - team * KS;
-    const int bm = (int)blockIdx.x / wgs, bc = (int)blockIdx.x - bm * wgs;  // row tile, place among its wgs workgroups
-    const int m0 = bm * 16 * R;
+    const int teams = kRowWaves / KS, team = wave / KS, part = wave - team * KS;
     const uint32_t frags = (uint32_t)tiles * (uint32_t)KB;
     const auto rx = make_rsrc(xq, (uint32_t)M * (uint32_t)K);
     const auto rw = make_rsrc(tiled, frags * 1024u);
@@ -147,37 +146,32 @@ __global__ __launch_bounds__(W * 64) void w4_rows_kernel(const int8_t *__restric
     struct Stage {
         uint4 w[NT];
         uint32_t s[NT][P == 4 ? 2 : 1], z[NT];
-        uint4 a[R][2];
+        uint4 a[2];
     };
-    const int steps_tile = (KB - part + KS - 1) / KS;  // this wave's blocks of a tile group
-    int group = bc * teams + team;        // of the next step to load
+    const int mine = (KB - part + KS - 1) / KS;     // this wave's blocks of a tile group
+    int group = (int)blockIdx.x * teams + team;
     const int stride = wgs * teams;
-    uint32_t arow[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const int tok = m0 + 16 * r + 4 * (n & 3) + (n >> 2);
-        arow[r] = tok < M ? (uint32_t)tok * (uint32_t)K : kOOB;
-    }
+    const int token = 4 * (n & 3) + (n >> 2);
+    const uint32_t arow = token < M ? (uint32_t)token * (uint32_t)K : kOOB;
     auto load = [&](Stage &st, int grp, int step) {
         const int kb = part + KS * step;
-        const bool live = step < steps_tile;
+        const bool live = step < mine;
+        const uint32_t alive = live ? arow : kOOB;
 #pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if constexpr (P == 4) {
-                    // the columns of byte halves 0..7 and 8..15 of the fragment's lane
-                    const int k = kb * kBlk + 64 * h + 8 * g;
-                    const uint32_t o0 = live && arow[r] != kOOB && k < K ? arow[r] + (uint32_t)k : kOOB;
-                    const uint32_t o1 = live && arow[r] != kOOB && k + 32 < K ? arow[r] + (uint32_t)k + 32u : kOOB;
-                    const auto lo = __builtin_amdgcn_raw_buffer_load_b64(rx, o0, 0, 0);
-                    const auto hi = __builtin_amdgcn_raw_buffer_load_b64(rx, o1, 0, 0);
-                    st.a[r][h] = make_uint4(lo[0], lo[1], hi[0], hi[1]);
-                } else {
-                    const int k = kb * kBlk + 64 * h + 16 * g;
-                    st.a[r][h] = bload16(rx, live && arow[r] != kOOB && k < K ? arow[r] + (uint32_t)k : kOOB);
-                }
+        for (int h = 0; h < 2; ++h) {
+            if constexpr (P == 4) {
+                // the columns of byte halves 0..7 and 8..15 of the fragment's lane
+                const int k = kb * kBlk + 64 * h + 8 * g;
+                const auto lo = __builtin_amdgcn_raw_buffer_load_b64(
+                    rx, alive != kOOB && k < K ? alive + (uint32_t)k : kOOB, 0, 0);
+                const auto hi = __builtin_amdgcn_raw_buffer_load_b64(
+                    rx, alive != kOOB && k + 32 < K ? alive + (uint32_t)k + 32u : kOOB, 0, 0);
+                st.a[h] = make_uint4(lo[0], lo[1], hi[0], hi[1]);
+            } else {
+                const int k = kb * kBlk + 64 * h + 16 * g;
+                st.a[h] = bload16(rx, alive != kOOB && k < K ? alive + (uint32_t)k : kOOB);
             }
+        }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             const int tile = grp * NT + t;
@@ -185,11 +179,9 @@ __global__ __launch_bounds__(W * 64) void w4_rows_kernel(const int8_t *__restric
             const bool ok = live && tile < tiles;
             st.w[t] = bload16(rw, ok ? f * 1024u + 16u * (uint32_t)lane : kOOB);
             const uint32_t so = ok ? (f * 16u + (uint32_t)n) * (2u * P) : kOOB;
-            if constexpr (P == 1) {
-                st.s[t][0] = __builtin_amdgcn_raw_buffer_load_b16(rs, so, 0, 0);
-            } else if constexpr (P == 2) {
-                st.s[t][0] = __builtin_amdgcn_raw_buffer_load_b32(rs, so, 0, 0);
-            } else {
+            if constexpr (P == 1) st.s[t][0] = __builtin_amdgcn_raw_buffer_load_b16(rs, so, 0, 0);
+            if constexpr (P == 2) st.s[t][0] = __builtin_amdgcn_raw_buffer_load_b32(rs, so, 0, 0);
+            if constexpr (P == 4) {
                 const auto v = __builtin_amdgcn_raw_buffer_load_b64(rs, so, 0, 0);
                 st.s[t][0] = v[0];
                 st.s[t][1] = v[1];
@@ -202,55 +194,49 @@ __global__ __launch_bounds__(W * 64) void w4_rows_kernel(const int8_t *__restric
             }
         }
     };
-    float sum[NT][R][Q];
+    float sum[NT][Q];
     auto consume = [&](const Stage &st) {
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             const uint32_t wv[4] = {st.w[t].x, st.w[t].y, st.w[t].z, st.w[t].w};
-            v4i acc[R];
+            auto add = [&](const v4i &c, uint32_t sbits) {
+                const float s = __uint_as_float(sbits << 16);
+#pragma unroll
+                for (int i = 0; i < Q; ++i) sum[t][i] = __builtin_fmaf(s, (float)c[i], sum[t][i]);
+            };
+            const v4i zero = {0, 0, 0, 0};
+            v4i acc;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 v4i b;
 #pragma unroll
                 for (int d = 0; d < 4; ++d) {
                     const int p = P == 1 ? 0 : P == 2 ? h : 2 * h + (d >> 1);
-                    const uint32_t zrep = kZeros ? ((st.z[t] >> (8 * p)) & 0xFFu) * 0x01010101u : 0u;
-                    b[d] = nibbles<kZeros>(wv[d], h, zrep);
+                    b[d] = nibbles<kZeros>(wv[d], h, kZeros ? ((st.z[t] >> (8 * p)) & 0xFFu) * 0x01010101u : 0u);
                 }
-                auto add = [&](const v4i &c, int r, uint32_t sbits) {
-                    const float s = __uint_as_float(sbits << 16);
-#pragma unroll
-                    for (int i = 0; i < Q; ++i) sum[t][r][i] = __builtin_fmaf(s, (float)c[i], sum[t][r][i]);
-                };
-#pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    const uint4 av = st.a[r][h];
-                    const v4i a = {(int)av.x, (int)av.y, (int)av.z, (int)av.w}, zero = {0, 0, 0, 0};
-                    if constexpr (P == 4) {
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const long al = (long)((uint64_t)(uint32_t)a[2 * e] | (uint64_t)(uint32_t)a[2 * e + 1] << 32);
-                            const long bl = (long)((uint64_t)(uint32_t)b[2 * e] | (uint64_t)(uint32_t)b[2 * e + 1] << 32);
-                            const v4i c = __builtin_amdgcn_mfma_i32_16x16x32_i8(al, bl, zero, 0, 0, 0);
-                            add(c, r, e ? st.s[t][h] >> 16 : st.s[t][h]);
-                        }
-                    } else if constexpr (P == 2) {
-                        const v4i c = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, zero, 0, 0, 0);
-                        add(c, r, h ? st.s[t][0] >> 16 : st.s[t][0]);
-                    } else {
-                        acc[r] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, h ? acc[r] : zero, 0, 0, 0);
-                        if (h) add(acc[r], r, st.s[t][0]);
-                    }
+                const uint4 av = st.a[h];
+                const v4i a = {(int)av.x, (int)av.y, (int)av.z, (int)av.w};
+                if constexpr (P == 4) {
+                    auto two = [](const v4i &v, int e) {
+                        return (long)((uint64_t)(uint32_t)v[e] | (uint64_t)(uint32_t)v[e + 1] << 32);
+                    };
+                    add(__builtin_amdgcn_mfma_i32_16x16x32_i8(two(a, 0), two(b, 0), zero, 0, 0, 0), st.s[t][h]);
+                    add(__builtin_amdgcn_mfma_i32_16x16x32_i8(two(a, 2), two(b, 2), zero, 0, 0, 0), st.s[t][h] >> 16);
+                } else if constexpr (P == 2) {
+                    add(__builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, zero, 0, 0, 0), h ? st.s[t][0] >> 16 : st.s[t][0]);
+                } else {
+                    acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, h ? acc : zero, 0, 0, 0);
+                    if (h) add(acc, st.s[t][0]);
                 }
             }
         }
     };
 
     Stage ring[kDepth];
-    // (group, step) of the next load; every wave of a team loads and consumes
-    // in the same order, blocks past its share are predicated off
+    // (group, step) of the next load; every wave takes steps_max steps per group, so
+    // that barriers line up (blocks past its share are predicated off)
+    const int steps_max = (KB + KS - 1) / KS;
     int ld_group = group, ld_step = 0;
-    const int steps_max = (KB + KS - 1) / KS;  // of any wave, so that barriers line up
     auto load_next = [&](Stage &st) {
         load(st, ld_group, ld_step);
         if (++ld_step == steps_max) {
@@ -266,9 +252,7 @@ __global__ __launch_bounds__(W * 64) void w4_rows_kernel(const int8_t *__restric
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int r = 0; r < R; ++r)
-#pragma unroll
-                for (int i = 0; i < Q; ++i) sum[t][r][i] = 0.0f;
+            for (int i = 0; i < Q; ++i) sum[t][i] = 0.0f;
     };
     clear();
     int step = 0;
@@ -283,24 +267,20 @@ __global__ __launch_bounds__(W * 64) void w4_rows_kernel(const int8_t *__restric
             if (++step < steps_max) continue;
             // the team's partial sums of this tile group, added in wave order
             step = 0;
-            float *mine = red + wave * (NT * R * Q * 64);
+            float *own = red + wave * (NT * Q * 64);
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int r = 0; r < R; ++r)
-#pragma unroll
-                    for (int i = 0; i < Q; ++i) mine[((t * R + r) * Q + i) * 64 + lane] = sum[t][r][i];
+                for (int i = 0; i < Q; ++i) own[(t * Q + i) * 64 + lane] = sum[t][i];
             clear();
             asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-            const float *from = red + team * KS * (NT * R * Q * 64);
-            for (int o = part * 64 + lane; o < NT * R * Q * 64; o += KS * 64) {
-                // o = ((r Q + i) 4 + g') (16 NT) + channel
-                const int ch = o % (16 * NT), tk = o / (16 * NT);
-                const int gg = tk & 3, ri = tk >> 2, i = ri % Q, r = ri / Q;
-                const int m = m0 + 16 * r + 4 * i + gg, c = group * (16 * NT) + ch;
-                const float *at = from + (((ch >> 4) * R + r) * Q + i) * 64 + (ch & 15) + 16 * gg;
+            const float *from = red + team * KS * (NT * Q * 64);
+            for (int o = part * 64 + lane; o < NT * Q * 64; o += KS * 64) {
+                // o = token (16 NT) + channel, token 4 i + g'
+                const int ch = o % (16 * NT), m = o / (16 * NT), c = group * (16 * NT) + ch;
+                const float *at = from + ((ch >> 4) * Q + (m >> 2)) * 64 + (ch & 15) + 16 * (m & 3);
                 float v = 0.0f;
-                for (int w = 0; w < KS; ++w) v += at[w * (NT * R * Q * 64)];
+                for (int w = 0; w < KS; ++w) v += at[w * (NT * Q * 64)];
                 if (m < M && c < N) {
                     v = xs[m] * (v * post);
                     if (obf)
@@ -317,37 +297,57 @@ __global__ __launch_bounds__(W * 64) void w4_rows_kernel(const int8_t *__restric
 
 // --------------------------------------------------------------- product, many rows
 
-// Workgroup tile of 16 TR WR token rows x 16 TC (8 / WR) channels on eight
-// waves, each with TR x TC results of 16 x 16.  Everything a block of 128
-// columns needs is copied to LDS by LDS-DMA, S - 1 blocks ahead: the
-// activations, shared by the waves and stored in A operand order (every operand
-// read is contiguous, no bank conflicts), and each wave's own fragments,
-// scales and zero points.  (With the fragments loaded into registers instead,
-// the compiler's waits for them count only the loads it knows and so also wait
-// for younger activation copies.)
-template <int TR, int TC, int WR, int KP, int S, int P, bool kZeros>
-__global__ __launch_bounds__(512, TR * TC <= 16 ? 4 : 2) void w4_gemm_kernel(
-    const int8_t *__restrict__ xq, const uint8_t *__restrict__ tiled, int M, int K, int N, int nbm, int nbn,
-    const float *__restrict__ xs, void *__restrict__ y, int obf) {
-    constexpr int WP = 8 / KP;                     // waves of a column range
-    constexpr int BM = 16 * TR * WR, WC = WP / WR, BN = 16 * TC * WC;
-    constexpr int NA = BM / 8 / WP;                // activation loads (1 KiB) per wave and block
-    constexpr int NL = NA + TC + (kZeros ? 2 : 1);  // all loads per wave and block
+// Workgroup tile of 32 TR token rows on eight waves, each with TR results of 32 x 32
+// on v_mfma_i32_32x32x32_i8.  The waves form KP column ranges (range q takes blocks
+// q, q + KP, ...) of 8 / KP waves, which side by side cover 32 (8 / KP) channels;
+// the ranges' sums meet in LDS at the end, in their order.
+//
+// Everything a block of 128 columns needs is copied to LDS by LDS-DMA, S - 1
+// blocks ahead: the activations, shared by the waves of a range and stored in
+// 16-byte chunks by row, and each wave's own fragments, scales and zero points.
+// (With the fragments loaded into registers instead, the compiler's waits for
+// them count only the loads it knows and so also wait for younger activation
+// copies.)
+//
+// What bounds it is issue: every group of every result costs a conversion and a
+// multiply-add (2 P per result and block of 128) beside the product itself.
+// The 32 x 32 products take half the issue slots of 16 x 16 ones per
+// multiplication, and their K = 32 serves 32-column groups at full rate.
+//
+// K order.  Product operands hold 16 consecutive columns in lane half h of a row
+// or channel.  With P = 1 or 2 those are chunk 2 h + s of a 64-column half
+// (s = 0, 1: two products a half), the low or high nibbles of piece 2 h + s of
+// the fragment; with P = 4, chunk h of a 32-column group, the halves of pieces
+// 2 h and 2 h + 1.
+typedef int32_t v16i __attribute__((ext_vector_type(16)));
+
+template <int KP, int S, bool kZeros, int kARows>
+struct GemmLds {
+    static constexpr int kActs = KP * S * kARows * kBlk, kSums = KP > 1 ? 8 * kARows * 128 : 0;
+    // activations; the ranges' partial sums after the last block
+    __attribute__((aligned(16))) int8_t a[kActs > kSums ? kActs : kSums];
+    __attribute__((aligned(16))) uint8_t w[S][8][2048];
+    __attribute__((aligned(16))) uint8_t s[S][8][256], z[kZeros ? S : 1][8][256];
+};
+
+// One tile of 32 TR rows from row0, channels from 32 (8 / KP) bn; kARows >= 32 TR: what
+// the LDS has room for.
+template <int TR, int KP, int S, int P, bool kZeros, int kARows>
+__device__ __forceinline__ void w4_gemm_tile(GemmLds<KP, S, kZeros, kARows> &lds, const int8_t *__restrict__ xq,
+                                             const uint8_t *__restrict__ tiled, int M, int K, int N, int row0, int bn,
+                                             const float *__restrict__ xs, void *__restrict__ y, int obf) {
+    constexpr int WP = 8 / KP;                   // waves of a column range
+    constexpr int BM = 32 * TR;
+    constexpr int NA = BM / 8 / WP;              // activation loads (1 KiB) per wave and block
+    constexpr int NL = NA + (kZeros ? 4 : 3);    // all loads per wave and block
     static_assert(BM / 8 % WP == 0, "the waves of a range share its activation loads evenly");
-    static_assert(TC * 8 * P <= 64, "a wave's scales of a block are one load of 4 bytes per lane");
-    constexpr int kRangeBytes = BM * kBlk, kLds = KP * S * kRangeBytes;
-    constexpr int kSumBytes = KP > 1 ? 8 * TR * TC * 1024 : 0;  // partial sums, after the last block
-    __shared__ __attribute__((aligned(16))) int8_t abuf[kLds > kSumBytes ? kLds : kSumBytes];
-    __shared__ __attribute__((aligned(16))) uint8_t wbuf[S][8][TC * 1024];
-    __shared__ __attribute__((aligned(16))) uint8_t sbuf[S][8][256], zbuf[kZeros ? S : 1][8][256];
+    constexpr int kRangeBytes = BM * kBlk;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int n = lane & 15, g = lane >> 4;
+    const int n = lane & 31, h = lane >> 5;
     const int KB = (K + kBlk - 1) / kBlk, tiles = (N + 15) >> 4;
-    int bm, bn;
-    if (!gemm_tile(nbm, nbn, bm, bn)) return;  // padding workgroup
     const int part = wave / WP, pw = wave - part * WP;  // column range, wave of it
-    const int row0 = bm * BM, wr = pw / WC, tile0 = bn * (BN / 16) + (pw - wr * WC) * TC;
+    const int tile0 = 2 * (bn * WP + pw);
     const int steps = (KB + KP - 1) / KP;
 
     const uint32_t frags = (uint32_t)tiles * (uint32_t)KB;
@@ -356,28 +356,27 @@ __global__ __launch_bounds__(512, TR * TC <= 16 ? 4 : 2) void w4_gemm_kernel(
     const v4i rs = rsrc_words(tiled + (int64_t)frags * 1024, frags * (32u * P));
     const v4i rz = rsrc_words(tiled + (int64_t)frags * (1024 + 32 * P), kZeros ? frags * (16u * P) : 0u);
 
-    // activation load L = pw + WP j: rows 16 (L / 2) .., columns 64 (L % 2) ..
-    // of a block, chunk g of row n at 16 lane of KiB L
+    // activation load L = pw + WP j: rows 16 (L / 2) .., columns 64 (L % 2) .. of a
+    // block; lane l moves 16-byte chunk l / 16 of row l % 16 to 16 l of KiB L
     uint32_t aoff[NA], atail[NA];
 #pragma unroll
     for (int j = 0; j < NA; ++j) {
-        const int L = pw + WP * j, row = row0 + 16 * (L >> 1) + n, col = 64 * (L & 1) + 16 * g;
+        const int L = pw + WP * j, row = row0 + 16 * (L >> 1) + (lane & 15), col = 64 * (L & 1) + 16 * (lane >> 4);
         aoff[j] = row < M ? (uint32_t)row * (uint32_t)K + (uint32_t)col : kOOB;
         atail[j] = (KB - 1) * kBlk + col < K ? aoff[j] : kOOB;
     }
-    // scale load: dword `lane` of the wave's TC tiles of 8 P dwords; zero
-    // points: of 4 P dwords.  (A tile past the last one re-reads that one: its
-    // channels are not stored.)
+    // scale load: dword `lane` of the wave's two tiles of 8 P dwords; zero points:
+    // of 4 P dwords.  (A tile past the last one re-reads that one: its channels
+    // are not stored.)
     auto first = [&](int t) { return (uint32_t)min(tile0 + t, tiles - 1) * (uint32_t)KB; };
-    const uint32_t st = (uint32_t)lane / (8 * P), zt = (uint32_t)lane / (4 * P);
-    const uint32_t soff = st < TC ? first(st) * (32u * P) + 4u * (lane % (8 * P)) : kOOB;
-    const uint32_t zoff = zt < TC ? first(zt) * (16u * P) + 4u * (lane % (4 * P)) : kOOB;
-    uint32_t wfirst[TC];
-#pragma unroll
-    for (int t = 0; t < TC; ++t) wfirst[t] = __builtin_amdgcn_readfirstlane(first(t) * 1024u);
-    const uint32_t alds = S3D8_LDS_OFFSET(&abuf[0]) + (uint32_t)(kRangeBytes * part) + 1024u * (uint32_t)pw;
-    const uint32_t wlds = S3D8_LDS_OFFSET(&wbuf[0][wave][0]);
-    const uint32_t slds = S3D8_LDS_OFFSET(&sbuf[0][wave][0]), zlds = S3D8_LDS_OFFSET(&zbuf[0][wave][0]);
+    const int st = lane / (8 * P), zt = lane / (4 * P);
+    const uint32_t soff = st < 2 ? first(st) * (32u * P) + 4u * (lane % (8 * P)) : kOOB;
+    const uint32_t zoff = zt < 2 ? first(zt) * (16u * P) + 4u * (lane % (4 * P)) : kOOB;
+    const uint32_t wfirst[2] = {(uint32_t)__builtin_amdgcn_readfirstlane(first(0) * 1024u),
+                                (uint32_t)__builtin_amdgcn_readfirstlane(first(1) * 1024u)};
+    const uint32_t alds = S3D8_LDS_OFFSET(&lds.a[0]) + (uint32_t)(kRangeBytes * part) + 1024u * (uint32_t)pw;
+    const uint32_t wlds = S3D8_LDS_OFFSET(&lds.w[0][wave][0]);
+    const uint32_t slds = S3D8_LDS_OFFSET(&lds.s[0][wave][0]), zlds = S3D8_LDS_OFFSET(&lds.z[0][wave][0]);
     // step i of column range `part` is block part + KP i.  Past the last block
     // the activations are zeros and the weights those of the last one, so
     // that every wait counts the same and every range takes as many steps.
@@ -389,24 +388,17 @@ __global__ __launch_bounds__(512, TR * TC <= 16 ? 4 : 2) void w4_gemm_kernel(
             load_to_lds16_so(alds + (uint32_t)(KP * kRangeBytes) * slot + (uint32_t)(WP * 1024) * j,
                              kb < KB - 1 ? aoff[j] : kb == KB - 1 ? atail[j] : kOOB, kbc * kBlk, rx);
 #pragma unroll
-        for (int t = 0; t < TC; ++t)
-            load_to_lds16_so(wlds + (8u * TC * 1024u) * slot + 1024u * t, 16u * lane, wfirst[t] + kbc * 1024u, rw);
+        for (int t = 0; t < 2; ++t)
+            load_to_lds16_so(wlds + 16384u * slot + 1024u * t, 16u * lane, wfirst[t] + kbc * 1024u, rw);
         load_to_lds4_so(slds + 2048u * slot, soff, kbc * (32u * P), rs);
         if constexpr (kZeros) load_to_lds4_so(zlds + 2048u * slot, zoff, kbc * (16u * P), rz);
     };
 
-    float4 sum[TR][TC];
+    float sum[TR][16];
 #pragma unroll
     for (int r = 0; r < TR; ++r)
 #pragma unroll
-        for (int t = 0; t < TC; ++t) sum[r][t] = make_float4(0, 0, 0, 0);
-    typedef int32_t v2i __attribute__((ext_vector_type(2)));
-    auto add = [&](float4 &o, const v4i &c, float s) {
-        o.x = __builtin_fmaf(s, (float)c[0], o.x);
-        o.y = __builtin_fmaf(s, (float)c[1], o.y);
-        o.z = __builtin_fmaf(s, (float)c[2], o.z);
-        o.w = __builtin_fmaf(s, (float)c[3], o.w);
-    };
+        for (int e = 0; e < 16; ++e) sum[r][e] = 0.0f;
 
 #pragma unroll
     for (int i = 0; i < S - 1; ++i) issue(i, i);
@@ -417,155 +409,157 @@ __global__ __launch_bounds__(512, TR * TC <= 16 ? 4 : 2) void w4_gemm_kernel(
         // barrier, which also ends every read of step i - 1's slot
         wait_vmcnt_barrier<(S - 2) * NL>();
         issue(i + S - 1, slot == 0 ? S - 1 : slot - 1);
-        v4i b[2][TC];
-        float s[TC][P];
-#pragma unroll
-        for (int t = 0; t < TC; ++t) {
-            const uint4 w = *reinterpret_cast<const uint4 *>(&wbuf[slot][wave][1024 * t + 16 * lane]);
-            const uint32_t wv[4] = {w.x, w.y, w.z, w.w};
-            uint32_t sv[2] = {0, 0}, zv = 0;
-            const uint8_t *sp = &sbuf[slot][wave][32 * P * t + 2 * P * n], *zp = &zbuf[kZeros ? slot : 0][wave][16 * P * t + P * n];
-            if constexpr (P == 1) sv[0] = *reinterpret_cast<const uint16_t *>(sp);
-            if constexpr (P == 2) sv[0] = *reinterpret_cast<const uint32_t *>(sp);
-            if constexpr (P == 4) {
-                const uint2 v = *reinterpret_cast<const uint2 *>(sp);
-                sv[0] = v.x;
-                sv[1] = v.y;
-            }
-            if constexpr (kZeros) {
-                if constexpr (P == 1) zv = *zp;
-                if constexpr (P == 2) zv = *reinterpret_cast<const uint16_t *>(zp);
-                if constexpr (P == 4) zv = *reinterpret_cast<const uint32_t *>(zp);
-            }
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int d = 0; d < 4; ++d) {
-                    const int p = P == 1 ? 0 : P == 2 ? h : 2 * h + (d >> 1);
-                    b[h][t][d] = nibbles<kZeros>(wv[d], h, kZeros ? ((zv >> (8 * p)) & 0xFFu) * 0x01010101u : 0u);
-                }
-#pragma unroll
-            for (int p = 0; p < P; ++p) s[t][p] = __uint_as_float(p & 1 ? sv[p >> 1] & 0xFFFF0000u : sv[p >> 1] << 16);
+
+        // this lane's channel: pieces 2 h and 2 h + 1 of its fragment, scales, zero points
+        const uint8_t *wp = &lds.w[slot][wave][1024 * (n >> 4) + 16 * (n & 15) + 512 * h];
+        const uint4 w0 = *reinterpret_cast<const uint4 *>(wp), w1 = *reinterpret_cast<const uint4 *>(wp + 256);
+        const uint32_t w[2][4] = {{w0.x, w0.y, w0.z, w0.w}, {w1.x, w1.y, w1.z, w1.w}};
+        const uint8_t *sp = &lds.s[slot][wave][2 * P * n], *zp = &lds.z[kZeros ? slot : 0][wave][P * n];
+        uint32_t sv[2] = {0, 0}, zv = 0;
+        if constexpr (P == 1) sv[0] = *reinterpret_cast<const uint16_t *>(sp);
+        if constexpr (P == 2) sv[0] = *reinterpret_cast<const uint32_t *>(sp);
+        if constexpr (P == 4) {
+            const uint2 v = *reinterpret_cast<const uint2 *>(sp);
+            sv[0] = v.x;
+            sv[1] = v.y;
         }
-        // The products in TR P steps of TC results each.  A step reads the
-        // next one's activations, issues its own products and scales the
-        // previous step's results, so that neither the reads nor the products
-        // are waited for.
-        const int8_t *at = &abuf[kRangeBytes * (KP * slot + part) + wr * TR * 2048];
-        const v4i zero = {0, 0, 0, 0};
-        constexpr int kSteps = TR * P;
-        auto read_a = [&](int i, v4i (&a)[2]) {
-            const int r = i / P, p = i % P;
-            if constexpr (P == 4) {
-                // columns 32 p + 8 g .. + 7 of the block: half g % 2 of chunk 2 (p % 2) + g / 2
-                const v2i v = *reinterpret_cast<const v2i *>(at + 2048 * r + 1024 * (p >> 1) + 512 * (p & 1) +
-                                                             256 * (g >> 1) + 16 * n + 8 * (g & 1));
-                a[0][0] = v[0];
-                a[0][1] = v[1];
-            } else {
-                a[0] = *reinterpret_cast<const v4i *>(at + 2048 * r + 1024 * p + 16 * lane);
-                if constexpr (P == 1) a[1] = *reinterpret_cast<const v4i *>(at + 2048 * r + 1024 + 16 * lane);
+        if constexpr (kZeros) {
+            if constexpr (P == 1) zv = *zp;
+            if constexpr (P == 2) zv = *reinterpret_cast<const uint16_t *>(zp);
+            if constexpr (P == 4) zv = *reinterpret_cast<const uint32_t *>(zp);
+        }
+        float s[P];
+        uint32_t z[P];
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            s[p] = __uint_as_float(p & 1 ? sv[p >> 1] & 0xFFFF0000u : sv[p >> 1] << 16);
+            z[p] = kZeros ? ((zv >> (8 * p)) & 0xFFu) * 0x01010101u : 0u;
+        }
+        // operand j of the block's four (j = 2 half + s, or the 32-column group)
+        v4i b[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+                const uint32_t wd = P == 4 ? w[d >> 1][2 * (j & 1) + (d & 1)] : w[j & 1][d];
+                b[j][d] = nibbles<kZeros>(wd, j >> 1, z[P == 1 ? 0 : P == 2 ? j >> 1 : j]);
             }
+        // row 32 r + n of the tile, chunk of 16 columns as above
+        const int8_t *at = &lds.a[kRangeBytes * (KP * slot + part) + 2048 * (n >> 4) + 16 * (n & 15) +
+                                 (P == 4 ? 256 : 512) * h];
+        auto read_a = [&](int r, int j) {
+            return *reinterpret_cast<const v4i *>(at + 4096 * r + 1024 * (j >> 1) + (P == 4 ? 512 : 256) * (j & 1));
         };
-        auto two = [](int lo, int hi) { return (long)((uint64_t)(uint32_t)lo | (uint64_t)(uint32_t)hi << 32); };
-        v4i a[2][2], c[2][TC];
-        read_a(0, a[0]);
+        constexpr int kChain = 4 / P;  // products of one group
+        // A group's products back to back, the next group's activations behind
+        // them, then the scaling: a wave's vector operations do not run in the
+        // shadow of its own products but do beside another wave's (interleaved
+        // with the products they cost 187 us for 170 at 2048 x 4096 x 14336).
+        v4i a[2][kChain];
 #pragma unroll
-        for (int i = 0; i <= kSteps; ++i) {
-            const int p = i % P, now = i & 1;
-            if (i + 1 < kSteps) read_a(i + 1, a[now ^ 1]);
+        for (int q = 0; q < kChain; ++q) a[0][q] = read_a(0, q);
 #pragma unroll
-            for (int t = 0; t < TC; ++t) {
-                if (i < kSteps) {
-                    if constexpr (P == 4) {
-                        const v4i &bv = b[p >> 1][t];
-                        const int e = 2 * (p & 1);
-                        c[now][t] = __builtin_amdgcn_mfma_i32_16x16x32_i8(two(a[now][0][0], a[now][0][1]),
-                                                                          two(bv[e], bv[e + 1]), zero, 0, 0, 0);
-                    } else {
-                        c[now][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[now][0], b[p][t], zero, 0, 0, 0);
-                        if constexpr (P == 1)
-                            c[now][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[now][1], b[1][t], c[now][t], 0, 0, 0);
-                    }
-                }
-                if (i > 0) add(sum[(i - 1) / P][t], c[now ^ 1][t], s[t][(i - 1) % P]);
-            }
-            __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);  // the reads
+        for (int k = 0; k < TR * P; ++k) {
+            const int r = k / P, p = k % P;
+            v16i c = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
-            for (int t = 0; t < TC; ++t) {
-                __builtin_amdgcn_sched_group_barrier(0x008, P == 1 ? 2 : 1, 0);  // a product
-                __builtin_amdgcn_sched_group_barrier(0x002, 8, 0);               // and the scaling of one
-            }
+            for (int q = 0; q < kChain; ++q)
+                c = __builtin_amdgcn_mfma_i32_32x32x32_i8(a[k & 1][q], b[kChain * p + q], c, 0, 0, 0);
+            if (k + 1 < TR * P)
+#pragma unroll
+                for (int q = 0; q < kChain; ++q)
+                    a[(k + 1) & 1][q] = read_a((k + 1) / P, kChain * ((k + 1) % P) + q);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) sum[r][e] = __builtin_fmaf(s[p], (float)c[e], sum[r][e]);
             __builtin_amdgcn_sched_barrier(0);
         }
         slot = slot == S - 1 ? 0 : slot + 1;
     }
     wait_vmcnt<0>();  // loads of blocks past the end
-    // the ranges' sums, added in their order; the waves of a range then store
-    // TR / KP row tiles each
-    constexpr int TO = TR / KP;
-    static_assert(TR % KP == 0, "the ranges share the row tiles evenly");
-    float4 out[TO][TC];
+
+    // Result lane (n, h), element 4 q + e of row tile r: row 32 r + 8 q + 4 h + e, channel
+    // n.  In quads of rows (quad 4 r + q): the ranges' sums are added in their
+    // order, and the waves of a range store their share of the quads.
+    constexpr int TO = 4 * TR / KP;
+    static_assert(4 * TR % KP == 0, "the ranges share the quads evenly");
+    float4 out[TO];
     if constexpr (KP == 1) {
 #pragma unroll
-        for (int r = 0; r < TO; ++r)
-#pragma unroll
-            for (int t = 0; t < TC; ++t) out[r][t] = sum[r][t];
+        for (int o = 0; o < TO; ++o) {
+            const float *v = &sum[o >> 2][4 * (o & 3)];
+            out[o] = make_float4(v[0], v[1], v[2], v[3]);
+        }
     } else {
         wait_vmcnt_barrier<0>();  // every wave has read its last block
-        float4 *red = reinterpret_cast<float4 *>(&abuf[0]);
+        float4 *red = reinterpret_cast<float4 *>(&lds.a[0]);
 #pragma unroll
-        for (int r = 0; r < TR; ++r)
-#pragma unroll
-            for (int t = 0; t < TC; ++t) red[((part * WP + pw) * TR * TC + r * TC + t) * 64 + lane] = sum[r][t];
+        for (int o = 0; o < 4 * TR; ++o) {
+            const float *v = &sum[o >> 2][4 * (o & 3)];
+            red[((part * WP + pw) * 4 * TR + o) * 64 + lane] = make_float4(v[0], v[1], v[2], v[3]);
+        }
         wait_vmcnt_barrier<0>();
 #pragma unroll
-        for (int r = 0; r < TO; ++r)
+        for (int o = 0; o < TO; ++o) {
+            float4 v = make_float4(0, 0, 0, 0);
 #pragma unroll
-            for (int t = 0; t < TC; ++t) {
-                float4 v = make_float4(0, 0, 0, 0);
-#pragma unroll
-                for (int q = 0; q < KP; ++q) {
-                    const float4 u = red[((q * WP + pw) * TR * TC + (part * TO + r) * TC + t) * 64 + lane];
-                    v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
-                }
-                out[r][t] = v;
+            for (int q = 0; q < KP; ++q) {
+                const float4 u = red[((q * WP + pw) * 4 * TR + part * TO + o) * 64 + lane];
+                v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
             }
+            out[o] = v;
+        }
     }
-
-    // result lane (n, g), element i: row 4 g + i of the row tile, channel n.
     // Rows past M lie past the end of the buffer and channels past N get an
     // offset that does: those stores are dropped.
-    const int wrow = row0 + 16 * (TR * wr + TO * part), nrows = min(M - wrow, 16 * TO);
+    const int wrow = row0 + 8 * TO * part, nrows = min(M - wrow, 8 * TO);
     if (nrows <= 0) return;
     const uint32_t size = obf ? 2u : 4u, rowb = size * (uint32_t)N;
     const auto ry = make_rsrc(static_cast<char *>(y) + (int64_t)wrow * N * size, rowb * (uint32_t)nrows);
     const auto rxs = make_rsrc(xs + wrow, 4u * (uint32_t)nrows);
     const float post = kZeros ? 1.0f : 0.0625f;
-    uint32_t base[TC];
+    const int ch = 16 * tile0 + n;
+    const uint32_t base = ch < N ? 4u * h * rowb + size * (uint32_t)ch : kOOB;
 #pragma unroll
-    for (int t = 0; t < TC; ++t) {
-        const int ch = 16 * (tile0 + t) + n;
-        base[t] = ch < N ? 4u * g * rowb + size * (uint32_t)ch : kOOB;
-    }
+    for (int o = 0; o < TO; ++o) {
+        const uint4 sx = bload16(rxs, 32u * o + 16u * h);
+        const float f[4] = {__uint_as_float(sx.x) * (out[o].x * post), __uint_as_float(sx.y) * (out[o].y * post),
+                            __uint_as_float(sx.z) * (out[o].z * post), __uint_as_float(sx.w) * (out[o].w * post)};
 #pragma unroll
-    for (int r = 0; r < TO; ++r) {
-        const uint4 sx = bload16(rxs, 64u * r + 16u * g);
-        const float sxv[4] = {__uint_as_float(sx.x), __uint_as_float(sx.y), __uint_as_float(sx.z), __uint_as_float(sx.w)};
-#pragma unroll
-        for (int t = 0; t < TC; ++t) {
-            const float v[4] = {out[r][t].x, out[r][t].y, out[r][t].z, out[r][t].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t off = base[t] + (uint32_t)(16 * r + i) * rowb;
-                const float o = sxv[i] * (v[i] * post);
-                if (obf)
-                    __builtin_amdgcn_raw_buffer_store_b16(f32_to_bf16_rne(o), ry, off, 0, 0);
-                else
-                    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(o), ry, off, 0, 0);
-            }
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t off = base + (uint32_t)(8 * o + e) * rowb;
+            if (obf)
+                __builtin_amdgcn_raw_buffer_store_b16(f32_to_bf16_rne(f[e]), ry, off, 0, 0);
+            else
+                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(f[e]), ry, off, 0, 0);
         }
     }
+}
+
+// Workgroups as gemm_tile, but the tiles past the first `big` of an XCD go to two
+// workgroups of half the rows each: what would be less than half a round of
+// tiles on the XCD's CUs is then less than a round of halves.
+template <int TR, int KP, int S, int P, bool kZeros>
+__global__ __launch_bounds__(512, 4) void w4_gemm_kernel(const int8_t *__restrict__ xq,
+                                                         const uint8_t *__restrict__ tiled, int M, int K, int N,
+                                                         int nbm, int nbn, int big, const float *__restrict__ xs,
+                                                         void *__restrict__ y, int obf) {
+    __shared__ GemmLds<KP, S, kZeros, 32 * TR> lds;
+    const int nt = nbm * nbn, per_xcd = (nt + kXcds - 1) / kXcds;
+    const int i = (int)(blockIdx.x / kXcds);
+    const int L = (int)(blockIdx.x % kXcds) * per_xcd + (i < big ? i : big + ((i - big) >> 1));
+    if (L >= nt) return;  // padding workgroup
+    int bm, bn;
+    gemm_tile_at(L, nbm, nbn, bm, bn);
+    const int row0 = bm * 32 * TR;
+    if constexpr (TR == 4 && KP == 1) {
+        if (i >= big) {
+            const int half = row0 + 16 * TR * ((i - big) & 1);
+            if (half < M) w4_gemm_tile<TR / 2, KP, S, P, kZeros>(lds, xq, tiled, M, K, N, half, bn, xs, y, obf);
+            return;
+        }
+    }
+    w4_gemm_tile<TR, KP, S, P, kZeros>(lds, xq, tiled, M, K, N, row0, bn, xs, y, obf);
 }
 
 // --------------------------------------------------------------- launches
@@ -579,28 +573,26 @@ struct W4Args {
     int obf;
 };
 
-template <int R, int NT, int Q, int W>
+template <int NT, int Q>
 void launch_rows(const W4Args &a, int P, bool zeros, int cus, hipStream_t stream) {
     const int KB = (a.K + kBlk - 1) / kBlk, groups = ((a.N + 15) / 16 + NT - 1) / NT;
-    // as many waves on one group's columns as it has blocks, until the groups
-    // fill the waves of every CU
-    int KS = W;
-    while (KS > 1 && (KS / 2 >= KB || (int64_t)groups * KS > (int64_t)cus * W * 2)) KS /= 2;
-    const int teams = W / KS;
+    // as many waves on a group's columns as it has blocks, fewer (at least 4) once
+    // the groups give every wave of every CU two: 128256 channels at one token
+    // take 48.9 us with 4, 55.6 with 2; 28672 take 14.7 with 8, 16.0 with 16
+    int KS = kRowWaves;
+    while (KS > 1 && (KS / 2 >= KB || (KS > 4 && (int64_t)groups * KS > (int64_t)cus * kRowWaves * 2))) KS /= 2;
+    const int teams = kRowWaves / KS;
     const int wgs = std::min((groups + teams - 1) / teams, cus);
     const int rounds = (groups + wgs * teams - 1) / (wgs * teams);
-    typedef void (*Fn)(const int8_t *, const float *, const uint8_t *, int, int, int, int, int, int, void *, int);
+    typedef void (*Fn)(const int8_t *, const uint8_t *, int, int, int, int, int, int, const float *, void *, int);
     static const Fn fns[3][2] = {
-        {w4_rows_kernel<R, NT, Q, 1, false, W>, w4_rows_kernel<R, NT, Q, 1, true, W>},
-        {w4_rows_kernel<R, NT, Q, 2, false, W>, w4_rows_kernel<R, NT, Q, 2, true, W>},
-        {w4_rows_kernel<R, NT, Q, 4, false, W>, w4_rows_kernel<R, NT, Q, 4, true, W>},
+        {w4_rows_kernel<NT, Q, 1, false>, w4_rows_kernel<NT, Q, 1, true>},
+        {w4_rows_kernel<NT, Q, 2, false>, w4_rows_kernel<NT, Q, 2, true>},
+        {w4_rows_kernel<NT, Q, 4, false>, w4_rows_kernel<NT, Q, 4, true>},
     };
-    hipLaunchKernelGGL(fns[P == 4 ? 2 : P - 1][zeros], dim3(wgs * ((a.M + 16 * R - 1) / (16 * R))), dim3(W * 64), 0,
-                       stream, a.xq, a.xs, a.tiled, a.M, a.K, a.N, KS, rounds, wgs, a.y, a.obf);
+    hipLaunchKernelGGL(fns[P == 4 ? 2 : P - 1][zeros], dim3(wgs), dim3(kRowWaves * 64), 0, stream, a.xq, a.tiled, a.M,
+                       a.K, a.N, KS, rounds, wgs, a.xs, a.y, a.obf);
 }
-
-// Token rows of one call: keeps every launch under 2^32 threads.
-constexpr int64_t kMaxRows = 1 << 19;
 
 // Workgroup tiles of the GEMM: rows and channels, column ranges (waves split
 // between them), and the time of a step of `ranges` blocks and of everything
@@ -610,23 +602,31 @@ struct GemmTile {
     int rows, channels, ranges, step_ns, fixed_ns;
 };
 constexpr GemmTile kGemmTiles[] = {
-    {128, 256, 1, 1500, 3000}, {64, 256, 1, 920, 3000}, {64, 128, 2, 950, 3000},
-    {64, 64, 4, 1050, 3000},   {32, 128, 2, 620, 3000}, {64, 32, 4, 650, 3000},
+    {128, 256, 1, 1400, 3000}, {64, 256, 1, 825, 3000}, {64, 128, 2, 890, 3000},
+    {64, 64, 4, 970, 3000},    {32, 128, 2, 510, 3000}, {32, 64, 4, 575, 3000},
 };
 
-// The tile with the least estimated time: rounds of workgroups on the CUs
-// times a workgroup's time.
-int gemm_tile_choice(int64_t M, int64_t K, int64_t N, int cus) {
-    const int64_t KB = (K + kBlk - 1) / kBlk;
-    int best = 0;
+struct GemmPlan {
+    int tile, big;  // tile of kGemmTiles; whole tiles of an XCD (the rest are halved)
+};
+
+// The tile with the least estimated time: rounds of workgroups on an XCD's CUs
+// times a workgroup's time.  On the largest tile a last round that is at most
+// half full is taken in halves (0.6 of a round).
+GemmPlan gemm_plan(int64_t M, int64_t K, int64_t N, int cus) {
+    const int64_t KB = (K + kBlk - 1) / kBlk, cus_xcd = std::max(1, cus / kXcds);
+    GemmPlan best{};
     int64_t least = 0;
     for (int i = 0; i < (int)(sizeof(kGemmTiles) / sizeof(kGemmTiles[0])); ++i) {
         const GemmTile &t = kGemmTiles[i];
         const int64_t wgs = ((M + t.rows - 1) / t.rows) * ((N + t.channels - 1) / t.channels);
-        const int64_t ns = ((wgs + cus - 1) / cus) * ((KB + t.ranges - 1) / t.ranges * t.step_ns + t.fixed_ns);
+        const int64_t per_xcd = (wgs + kXcds - 1) / kXcds, rest = per_xcd % cus_xcd;
+        const bool halves = i == 0 && rest > 0 && 2 * rest <= cus_xcd;
+        const int64_t tenths = per_xcd / cus_xcd * 10 + (halves ? 6 : rest ? 10 : 0);
+        const int64_t ns = tenths * ((KB + t.ranges - 1) / t.ranges * t.step_ns + t.fixed_ns);
         if (i == 0 || ns < least) {
             least = ns;
-            best = i;
+            best = {i, (int)(halves ? per_xcd - rest : per_xcd)};
         }
     }
     return best;
@@ -635,19 +635,23 @@ int gemm_tile_choice(int64_t M, int64_t K, int64_t N, int cus) {
 // a wave's rows of output stay under 2^31 bytes (32-bit store offsets)
 constexpr int64_t kGemmMaxN = (int64_t(1) << 31) / (4 * 128) - 1;
 
-template <int TR, int TC, int WR, int KP, int S>
-void launch_gemm(const W4Args &a, int P, bool zeros, hipStream_t stream) {
-    constexpr int BM = 16 * TR * WR, BN = 16 * TC * (8 / KP / WR);
+template <int TR, int KP, int S>
+void launch_gemm(const W4Args &a, int P, bool zeros, int big, hipStream_t stream) {
+    constexpr int BM = 32 * TR, BN = 32 * (8 / KP);
     const int nbm = (a.M + BM - 1) / BM, nbn = (a.N + BN - 1) / BN;
-    typedef void (*Fn)(const int8_t *, const uint8_t *, int, int, int, int, int, const float *, void *, int);
+    const int per_xcd = (nbm * nbn + kXcds - 1) / kXcds;
+    typedef void (*Fn)(const int8_t *, const uint8_t *, int, int, int, int, int, int, const float *, void *, int);
     static const Fn fns[3][2] = {
-        {w4_gemm_kernel<TR, TC, WR, KP, S, 1, false>, w4_gemm_kernel<TR, TC, WR, KP, S, 1, true>},
-        {w4_gemm_kernel<TR, TC, WR, KP, S, 2, false>, w4_gemm_kernel<TR, TC, WR, KP, S, 2, true>},
-        {w4_gemm_kernel<TR, TC, WR, KP, S, 4, false>, w4_gemm_kernel<TR, TC, WR, KP, S, 4, true>},
+        {w4_gemm_kernel<TR, KP, S, 1, false>, w4_gemm_kernel<TR, KP, S, 1, true>},
+        {w4_gemm_kernel<TR, KP, S, 2, false>, w4_gemm_kernel<TR, KP, S, 2, true>},
+        {w4_gemm_kernel<TR, KP, S, 4, false>, w4_gemm_kernel<TR, KP, S, 4, true>},
     };
-    hipLaunchKernelGGL(fns[P == 4 ? 2 : P - 1][zeros], dim3((nbm * nbn + kXcds - 1) / kXcds * kXcds), dim3(512), 0,
-                       stream, a.xq, a.tiled, a.M, a.K, a.N, nbm, nbn, a.xs, a.y, a.obf);
+    hipLaunchKernelGGL(fns[P == 4 ? 2 : P - 1][zeros], dim3((2 * per_xcd - big) * kXcds), dim3(512), 0, stream, a.xq,
+                       a.tiled, a.M, a.K, a.N, nbm, nbn, big, a.xs, a.y, a.obf);
 }
+
+// Token rows of one call: keeps every launch under 2^32 threads.
+constexpr int64_t kMaxRows = 1 << 19;
 
 int check_w4(int64_t M, int64_t K, int64_t N, int64_t group, bool zeros) {
     if (M <= 0 || K <= 0 || N <= 0 || group <= 0)
@@ -671,6 +675,8 @@ int check_linear(const int8_t *xq, const float *xs, int64_t M, int64_t K, int64_
     if (has_zeros != 0 && has_zeros != 1) return s3d8::fail(S3D8_ERR_INVALID_ARG, "has_zeros must be 0 or 1");
     int rc = check_w4(M, K, N, group, has_zeros != 0);
     if (rc) return rc;
+    if (M > 16 && N > kGemmMaxN)
+        return s3d8::fail(S3D8_ERR_SHAPE, "N over 4194303 is not supported for M > 16");
     if (tiled_bytes != w4_bytes(N, K, group, has_zeros != 0))
         return s3d8::fail(S3D8_ERR_INVALID_ARG,
                           "tiled_bytes is not s3d8_w4_tiled_bytes(N, K, group, has_zeros): pass the matrix as "
@@ -686,23 +692,32 @@ int launch_linear(const int8_t *xq, const float *xs, int64_t M, int64_t K, int64
                   int64_t group, bool zeros, void *y, int32_t out_type, int cus, hipStream_t stream) {
     const W4Args a{xq, xs, tiled, (int)M, (int)K, (int)N, y, out_type == S3D8_OUT_BF16};
     const int P = per_block(K, group);
-    if (M <= 4)
-        launch_rows<1, 1, 1, 16>(a, P, zeros, cus, stream);
-    else if (M <= 8)
-        launch_rows<1, 2, 2, 16>(a, P, zeros, cus, stream);
-    else if (M <= 16)
-        launch_rows<1, 2, 4, 16>(a, P, zeros, cus, stream);
-    else if (N > kGemmMaxN)
-        launch_rows<2, 2, 4, 8>(a, P, zeros, cus, stream);
-    else
-        switch (gemm_tile_choice(M, K, N, cus)) {
-            case 0: launch_gemm<8, 2, 1, 1, 2>(a, P, zeros, stream); break;
-            case 1: launch_gemm<4, 2, 1, 1, 3>(a, P, zeros, stream); break;
-            case 2: launch_gemm<4, 2, 1, 2, 3>(a, P, zeros, stream); break;
-            case 3: launch_gemm<4, 2, 1, 4, 3>(a, P, zeros, stream); break;
-            case 4: launch_gemm<2, 2, 1, 2, 3>(a, P, zeros, stream); break;
-            default: launch_gemm<4, 1, 1, 4, 3>(a, P, zeros, stream); break;
+    if (M <= 16) {
+        // Tiles per group: one while a CU has no more than one (4096 -> 1024 at one
+        // token 4.3 us, 4.6 with two), else two (4096 -> 14336: 9.4 us, 9.8 with
+        // one, 9.3 with four; 8192: 6.7, 7.4, 7.8), or four where the activations
+        // that each group reads again are many (16 tokens, 14336: 10.5, 11.8 with two).
+        const int64_t tiles = (N + 15) / 16;
+        const int nt = tiles <= cus ? 1 : M > 8 && tiles > 3 * cus ? 4 : 2;
+        if (M <= 4)
+            nt == 1 ? launch_rows<1, 1>(a, P, zeros, cus, stream) : launch_rows<2, 1>(a, P, zeros, cus, stream);
+        else if (M <= 8)
+            nt == 1 ? launch_rows<1, 2>(a, P, zeros, cus, stream) : launch_rows<2, 2>(a, P, zeros, cus, stream);
+        else if (nt == 4)
+            launch_rows<4, 4>(a, P, zeros, cus, stream);
+        else
+            nt == 1 ? launch_rows<1, 4>(a, P, zeros, cus, stream) : launch_rows<2, 4>(a, P, zeros, cus, stream);
+    } else {
+        const GemmPlan plan = gemm_plan(M, K, N, cus);
+        switch (plan.tile) {
+            case 0: launch_gemm<4, 1, 2>(a, P, zeros, plan.big, stream); break;
+            case 1: launch_gemm<2, 1, 3>(a, P, zeros, plan.big, stream); break;
+            case 2: launch_gemm<2, 2, 3>(a, P, zeros, plan.big, stream); break;
+            case 3: launch_gemm<2, 4, 3>(a, P, zeros, plan.big, stream); break;
+            case 4: launch_gemm<1, 2, 3>(a, P, zeros, plan.big, stream); break;
+            default: launch_gemm<1, 4, 3>(a, P, zeros, plan.big, stream); break;
         }
+    }
     return s3d8::launch_status();
 }
 
