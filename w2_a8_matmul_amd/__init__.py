@@ -220,7 +220,7 @@ def _y_out(y, M, N, out, device):
     torch = _torch()
     dtype = torch.float32 if out == "f32" else torch.bfloat16
     if y is None:
-        return torch.empty((M, N), dtype=dtype, device=device)
+        return torch.empty(M, N, dtype=dtype, device=device)
     _dev_check(y, dtype, "y", device, numel=M * N)
     return y
 
@@ -237,11 +237,11 @@ def _codes_out(xq, xs, M, K, device):
     """Activation codes and scales written by quant_act / forward."""
     torch = _torch()
     if xq is None:
-        xq = torch.empty((M, K), dtype=torch.int8, device=device)
+        xq = torch.empty(M, K, dtype=torch.int8, device=device)
     else:
         _dev_check(xq, torch.int8, "xq", device, numel=M * K)
     if xs is None:
-        xs = torch.empty((M,), dtype=torch.float32, device=device)
+        xs = torch.empty(M, dtype=torch.float32, device=device)
     else:
         _dev_check(xs, torch.float32, "xs", device, numel=M)
     return xq, xs
@@ -641,7 +641,7 @@ def _rows_out(out, rows, xq, xs, M, K, device):
         raise ValueError("xq and xs go with out='codes'")
     dtype = torch.float32 if out == "f32" else torch.bfloat16
     if rows is None:
-        rows = torch.empty((M, K), dtype=dtype, device=device)
+        rows = torch.empty(M, K, dtype=dtype, device=device)
     else:
         _dev_check(rows, dtype, "rows", device, numel=M * K)
     return rows, None, None
