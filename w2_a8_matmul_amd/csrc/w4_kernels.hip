@@ -608,26 +608,24 @@ constexpr GemmTile kGemmTiles[] = {
 
 struct GemmPlan {
     int tile, big;  // tile of kGemmTiles; whole tiles of an XCD (the rest are halved)
+    int64_t ns;     // estimated time
 };
 
 // The tile with the least estimated time: rounds of workgroups on an XCD's CUs
 // times a workgroup's time.  On the largest tile a last round that is at most
-// half full is taken in halves (0.6 of a round).
+// half full is taken in halves, beside the workgroups before them on a CU (0.3 of a
+// round: 2048 x 4096 -> 14336 has 3.5 rounds and takes 159 us, a round 47; 0.6 alone).
 GemmPlan gemm_plan(int64_t M, int64_t K, int64_t N, int cus) {
     const int64_t KB = (K + kBlk - 1) / kBlk, cus_xcd = std::max(1, cus / kXcds);
     GemmPlan best{};
-    int64_t least = 0;
     for (int i = 0; i < (int)(sizeof(kGemmTiles) / sizeof(kGemmTiles[0])); ++i) {
         const GemmTile &t = kGemmTiles[i];
         const int64_t wgs = ((M + t.rows - 1) / t.rows) * ((N + t.channels - 1) / t.channels);
         const int64_t per_xcd = (wgs + kXcds - 1) / kXcds, rest = per_xcd % cus_xcd;
         const bool halves = i == 0 && rest > 0 && 2 * rest <= cus_xcd;
-        const int64_t tenths = per_xcd / cus_xcd * 10 + (halves ? 6 : rest ? 10 : 0);
-        const int64_t ns = tenths * ((KB + t.ranges - 1) / t.ranges * t.step_ns + t.fixed_ns);
-        if (i == 0 || ns < least) {
-            least = ns;
-            best = {i, (int)(halves ? per_xcd - rest : per_xcd)};
-        }
+        const int64_t rounds = per_xcd / cus_xcd, tenths = 10 * rounds + (halves ? (rounds ? 3 : 6) : rest ? 10 : 0);
+        const int64_t ns = tenths * ((KB + t.ranges - 1) / t.ranges * t.step_ns + t.fixed_ns) / 10;
+        if (i == 0 || ns < best.ns) best = {i, (int)(halves ? per_xcd - rest : per_xcd), ns};
     }
     return best;
 }
@@ -688,36 +686,60 @@ int check_linear(const int8_t *xq, const float *xs, int64_t M, int64_t K, int64_
     return S3D8_OK;
 }
 
+// Up to 16 rows.  Tiles per group: one while a CU has no more than one (4096 -> 1024 at
+// one token 4.3 us, 4.6 with two), else two (4096 -> 14336: 9.4 us, 9.8 with one, 9.3
+// with four; 8192: 6.7, 7.4, 7.8), or four where the activations that each group reads
+// again are many (16 tokens, 14336: 10.5, 11.8 with two).
+void launch_few(const W4Args &a, int P, bool zeros, int cus, hipStream_t stream) {
+    const int64_t tiles = ((int64_t)a.N + 15) / 16;
+    const int nt = tiles <= cus ? 1 : a.M > 8 && tiles > 3 * cus ? 4 : 2;
+    if (a.M <= 4)
+        nt == 1 ? launch_rows<1, 1>(a, P, zeros, cus, stream) : launch_rows<2, 1>(a, P, zeros, cus, stream);
+    else if (a.M <= 8)
+        nt == 1 ? launch_rows<1, 2>(a, P, zeros, cus, stream) : launch_rows<2, 2>(a, P, zeros, cus, stream);
+    else if (nt == 4)
+        launch_rows<4, 4>(a, P, zeros, cus, stream);
+    else
+        nt == 1 ? launch_rows<1, 4>(a, P, zeros, cus, stream) : launch_rows<2, 4>(a, P, zeros, cus, stream);
+}
+
+void launch_many(const W4Args &a, const GemmPlan &plan, int P, bool zeros, hipStream_t stream) {
+    switch (plan.tile) {
+        case 0: launch_gemm<4, 1, 2>(a, P, zeros, plan.big, stream); break;
+        case 1: launch_gemm<2, 1, 3>(a, P, zeros, plan.big, stream); break;
+        case 2: launch_gemm<2, 2, 3>(a, P, zeros, plan.big, stream); break;
+        case 3: launch_gemm<2, 4, 3>(a, P, zeros, plan.big, stream); break;
+        case 4: launch_gemm<1, 2, 3>(a, P, zeros, plan.big, stream); break;
+        default: launch_gemm<1, 4, 3>(a, P, zeros, plan.big, stream); break;
+    }
+}
+
 int launch_linear(const int8_t *xq, const float *xs, int64_t M, int64_t K, int64_t N, const uint8_t *tiled,
                   int64_t group, bool zeros, void *y, int32_t out_type, int cus, hipStream_t stream) {
-    const W4Args a{xq, xs, tiled, (int)M, (int)K, (int)N, y, out_type == S3D8_OUT_BF16};
+    const bool bf = out_type == S3D8_OUT_BF16;
+    const W4Args a{xq, xs, tiled, (int)M, (int)K, (int)N, y, bf};
     const int P = per_block(K, group);
     if (M <= 16) {
-        // Tiles per group: one while a CU has no more than one (4096 -> 1024 at one
-        // token 4.3 us, 4.6 with two), else two (4096 -> 14336: 9.4 us, 9.8 with
-        // one, 9.3 with four; 8192: 6.7, 7.4, 7.8), or four where the activations
-        // that each group reads again are many (16 tokens, 14336: 10.5, 11.8 with two).
-        const int64_t tiles = (N + 15) / 16;
-        const int nt = tiles <= cus ? 1 : M > 8 && tiles > 3 * cus ? 4 : 2;
-        if (M <= 4)
-            nt == 1 ? launch_rows<1, 1>(a, P, zeros, cus, stream) : launch_rows<2, 1>(a, P, zeros, cus, stream);
-        else if (M <= 8)
-            nt == 1 ? launch_rows<1, 2>(a, P, zeros, cus, stream) : launch_rows<2, 2>(a, P, zeros, cus, stream);
-        else if (nt == 4)
-            launch_rows<4, 4>(a, P, zeros, cus, stream);
-        else
-            nt == 1 ? launch_rows<1, 4>(a, P, zeros, cus, stream) : launch_rows<2, 4>(a, P, zeros, cus, stream);
-    } else {
-        const GemmPlan plan = gemm_plan(M, K, N, cus);
-        switch (plan.tile) {
-            case 0: launch_gemm<4, 1, 2>(a, P, zeros, plan.big, stream); break;
-            case 1: launch_gemm<2, 1, 3>(a, P, zeros, plan.big, stream); break;
-            case 2: launch_gemm<2, 2, 3>(a, P, zeros, plan.big, stream); break;
-            case 3: launch_gemm<2, 4, 3>(a, P, zeros, plan.big, stream); break;
-            case 4: launch_gemm<1, 2, 3>(a, P, zeros, plan.big, stream); break;
-            default: launch_gemm<1, 4, 3>(a, P, zeros, plan.big, stream); break;
+        launch_few(a, P, zeros, cus, stream);
+        return s3d8::launch_status();
+    }
+    GemmPlan plan = gemm_plan(M, K, N, cus);
+    // Up to 16 rows past a multiple of 64 (the 1601 tokens of an image) cost the
+    // GEMM a row of tiles; where that is more than a launch of the kernel for
+    // few rows (its weights at 4 TB/s and 3.5 us), they go there: 1601 x 5120 ->
+    // 1280 takes 32.7 us in one launch, 30.1 in two.
+    const int64_t rest = M % 64, whole = M - rest;
+    if (rest > 0 && rest <= 16 && whole > 16) {
+        const GemmPlan most = gemm_plan(whole, K, N, cus);
+        if (most.ns + 3500 + w4_bytes(N, K, group, zeros) / 4000 < plan.ns) {
+            const W4Args last{xq + whole * K, xs + whole, tiled, (int)rest, (int)K, (int)N,
+                              static_cast<char *>(y) + whole * N * (bf ? 2 : 4), bf};
+            launch_few(last, P, zeros, cus, stream);
+            launch_many({xq, xs, tiled, (int)whole, (int)K, (int)N, y, bf}, most, P, zeros, stream);
+            return s3d8::launch_status();
         }
     }
+    launch_many(a, plan, P, zeros, stream);
     return s3d8::launch_status();
 }
 
