@@ -427,7 +427,8 @@ int32_t s3d8_dequant_ex(const uint8_t *packed, const void *table, int32_t format
  *     packed   uint8 [N][K/2], row-major: byte (n, j) holds the codes of input
  *              columns 2j (low nibble) and 2j + 1 (high nibble), 0..15;
  *     scales   uint16 [N][G]: bfloat16 bit patterns, finite;
- *     zeros    uint8 [N][G], entries 0..15, or absent: every zero point is 8.
+ *     zeros    uint8 [N][G], entries 0..15 (not checked), or absent: every zero
+ *              point is 8.
  *   Weight: w_nk = scales[n][k / group] * (q_nk - z[n][k / group]).
  * Linear:
  *   acc_mng = sum over the columns k of group g of xq_mk * (q_nk - z_ng)
@@ -521,7 +522,8 @@ typedef struct s3d8_block_norm_args {
     int8_t *xq;               /* out, int8 [M][K] for CODES, else NULL                  */
     float *xs;                /* out, fp32 [M] for CODES, else NULL                     */
     int64_t M, K;
-    float residual_scale, eps;
+    double eps;
+    float residual_scale;
     int32_t kind;             /* S3D8_NORM_RMS or S3D8_NORM_LAYER, for both norms       */
     int32_t h_type, branch_type, out_type;
     int32_t gate_channels;    /* gate is [K] rather than [1]                            */

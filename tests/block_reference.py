@@ -91,7 +91,7 @@ def normalise(v, kind: str, eps: float, w, b):
     d = v.astype(np.float64)
     mu = d.mean(1, keepdims=True) if kind == "layer" else 0.0
     var = ((d - mu) ** 2).mean(1, keepdims=True)
-    r = (1.0 / np.sqrt(var + np.float64(F(eps)))).astype(F)
+    r = (1.0 / np.sqrt(var + eps)).astype(F)
     u = (v - mu.astype(F)) * r if kind == "layer" else v * r
     u = u * w
     return u + b if b is not None else u

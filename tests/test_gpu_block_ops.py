@@ -107,6 +107,18 @@ def test_norm_rows(gpu, M):
     norm_case(gpu, M, 1280, "layer", gate="tanh", out="bf16", seed=2)
 
 
+def test_norm_small_rows_see_eps(gpu):
+    """Rows whose mean square is near eps, and another eps."""
+    g = rng(7307)
+    K = 1280
+    h = (g.standard_normal((6, K)) * np.geomspace(1e-5, 1e-1, 6)[:, None]).astype(F)
+    w = np.ones(K, F)
+    for kind in ("rms", "layer"):
+        for eps in (1e-5, 1e-6, 1e-12):
+            _, u_r = ref.block_norm(h, w, eps=eps, kind=kind)
+            check_rows("codes", s3d8.block_norm(dev(h, gpu), dev(w, gpu), eps=eps, kind=kind), u_r)
+
+
 def test_norm_edge_rows(gpu):
     """Zero rows (codes and scale 0), a single value, a constant row under LAYER, tiny and large values."""
     K = 256
@@ -179,6 +191,18 @@ def test_glu_values(gpu):
     assert np.isfinite(a).all()
     for out in ("f32", "codes"):
         check_rows(out, s3d8.glu_act(dev(gate, gpu), dev(up, gpu), out=out), a)
+
+
+def test_glu_equal_values(gpu):
+    """Rows of few distinct values: everything is the row's maximum, or on a border with it."""
+    for K in (48, 1040, 4096, 14336):
+        gate = np.stack([np.full(K, 1.25), np.where(np.arange(K) % 2, -2.0, 2.0), np.full(K, 30.0),
+                         np.where(np.arange(K) == K - 1, 3.0, 1e-3)]).astype(F)
+        up = np.stack([np.full(K, -0.75), np.full(K, 1.0), np.where(np.arange(K) % 3, 127.0, 63.5),
+                       np.full(K, 1.0)]).astype(F)
+        for bf in (False, True):
+            g, u = (ref.round_bf16(gate), ref.round_bf16(up)) if bf else (gate, up)
+            check_rows("codes", s3d8.glu_act(dev(g, gpu, bf), dev(u, gpu, bf)), ref.glu(g, u))
 
 
 def test_glu_rounding_borders(gpu):

@@ -586,10 +586,13 @@ def w4_forward(x, tiled, N: int, group: int, zeros: bool = False, y=None, xq=Non
 
 class W4Linear:
     """A W4 weight matrix resident in device memory, in the tiled layout
-    (``packed``, ``scales``, ``zeros``: numpy arrays or device tensors)."""
+    (``packed``, ``scales``, ``zeros``: numpy arrays or device tensors; on the
+    device of ``packed`` unless ``device`` says another)."""
 
-    def __init__(self, packed, scales, group: int, zeros=None, device="cuda"):
+    def __init__(self, packed, scales, group: int, zeros=None, device=None):
         torch = _torch()
+        if device is None:
+            device = packed.device if isinstance(packed, torch.Tensor) else "cuda"
 
         def resident(a, kind):
             if isinstance(a, torch.Tensor):
@@ -697,7 +700,7 @@ def block_norm(h, weight, bias=None, *, branch=None, post_weight=None, post_bias
     rows, xq, xs = _rows_out(out, rows, xq, xs, M, K, dev)
     args = _lib.BLOCK_NORM_ARGS(h.data_ptr(), _ptr(branch), _ptr(post_weight), _ptr(post_bias), _ptr(gate),
                                 weight.data_ptr(), _ptr(bias), _ptr(h_out), _ptr(rows), _ptr(xq), _ptr(xs), M, K,
-                                residual_scale, eps, _KINDS[kind], ht, bt, _ROWS[out], channels, bool(tanh_gate))
+                                eps, residual_scale, _KINDS[kind], ht, bt, _ROWS[out], channels, bool(tanh_gate))
     _enqueue("s3d8_block_norm", dev, args)
     u = (xq, xs) if rows is None else (rows,)
     if branch is not None:

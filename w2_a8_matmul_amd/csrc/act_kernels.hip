@@ -180,7 +180,7 @@ __device__ __forceinline__ void row_out(const float4 (&v)[NV], int64_t row, int 
 // rounded to fp32 once: an fp32 sum would depend on its order, and its last
 // bit moves codes across their rounding borders.
 template <int T, int NV, bool kLayer>
-__device__ __forceinline__ void normalise(float4 (&v)[NV], int K, float eps, const float *__restrict__ w,
+__device__ __forceinline__ void normalise(float4 (&v)[NV], int K, double eps, const float *__restrict__ w,
                                           const float *__restrict__ b, double *slot) {
     const int n4 = K >> 2;
     double mu = 0.0, q = 0.0;
@@ -203,7 +203,7 @@ __device__ __forceinline__ void normalise(float4 (&v)[NV], int K, float eps, con
         square(v[j].z);
         square(v[j].w);
     }
-    const float r = (float)(1.0 / sqrt(block_sum<T>(q, slot) / (double)K + (double)eps));
+    const float r = (float)(1.0 / sqrt(block_sum<T>(q, slot) / (double)K + eps));
     const float m = (float)mu;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -518,7 +518,7 @@ int32_t s3d8_block_norm(const s3d8_block_norm_args *args, void *stream) {
     if (a.post_bias && !a.post_weight) return s3d8::fail(S3D8_ERR_INVALID_ARG, "post_bias needs post_weight");
     if (!row_type(a.h_type) || (a.branch && !row_type(a.branch_type)))
         return s3d8::fail(S3D8_ERR_INVALID_ARG, "unknown row type");
-    if (!(a.eps > 0.0f)) return s3d8::fail(S3D8_ERR_INVALID_ARG, "eps must be positive");
+    if (!(a.eps > 0.0)) return s3d8::fail(S3D8_ERR_INVALID_ARG, "eps must be positive");
     int rc = check_rows(a.M, a.K);
     if (rc) return rc;
     rc = check_out(a.out_type, a.rows, a.xq, a.xs);
