@@ -434,8 +434,8 @@ int32_t s3d8_dequant_ex(const uint8_t *packed, const void *table, int32_t format
  *   acc_mng = sum over the columns k of group g of xq_mk * (q_nk - z_ng)
  *             (exact INT32),
  *   y_mn    = s_m * sum_g scales_ng * float(acc_mng)   (fp32 sums, in an order
- *             that depends on the shape alone, so repeated calls give the
- *             same bits). */
+ *             that depends on the shape and the device's CU count alone, so
+ *             repeated calls give the same bits). */
 
 /* Encode a matrix to W4 on the host.  Per group, in fp32 (IEEE division, round
  * half to even):
@@ -546,9 +546,9 @@ typedef struct s3d8_block_norm_args {
  * The sums, mu and r are computed in 64 bits and then rounded to fp32; every
  * other operation is one IEEE fp32 operation.  (The codes are whole numbers:
  * sums in 64 bits keep them from depending on the order of summation.)
- * K is a positive multiple of 16, at most 65536; at most 524288 rows.  Row matrices must be 16-B
- * aligned, fp32 vectors [K] as well; values finite, eps > 0.  Outputs other
- * than h_out = h must not overlap inputs.
+ * K is a positive multiple of 16, at most 65536; at most 524288 rows.  Row
+ * matrices must be 16-B aligned, fp32 vectors [K] as well; values finite,
+ * eps > 0.  Outputs other than h_out = h must not overlap inputs.
  * Errors: INVALID_ARG, SHAPE, ALIGN, DEVICE, HIP. */
 int32_t s3d8_block_norm(const s3d8_block_norm_args *args, void *stream);
 
@@ -563,7 +563,8 @@ int32_t s3d8_block_norm(const s3d8_block_norm_args *args, void *stream);
  *                elements.
  *   rows         out, device [M][K] for out_type F32 or BF16, 16-B aligned, else NULL.
  *   xq, xs       out, int8 [M][K] (16-B aligned) and fp32 [M] for CODES, else NULL.
- * K is a positive multiple of 16, at most 65536; at most 524288 rows.
+ * K is a positive multiple of 16, at most 65536; at most 524288 rows.  Outputs
+ * must not overlap inputs.
  * Errors: INVALID_ARG, SHAPE, ALIGN, DEVICE, HIP. */
 int32_t s3d8_glu_act(const void *gate, int64_t ld_gate, const void *up, int64_t ld_up, int64_t M, int64_t K,
                      int32_t in_type, int32_t out_type, void *rows, int8_t *xq, float *xs, void *stream);

@@ -338,3 +338,73 @@ def test_mlp_block_in_a_graph(gpu, M):
         b.check(out)
         for e, r in zip(b.run(), out):
             assert torch.equal(e, r)
+
+
+def test_side_streams_at_once(gpu):
+    """The norm on one stream and the gated activation on another, both at once, several calls each."""
+    g = rng(7307)
+    M, K = 300, 2064
+    h, br, w = rows(g, M, K, True), rows(g, M, K, True, 0.5), (1 + 0.1 * g.standard_normal(K)).astype(F)
+    gate, up = rows(g, M, K, False, 2.0), rows(g, M, K, False)
+    dh, dbr, dw, dg, du = dev(h, gpu, True), dev(br, gpu, True), dev(w, gpu), dev(gate, gpu), dev(up, gpu)
+    torch.cuda.synchronize()
+    one, two = torch.cuda.Stream(gpu), torch.cuda.Stream(gpu)
+    with torch.cuda.stream(one):
+        norms = [s3d8.block_norm(dh, dw, branch=dbr) for _ in range(4)]
+    with torch.cuda.stream(two):
+        glus = [s3d8.glu_act(dg, du) for _ in range(4)]
+    torch.cuda.synchronize()
+    h_r, u_r = ref.block_norm(h, w, None, br, h_bf16=True)
+    a_r = ref.glu(gate, up)
+    for n in norms:
+        same(n[0], h_r)
+        check_rows("codes", n[1:], u_r)
+    for a in glus:
+        check_rows("codes", a, a_r)
+
+
+def test_most_rows(gpu):
+    """2^19 rows of 16."""
+    M, K = 1 << 19, 16
+    norm_case(gpu, M, K, post=True)
+    norm_case(gpu, M, K, "layer", h_bf=True, b_bf=True, out="bf16")
+    g = rng(7308)
+    gate, up = rows(g, M, K, True, 2.0), rows(g, M, K, True)
+    check_rows("codes", s3d8.glu_act(dev(gate, gpu, True), dev(up, gpu, True)), ref.glu(gate, up))
+
+
+def test_offsets_past_32_bits(gpu):
+    """Row matrices of more than 2^31 elements (and 2^32 bytes): the rows at the ends."""
+    K, few = 65536, 3
+    g = rng(7309)
+    h, br, w = rows(g, few, K, True), rows(g, few, K, True, 0.5), (1 + 0.1 * g.standard_normal(K)).astype(F)
+    h_r, u_r = ref.block_norm(h, w, None, br, h_bf16=True)
+    M = 33000  # 2.16e9 elements
+    dh = torch.zeros((M, K), dtype=torch.bfloat16, device=gpu)
+    dbr = torch.zeros_like(dh)
+    for d, x in ((dh, h), (dbr, br)):
+        d[:few] = dev(x, gpu, True)
+        d[M - few:] = dev(x, gpu, True)
+    h1, xq, xs = s3d8.block_norm(dh, dev(w, gpu), branch=dbr)
+    for at in (slice(0, few), slice(M - few, M)):
+        same(h1[at], h_r)
+        check_rows("codes", (xq[at], xs[at]), u_r)
+    assert not h1[few:M - few:97].any() and not xq[few:M - few:97].any() and not xs[few:M - few].any()
+    del h1, xq, xs, dbr
+    # the halves of one matrix, twice the row stride
+    M = 17000
+    both = torch.zeros((M, 2 * K), dtype=torch.bfloat16, device=gpu)
+    for at in (slice(0, few), slice(M - few, M)):
+        both[at, :K] = dev(h, gpu, True)
+        both[at, K:] = dev(br, gpu, True)
+    out = s3d8.glu_act(both[:, :K], both[:, K:], out="bf16")
+    for at in (slice(0, few), slice(M - few, M)):
+        check_rows("bf16", out[at], ref.glu(h, br))
+    assert not out[few:M - few:97].any()
+
+
+def test_gate_must_be_a_tensor(gpu):
+    h = torch.zeros((2, 64), device=gpu)
+    w = torch.ones(64, device=gpu)
+    with pytest.raises(TypeError):
+        s3d8.block_norm(h, w, branch=h.clone(), gate=0.5)

@@ -207,3 +207,52 @@ def test_binding_refusals(gpu):
     with pytest.raises((ValueError, s3d8.S3D8Error)):
         s3d8.w4_tile(packed, sc, 0)
     torch.cuda.synchronize()
+
+
+def test_many_rows_in_a_graph(gpu):
+    """1601 rows, which may take two launches (the last row by itself), captured once and replayed."""
+    M, N, K, group = 1601, 1280, 5120, 128
+    q, scales, z = matrix(N, K, group, True)
+    lin = tiled_on(gpu, q, scales, z, group)
+    dq, ds = (torch.from_numpy(t).to(gpu) for t in codes(M, K))
+    lin.linear(dq, ds)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream(gpu)
+    side.wait_stream(torch.cuda.current_stream(gpu))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        y = lin.linear(dq, ds)
+    for word in (1, 2, 3):
+        xq, xs = codes(M, K, word)
+        dq.copy_(torch.from_numpy(xq))
+        ds.copy_(torch.from_numpy(xs))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(lin.linear(dq, ds), y)
+        some = [0, 1, 63, 64, 800, 1535, 1536, 1599, 1600]
+        check(y[some], xq[some], xs[some], q, scales, z, group)
+
+
+@pytest.mark.parametrize("M,N,K", [(1 << 19, 20, 16), (1 << 19, 4080, 32), (16, 1 << 22, 32)])
+def test_largest_sizes(gpu, M, N, K):
+    """The most rows, an output of 8.6 GB, channels past 2^22: some rows and channels against the plain form."""
+    q, scales, z = matrix(min(N, 4096), K, 32, False)
+    times = N // q.shape[0]
+    lin = tiled_on(gpu, np.tile(q, (times, 1)), np.tile(scales, (times, 1)), None, 32)
+    xq, xs = codes(1024, K)
+    xq, xs = xq[:M], xs[:M]
+    dq, ds = torch.from_numpy(xq).to(gpu), torch.from_numpy(xs).to(gpu)
+    rep = M // xq.shape[0]
+    y = lin.linear(dq.repeat(rep, 1), ds.repeat(rep))
+    check(y[:xq.shape[0], :q.shape[0]], xq, xs, q, scales, None, 32)
+    check(y[M - xq.shape[0]:, N - q.shape[0]:], xq, xs, q, scales, None, 32)
+    for a in range(0, M, max(M // 4, xq.shape[0])):
+        assert torch.equal(y[a:a + xq.shape[0], :q.shape[0]], y[:xq.shape[0], :q.shape[0]])
+
+
+def test_module_refuses_other_types(gpu):
+    q, scales, z = matrix(40, 128, 64, True)
+    for args in ((ref.pack(q), ref.bf16_value(scales), 64, z), (ref.pack(q).astype(np.int32), scales, 64, z),
+                 (ref.pack(q), scales, 64, z.astype(np.float32))):
+        with pytest.raises(TypeError):
+            s3d8.W4Linear(*args, device=gpu)

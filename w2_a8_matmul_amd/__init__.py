@@ -597,7 +597,10 @@ class W4Linear:
         def resident(a, kind):
             if isinstance(a, torch.Tensor):
                 return a.to(device).contiguous()
-            return torch.as_tensor(np.ascontiguousarray(a, kind).view(np.int16 if kind == np.uint16 else kind)).to(device)
+            a = np.ascontiguousarray(a)
+            if a.dtype != kind:  # (float scales would become zeros)
+                raise TypeError(f"packed and zeros must be uint8, scales uint16 bf16 bits, got {a.dtype}")
+            return torch.as_tensor(a.view(np.int16 if kind is np.uint16 else kind)).to(device)
 
         packed = resident(packed, np.uint8)
         self.N, self.K, self.group, self.zeros = packed.shape[0], 2 * packed.shape[1], int(group), zeros is not None
@@ -695,7 +698,7 @@ def block_norm(h, weight, bias=None, *, branch=None, post_weight=None, post_bias
         _dev_check(post_bias, torch.float32, "post_bias", dev, numel=K)
     channels = 0
     if gate is not None:
-        channels = int(gate.numel() != 1)
+        channels = int(not isinstance(gate, torch.Tensor) or gate.numel() != 1)
         _dev_check(gate, torch.float32, "gate", dev, numel=K if channels else 1)
     rows, xq, xs = _rows_out(out, rows, xq, xs, M, K, dev)
     args = _lib.BLOCK_NORM_ARGS(h.data_ptr(), _ptr(branch), _ptr(post_weight), _ptr(post_bias), _ptr(gate),
