@@ -157,19 +157,19 @@ __device__ __forceinline__ void row_out(const float4 (&v)[NV], int64_t row, int 
     if (threadIdx.x == 0) xs[row] = s;
     // The code is rne(fl(x / s)).  t = x fl(1 / s) differs from x / s by less than
     // 127 2^-23, fl(x / s) by less than 127 2^-24: where t is further than 2^-15
-    // from a border k + 1/2, rne(t) is the code.  A thread with a value nearer
-    // than that (or with 1 / s infinite) divides.
+    // from a border k + 1/2, rne(t) is the code.  Four values of which one is nearer
+    // than that (or 1 / s infinite) divide: few, but where u is a bf16 row but for a
+    // factor, half the row's maximum is an exact tie, which most rows hold.
     const float rs = 1.0f / s;
-    float far = 0.0f;
+    auto code = [&](float x) {
+        return a == 0.0f ? 0u : (uint32_t)(uint8_t)(int8_t)fminf(127.0f, fmaxf(-127.0f, rintf(x / s)));
+    };
     uint32_t q[NV];
 #pragma unroll
-    for (int j = 0; j < NV; ++j) q[j] = codes4(v[j], rs, far);
-    if (!(far <= 0.5f - 0x1p-15f && rs < INFINITY)) {
-        auto code = [&](float x) {
-            return a == 0.0f ? 0u : (uint32_t)(uint8_t)(int8_t)fminf(127.0f, fmaxf(-127.0f, rintf(x / s)));
-        };
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
+    for (int j = 0; j < NV; ++j) {
+        float far = 0.0f;
+        q[j] = codes4(v[j], rs, far);
+        if (!(far <= 0.5f - 0x1p-15f && rs < INFINITY))
             q[j] = code(v[j].x) | code(v[j].y) << 8 | code(v[j].z) << 16 | code(v[j].w) << 24;
     }
 #pragma unroll
