@@ -155,12 +155,14 @@ __device__ __forceinline__ void row_out(const float4 (&v)[NV], int64_t row, int 
     a = block_max<T>(a, slot);
     const float s = a / 127.0f;
     if (threadIdx.x == 0) xs[row] = s;
-    // The code is rne(fl(x / s)).  t = x fl(1 / s) differs from x / s by less than
-    // 127 2^-23, fl(x / s) by less than 127 2^-24: where t is further than 2^-15
+    // The code is rne(fl(x / s)).  t = x rcp(s), the reciprocal good to an ulp, differs
+    // from x / s by less than 127 2^-23, fl(x / s) by less than 127 2^-24: where t is further than 2^-15
     // from a border k + 1/2, rne(t) is the code.  Four values of which one is nearer
     // than that (or 1 / s infinite) divide: few, but where u is a bf16 row but for a
     // factor, half the row's maximum is an exact tie, which most rows hold.
-    const float rs = 1.0f / s;
+    // (s <= 2^121, so that the reciprocal is no subnormal number; that of a
+    // subnormal s may be infinite.)
+    const float rs = __builtin_amdgcn_rcpf(s);
     auto code = [&](float x) {
         return a == 0.0f ? 0u : (uint32_t)(uint8_t)(int8_t)fminf(127.0f, fmaxf(-127.0f, rintf(x / s)));
     };
@@ -183,15 +185,20 @@ __device__ __forceinline__ void row_out(const float4 (&v)[NV], int64_t row, int 
 // rounded to fp32 once: an fp32 sum would depend on its order, and its last
 // bit moves codes across their rounding borders.
 template <int T, int NV, bool kLayer>
-__device__ __forceinline__ void normalise(float4 (&v)[NV], int K, double eps, const float *__restrict__ w,
-                                          const float *__restrict__ b, double *slot) {
+__device__ __forceinline__ void normalise(float4 (&v)[NV], int K, double inv_k, double eps,
+                                          const float *__restrict__ w, const float *__restrict__ b, double *slot) {
     const int n4 = K >> 2;
+    // x / K with inv_k = fl(1 / K): the product and its remainder's share
+    auto mean = [&](double x) {
+        const double m = x * inv_k;
+        return __builtin_fma(__builtin_fma(-m, (double)K, x), inv_k, m);
+    };
     double mu = 0.0, q = 0.0;
     if constexpr (kLayer) {
         double s = 0.0;
 #pragma unroll
         for (int j = 0; j < NV; ++j) s += ((double)v[j].x + (double)v[j].y) + ((double)v[j].z + (double)v[j].w);
-        mu = block_sum<T>(s, slot) / (double)K;
+        mu = mean(block_sum<T>(s, slot));
         slot += T / 64;
     }
     auto square = [&](float x) {
@@ -206,7 +213,12 @@ __device__ __forceinline__ void normalise(float4 (&v)[NV], int K, double eps, co
         square(v[j].z);
         square(v[j].w);
     }
-    const float r = (float)(1.0 / sqrt(block_sum<T>(q, slot) / (double)K + eps));
+    // 1 / sqrt(d): two Newton steps on the hardware's estimate, to a relative 2^-51
+    const double d = mean(block_sum<T>(q, slot)) + eps;
+    double y = __builtin_amdgcn_rsq(d);
+    y = __builtin_fma(0.5 * y, __builtin_fma(-d * y, y, 1.0), y);
+    y = __builtin_fma(0.5 * y, __builtin_fma(-d * y, y, 1.0), y);
+    const float r = (float)y;
     const float m = (float)mu;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -268,7 +280,7 @@ __device__ __forceinline__ float tanh_rounded(float g) {
 // LDS and the same workgroup for every width).  More than one row a workgroup (the
 // weights kept in registers, the next row's loads ahead) takes 172 registers and 31 us.
 template <int T, int NV, bool kLayer>
-__global__ __launch_bounds__(T) void block_norm_kernel(const s3d8_block_norm_args p) {
+__global__ __launch_bounds__(T) void block_norm_kernel(const s3d8_block_norm_args p, double inv_k) {
     __shared__ double sums[4][T / 64];
     __shared__ float maxima[T / 64];
     const int64_t row = blockIdx.x;
@@ -289,7 +301,7 @@ __global__ __launch_bounds__(T) void block_norm_kernel(const s3d8_block_norm_arg
     if (p.branch) {
         float4 t[NV];
         load(t, p.branch, p.branch_type == S3D8_ROWS_BF16);
-        if (p.post_weight) normalise<T, NV, kLayer>(t, K, p.eps, p.post_weight, p.post_bias, sums[0]);
+        if (p.post_weight) normalise<T, NV, kLayer>(t, K, inv_k, p.eps, p.post_weight, p.post_bias, sums[0]);
         if (p.gate) {
             const bool one = !p.gate_channels, squash = p.gate_tanh;
             const float g1 = one ? (squash ? tanh_rounded(*p.gate) : *p.gate) : 1.0f;
@@ -326,7 +338,7 @@ __global__ __launch_bounds__(T) void block_norm_kernel(const s3d8_block_norm_arg
             }
         }
     }
-    normalise<T, NV, kLayer>(h, K, p.eps, p.weight, p.bias, sums[2]);
+    normalise<T, NV, kLayer>(h, K, inv_k, p.eps, p.weight, p.bias, sums[2]);
     row_out<T, NV>(h, row, K, p.out_type, p.rows, p.xq, p.xs, maxima);
 }
 
@@ -357,7 +369,7 @@ __device__ __forceinline__ float gated_near(float g, float u) {
 // but with gated() (some 45 instructions) only where fp32 cannot tell:
 //   - the row's maximum is gated() of the elements whose gated_near() is
 //     within 2^-18 of the largest one (the true maximum's is within 2^-19);
-//   - t = near fl(1 / s) is off from x / s by less than 127 (2^-20 + 2^-22) < 2^-12.6,
+//   - t = near rcp(s) is off from x / s by less than 127 (2^-20 + 2^-22) < 2^-12.6,
 //     fl(x / s) by 127 2^-24: where t is further than 2^-12 from a border k + 1/2
 //     its nearest integer is the code (all but one value in 2^11).
 // Both kinds go through a list in LDS, so that the few of them take one pass of
@@ -408,7 +420,7 @@ __device__ __forceinline__ bool glu_codes(const Raw<kBF> (&g4)[NV], const Raw<kB
     for (int k = threadIdx.x; k < 4 * listed; k += T) a = fmaxf(a, fabsf(gated(gl[k], ul[k])));
     a = block_max<T>(a, slots[1]);
     lds_barrier();
-    const float s = a / 127.0f, rs = 1.0f / s;
+    const float s = a / 127.0f, rs = __builtin_amdgcn_rcpf(s);
     if (threadIdx.x == 0) xs[row] = s;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -548,7 +560,7 @@ int32_t s3d8_block_norm(const s3d8_block_norm_args *args, void *stream) {
     int threads = 0;
     const auto fn = a.kind == S3D8_NORM_LAYER ? row_kernel<BlockNorm<true>>(a.M, a.K, cus, 7, threads)
                                               : row_kernel<BlockNorm<false>>(a.M, a.K, cus, 7, threads);
-    hipLaunchKernelGGL(fn, dim3((unsigned)a.M), dim3(threads), 0, (hipStream_t)stream, a);
+    hipLaunchKernelGGL(fn, dim3((unsigned)a.M), dim3(threads), 0, (hipStream_t)stream, a, 1.0 / (double)a.K);
     return s3d8::launch_status();
 }
 
