@@ -6,7 +6,7 @@
 // reductions, and is written once.  So the bytes moved are the floor, but the
 // arithmetic is close to it: statistics and values are held in 64 bits so that
 // the codes are the correctly rounded ones, and vector instructions issue most
-// of the time a launch takes (84% and 87% at the large sizes below).
+// of the time a launch takes (72% and 84% at the large sizes below).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -193,7 +193,7 @@ __device__ __forceinline__ void normalise(float4 (&v)[NV], int K, double inv_k, 
         const double m = x * inv_k;
         return __builtin_fma(__builtin_fma(-m, (double)K, x), inv_k, m);
     };
-    double mu = 0.0, q = 0.0;
+    double mu = 0.0;
     if constexpr (kLayer) {
         double s = 0.0;
 #pragma unroll
@@ -201,20 +201,21 @@ __device__ __forceinline__ void normalise(float4 (&v)[NV], int K, double inv_k, 
         mu = mean(block_sum<T>(s, slot));
         slot += T / 64;
     }
-    auto square = [&](float x) {
+    double qs[2] = {0.0, 0.0};  // two chains
+    auto square = [&](float x, double &q) {
         const double y = kLayer ? (double)x - mu : (double)x;
         q = __builtin_fma(y, y, q);
     };
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         if (kLayer && (int)threadIdx.x + j * T >= n4) continue;  // (past the row v is 0, not mu)
-        square(v[j].x);
-        square(v[j].y);
-        square(v[j].z);
-        square(v[j].w);
+        square(v[j].x, qs[0]);
+        square(v[j].y, qs[1]);
+        square(v[j].z, qs[0]);
+        square(v[j].w, qs[1]);
     }
     // 1 / sqrt(d): two Newton steps on the hardware's estimate, to a relative 2^-51
-    const double d = mean(block_sum<T>(q, slot)) + eps;
+    const double d = mean(block_sum<T>(qs[0] + qs[1], slot)) + eps;
     double y = __builtin_amdgcn_rsq(d);
     y = __builtin_fma(0.5 * y, __builtin_fma(-d * y, y, 1.0), y);
     y = __builtin_fma(0.5 * y, __builtin_fma(-d * y, y, 1.0), y);
@@ -224,12 +225,15 @@ __device__ __forceinline__ void normalise(float4 (&v)[NV], int K, double inv_k, 
     for (int j = 0; j < NV; ++j) {
         const int i = threadIdx.x + j * T;
         if (i >= n4) continue;
+        // both vectors asked for before either is used
+        const float4 wv = reinterpret_cast<const float4 *>(w)[i];
+        float4 bv;
+        if (kLayer && b) bv = reinterpret_cast<const float4 *>(b)[i];
         float4 u = v[j];
         if constexpr (kLayer) u = map4(u, [&](float x) { return x - m; });
-        u = zip4(map4(u, [&](float x) { return x * r; }), reinterpret_cast<const float4 *>(w)[i],
-                 [](float x, float y) { return x * y; });
+        u = zip4(map4(u, [&](float x) { return x * r; }), wv, [](float x, float y) { return x * y; });
         if constexpr (kLayer)
-            if (b) u = zip4(u, reinterpret_cast<const float4 *>(b)[i], [](float x, float y) { return x + y; });
+            if (b) u = zip4(u, bv, [](float x, float y) { return x + y; });
         v[j] = u;
     }
 }
@@ -274,11 +278,14 @@ __device__ __forceinline__ float tanh_rounded(float g) {
 // codes, with the row in registers from the loads to the last store.
 //
 // Measured, RMS with a branch and its post norm, codes out: 2048 x 4096 in bf16
-// 17.4 us (58.7 MB at 3.4 TB/s), one row 3.3 us; layer norm, 1601 x 1280 in
-// fp32 with a gate, 9.4 us.  51 vector instructions per element of the first
-// issue 84% of its time, most of them 64-bit (34 us with sums by shuffles through
-// LDS and the same workgroup for every width).  More than one row a workgroup (the
-// weights kept in registers, the next row's loads ahead) takes 172 registers and 31 us.
+// 15.4 us (58.7 MB at 3.8 TB/s), 17.2 with operands in no cache; RMS of one row
+// 2.8 us; layer norm, 1601 x 1280 in fp32 with a gate, 8.9 us.  33 vector
+// instructions per element of the first issue 72% of its time, most of them
+// 64-bit (34 us with sums by shuffles through LDS and the same workgroup for every
+// width).  The weights loaded before the sums rather than after them gain at some
+// sizes what they lose at others (8192 x 4096: 52.8 us for 56.3, 1601 x 5120: 25.7
+// for 24.9).  More than one row a workgroup (the weights kept in registers, the
+// next row's loads ahead) takes 172 registers and 31 us.
 template <int T, int NV, bool kLayer>
 __global__ __launch_bounds__(T) void block_norm_kernel(const s3d8_block_norm_args p, double inv_k) {
     __shared__ double sums[4][T / 64];
@@ -296,15 +303,18 @@ __global__ __launch_bounds__(T) void block_norm_kernel(const s3d8_block_norm_arg
             load_row<T, NV, false>(v, x, base, n4);
         }
     };
+    // one gate for all: by a scalar load, and its tanh while the row is on its way
+    const bool one = !p.gate_channels, squash = p.gate_tanh;
+    float g1 = 1.0f;
+    if (p.gate && one) g1 = *p.gate;
     float4 h[NV];
     load(h, p.h, p.h_type == S3D8_ROWS_BF16);
     if (p.branch) {
         float4 t[NV];
         load(t, p.branch, p.branch_type == S3D8_ROWS_BF16);
+        if (squash) g1 = tanh_rounded(g1);
         if (p.post_weight) normalise<T, NV, kLayer>(t, K, inv_k, p.eps, p.post_weight, p.post_bias, sums[0]);
         if (p.gate) {
-            const bool one = !p.gate_channels, squash = p.gate_tanh;
-            const float g1 = one ? (squash ? tanh_rounded(*p.gate) : *p.gate) : 1.0f;
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 const int i = threadIdx.x + j * T;
@@ -444,7 +454,7 @@ __device__ __forceinline__ bool glu_codes(const Raw<kBF> (&g4)[NV], const Raw<kB
 }
 
 // One workgroup per row.  Measured in bf16, codes out: 2048 x 14336 33 us (147 MB
-// at 4.5 TB/s; 27.5 vector instructions per element, issuing 87% of the time),
+// at 4.5 TB/s; 27 vector instructions per element, issuing 84% of the time),
 // 58.7 us with gated() for every element; one row of 14336 in fp32 5.2 us,
 // 5 x 1744 to fp32 2.5 us (both little more than a launch and their latency).
 template <int T, int NV, bool kBF>
