@@ -6,7 +6,7 @@
 // reductions, and is written once.  So the bytes moved are the floor, but the
 // arithmetic is close to it: statistics and values are held in 64 bits so that
 // the codes are the correctly rounded ones, and vector instructions issue most
-// of the time a launch takes (72% and 84% at the large sizes below).
+// of the time a launch takes (70% and 84% at the large sizes below).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -278,9 +278,9 @@ __device__ __forceinline__ float tanh_rounded(float g) {
 // codes, with the row in registers from the loads to the last store.
 //
 // Measured, RMS with a branch and its post norm, codes out: 2048 x 4096 in bf16
-// 15.4 us (58.7 MB at 3.8 TB/s), 17.2 with operands in no cache; RMS of one row
-// 2.8 us; layer norm, 1601 x 1280 in fp32 with a gate, 8.9 us.  33 vector
-// instructions per element of the first issue 72% of its time, most of them
+// 15.1 us (58.7 MB at 3.9 TB/s), 17.2 with operands in no cache; RMS of one row
+// 2.9 us; layer norm, 1601 x 1280 in fp32 with a gate, 8.9 us.  34 vector
+// instructions per element of the first issue 70% of its time, most of them
 // 64-bit (34 us with sums by shuffles through LDS and the same workgroup for every
 // width).  The weights loaded before the sums rather than after them gain at some
 // sizes what they lose at others (8192 x 4096: 52.8 us for 56.3, 1601 x 5120: 25.7

@@ -319,8 +319,8 @@ __global__ __launch_bounds__(kRowWaves * 64) void w4_rows_kernel(
 // multiply-add (2 P per result and block of 128) beside the product itself.
 // The 32 x 32 products take half the issue slots of 16 x 16 ones per
 // multiplication, and their K = 32 serves 32-column groups at full rate.
-// 2048 x 4096 -> 14336 takes 159 us with groups of 64 (1.51 PFLOP/s; 159 to 173 by
-// card), 132 with 128, 230 with 32 and zero points: at 64, vector
+// 2048 x 4096 -> 14336 takes 159 us with groups of 64 (1.51 POP/s; 157 to 187 by
+// card and by how long it has been running), 132 with 128, 230 with 32 and zero points: at 64, vector
 // instructions issue 96% of the time and the matrix cores run 37% of it, LDS has
 // no bank conflict.
 //
