@@ -441,7 +441,8 @@ int32_t s3d8_dequant_ex(const uint8_t *packed, const void *table, int32_t format
  * half to even):
  *   zeros NULL:  a = max |w|, s = bf16(a / 7), q = clamp(rne(w / s), -8, 7) + 8;
  *   otherwise:   lo = min(0, min w), hi = max(0, max w), s = bf16((hi - lo) / 15),
- *                z = clamp(rne(-lo / s), 0, 15), q = clamp(rne(w / s) + z, 0, 15).
+ *                z = clamp(rne(-lo / s), 0, 15), q = clamp(rne(w / s) + z, 0, 15);
+ *                where hi - lo is over the largest fp32, s = bf16(hi / 15 - lo / 15).
  * A group whose scale is 0 has every code at its zero point (z = 8 there).
  *   W            host fp32 [N][K], row-major, finite.
  *   group        columns per scale, a positive multiple of 32.

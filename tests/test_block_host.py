@@ -172,3 +172,25 @@ def test_glu_refusals():
     assert call(xq=A + 8) == ALIGN and call(xs=A + 1) == ALIGN
     assert call(rows=A) == INVALID and call(xq=None) == INVALID and call(o=1) == INVALID
     assert call(o=0, rows=A + 8, xq=None, xs=None) == ALIGN
+
+
+def test_encode_ranges_past_the_largest_fp32():
+    """Finite groups whose hi - lo is over the largest fp32: a finite scale, the codes of the definition with it."""
+    ends = [(3.0e38, -3.0e38), (2.5e38, -1.5e38), (1.0e38, -3.25e38), (3.4028235e38, -3.4028235e38)]
+    W = np.zeros((len(ends), 32), np.float32)
+    for r, (hi, lo) in enumerate(ends):
+        W[r] = np.linspace(lo, hi, 32, dtype=np.float64).astype(np.float32)
+    packed, scales, z = w4_encode(W, 32, True)
+    wide = W.astype(np.float64)
+    # the range in 64 bits; rounded to fp32, then to bf16 (none of these lies near a border of the latter)
+    s = ref.bf16_bits(((wide.max(1) - wide.min(1)) / 15).astype(np.float32))
+    assert np.array_equal(scales[:, 0], s)
+    step = ref.bf16_value(s).astype(np.float64)[:, None]
+    z_r = np.clip(np.rint(-wide.min(1, keepdims=True) / step), 0, 15)
+    q_r = np.clip(np.rint(wide / step) + z_r, 0, 15).astype(np.uint8)
+    assert np.array_equal(z, z_r) and np.array_equal(packed, ref.pack(q_r))
+    # without zero points the largest magnitude decides, which cannot overflow
+    packed, scales, _ = w4_encode(W, 32)
+    q_r, s_r, _ = ref.w4_encode(W, 32, False)
+    assert np.isfinite(ref.bf16_value(scales)).all()
+    assert np.array_equal(scales, s_r) and np.array_equal(packed, ref.pack(q_r))

@@ -328,7 +328,8 @@ void encode_group(const float *w, int64_t n, bool affine, uint16_t *scale, uint8
         lo = std::min(lo, w[j]);
         hi = std::max(hi, w[j]);
     }
-    *scale = bf16_from_f32(affine ? (hi - lo) / 15.0f : std::max(hi, -lo) / 7.0f);
+    const float range = std::isfinite(hi - lo) ? (hi - lo) / 15.0f : hi / 15.0f - lo / 15.0f;
+    *scale = bf16_from_f32(affine ? range : std::max(hi, -lo) / 7.0f);
     const float s = f32_from_bf16(*scale);
     auto clamped = [](float v) { return std::min(15.0f, std::max(0.0f, v)); };
     *zero = affine && s != 0.0f ? (uint8_t)clamped(std::nearbyint(-lo / s)) : 8;
