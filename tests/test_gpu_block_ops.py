@@ -408,3 +408,22 @@ def test_gate_must_be_a_tensor(gpu):
     w = torch.ones(64, device=gpu)
     with pytest.raises(TypeError):
         s3d8.block_norm(h, w, branch=h.clone(), gate=0.5)
+
+
+def test_norm_gate_of_nan(gpu):
+    """tanh(NaN) is NaN: a scalar gate spoils every row, a channel's its channel of h'."""
+    M, K = 3, 64
+    g = rng(7310)
+    h, br, w = rows(g, M, K, False), rows(g, M, K, False, 0.5), np.ones(K, F)
+    args = dict(branch=dev(br, gpu), tanh_gate=True, out="f32")
+    for kind in ("rms", "layer"):
+        for bad in (np.nan, -np.nan):
+            h1, u = s3d8.block_norm(dev(h, gpu), dev(w, gpu), gate=dev(np.full(1, bad, F), gpu), kind=kind, **args)
+            assert h1.isnan().all() and u.isnan().all()
+            gate = g.standard_normal(K).astype(F)
+            gate[[0, 37]] = bad
+            h1, u = s3d8.block_norm(dev(h, gpu), dev(w, gpu), gate=dev(gate, gpu), kind=kind, **args)
+            at = np.isnan(gate)
+            assert np.array_equal(h1.isnan().cpu().numpy(), np.broadcast_to(at, (M, K))) and u.isnan().all()
+            h_r, _ = ref.block_norm(h, w, None, br, None, None, np.where(at, F(0), gate), True)
+            same(h1[:, torch.from_numpy(~at).to(gpu)], h_r[:, ~at])

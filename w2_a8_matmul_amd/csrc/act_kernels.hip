@@ -267,11 +267,12 @@ __device__ __forceinline__ double reciprocal(double d) {
     return __builtin_fma(q, __builtin_fma(-d, q, 1.0), q);
 }
 
-// tanh(g) = (e^2g - 1) / (e^2g + 1) in 64 bits, rounded to fp32.
+// tanh(g) = (e^2g - 1) / (e^2g + 1) in 64 bits, rounded to fp32.  (The clamp takes a NaN to
+// a bound.)
 __device__ __forceinline__ float tanh_rounded(float g) {
     const Exp e = exp_parts(2.0 * (double)__builtin_amdgcn_fmed3f(g, -20.0f, 20.0f));
     const double m = __builtin_fma(e.two_n, e.less_one, e.two_n - 1.0);
-    return __builtin_copysignf((float)(m * reciprocal(m + 2.0)), g);
+    return g != g ? g : __builtin_copysignf((float)(m * reciprocal(m + 2.0)), g);
 }
 
 // One workgroup per row: h += gate * norm(branch), then the norm of h and its
