@@ -427,3 +427,25 @@ def test_norm_gate_of_nan(gpu):
             assert np.array_equal(h1.isnan().cpu().numpy(), np.broadcast_to(at, (M, K))) and u.isnan().all()
             h_r, _ = ref.block_norm(h, w, None, br, None, None, np.where(at, F(0), gate), True)
             same(h1[:, torch.from_numpy(~at).to(gpu)], h_r[:, ~at])
+
+
+@pytest.mark.parametrize("K", [64, 1040, 4096, 14336])
+def test_codes_of_rows_past_the_largest_fp32(gpu, K):
+    """Finite operands whose product overflows: the codes and scale that quant_act makes of the infinite values."""
+    g = rng(7311, K)
+    up, gate = rows(g, 4, K, False), np.full((4, K), 50.0, F)
+    gate[0, 3], up[0, 3] = 1e30, 1e30
+    gate[1, [0, K - 1]], up[1, [0, K - 1]] = 3e38, (-3e38, 3e38)
+    gate[2], up[2] = 1e25, 1e25
+    a = s3d8.glu_act(dev(gate, gpu), dev(up, gpu), out="f32")
+    same(a, np.where(np.isinf(a.cpu().numpy()), np.copysign(F(np.inf), up), ref.glu(gate, np.where(gate > 60, F(0), up))))
+    assert a.isinf().sum(1).tolist() == [1, 2, K, 0]
+    for got, want in zip(s3d8.glu_act(dev(gate, gpu), dev(up, gpu)), s3d8.quant_act(a)):
+        same(got, want.cpu().numpy())
+    h, w, b = rows(g, 3, K, False), np.full(K, 3e38, F), np.full(K, 3e38, F)
+    for kind in ("rms", "layer"):
+        bias = dev(b, gpu) if kind == "layer" else None
+        u = s3d8.block_norm(dev(h, gpu), dev(w, gpu), bias, kind=kind, out="f32")
+        assert u.isinf().any(1).all() and not u.isnan().any()
+        for got, want in zip(s3d8.block_norm(dev(h, gpu), dev(w, gpu), bias, kind=kind), s3d8.quant_act(u)):
+            same(got, want.cpu().numpy())

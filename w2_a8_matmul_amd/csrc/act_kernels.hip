@@ -158,11 +158,12 @@ __device__ __forceinline__ void row_out(const float4 (&v)[NV], int64_t row, int 
     // The code is rne(fl(x / s)).  t = x rcp(s), the reciprocal good to an ulp, differs
     // from x / s by less than 127 2^-23, fl(x / s) by less than 127 2^-24: where t is further than 2^-15
     // from a border k + 1/2, rne(t) is the code.  Four values of which one is nearer
-    // than that (or 1 / s infinite) divide: few, but where u is a bf16 row but for a
+    // than that (or 1 / s infinite or 0) divide: few, but where u is a bf16 row but for a
     // factor, half the row's maximum is an exact tie, which most rows hold.
-    // (s <= 2^121, so that the reciprocal is no subnormal number; that of a
-    // subnormal s may be infinite.)
+    // (A finite s is at most 2^121, so that its reciprocal is no subnormal number; that of
+    // a subnormal s may be infinite, and finite operands can have infinite products.)
     const float rs = __builtin_amdgcn_rcpf(s);
+    const bool usable = rs > 0.0f && rs < INFINITY;
     auto code = [&](float x) {
         return a == 0.0f ? 0u : (uint32_t)(uint8_t)(int8_t)fminf(127.0f, fmaxf(-127.0f, rintf(x / s)));
     };
@@ -171,7 +172,7 @@ __device__ __forceinline__ void row_out(const float4 (&v)[NV], int64_t row, int 
     for (int j = 0; j < NV; ++j) {
         float far = 0.0f;
         q[j] = codes4(v[j], rs, far);
-        if (!(far <= 0.5f - 0x1p-15f && rs < INFINITY))
+        if (!(far <= 0.5f - 0x1p-15f && usable))
             q[j] = code(v[j].x) | code(v[j].y) << 8 | code(v[j].z) << 16 | code(v[j].w) << 24;
     }
 #pragma unroll
