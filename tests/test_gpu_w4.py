@@ -256,3 +256,35 @@ def test_module_refuses_other_types(gpu):
                  (ref.pack(q), scales, 64, z.astype(np.float32))):
         with pytest.raises(TypeError):
             s3d8.W4Linear(*args, device=gpu)
+
+
+@pytest.mark.parametrize("M", [1, 6, 12, 40, 200])
+@pytest.mark.parametrize("group,zeros", [(32, False), (64, False), (128, False), (64, True)])
+def test_scales_at_the_ends_of_their_range(gpu, M, group, zeros):
+    """Sums close to the largest fp32 (2^126.9) and subnormal scales: what the definition says is finite or exact stays so."""
+    N, K = 48, 512
+    G = K // group
+    q = np.zeros((N, K), np.uint8)
+    q[1::2] = 15
+    z = np.full((N, G), 8, np.uint8) if zeros else None
+    xq = np.full((M, K), 127, np.int8)
+    xq[M // 2] = -96
+    # every partial sum is an integer below 2^20 times the scale: exact in fp32
+    for exponent, x_exponent in ((107, -100), (-133, 60)):
+        scales = np.full((N, G), ref.bf16_bits(np.float32(2.0 ** exponent)), np.uint16)
+        xs = np.full((M,), 2.0 ** x_exponent, np.float32)
+        lin = tiled_on(gpu, q, scales, z, group)
+        y = lin.linear(torch.from_numpy(xq).to(gpu), torch.from_numpy(xs).to(gpu))
+        y_r, _ = ref.w4_linear(xq, xs, q, scales, z, group)
+        assert np.isfinite(y_r).all() and (np.abs(y_r) >= 2.0 ** -126).all()
+        assert np.array_equal(y.double().cpu().numpy(), y_r)
+    # random codes and scales, sums of up to 2^127
+    g = rng(7204, M, group)
+    q = g.integers(0, 16, (N, K), dtype=np.uint8)
+    scales = ref.bf16_bits((g.lognormal(0, 0.3, (N, G)) * 2.0 ** 111).astype(np.float32))
+    xq, _ = codes(M, K, 3)
+    xs = np.full((M,), 2.0 ** -90, np.float32)
+    y_r, size = ref.w4_linear(xq, xs, q, scales, z, group)
+    assert (size * 2.0 ** 90 < 2.0 ** 127).all()
+    lin = tiled_on(gpu, q, scales, z, group)
+    check(lin.linear(torch.from_numpy(xq).to(gpu), torch.from_numpy(xs).to(gpu)), xq, xs, q, scales, z, group)

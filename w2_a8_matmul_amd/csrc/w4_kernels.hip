@@ -29,8 +29,10 @@ namespace {
 // v_mfma_i32_16x16x32_i8, whose sum stays inside one 32-column group.
 // Without zero points the nibbles are q - 8 in two's complement: masked into
 // the high half of a byte they are 16 (q - 8), an INT8 operand in one or two
-// instructions for four weights, and the factor 16 is taken out of the fp32
-// sum (exactly).  With zero points the nibbles are q.
+// instructions for four weights, and the factor 16 is taken out of the scale
+// (exactly: a bf16 scale is a multiple of 2^-133, a sixteenth of it an fp32 number;
+// taken out of the sum instead, it made sums over 2^124 infinite).  With zero points the
+// nibbles are q.
 //
 // The scales follow the fragments: P = 1, 2 or 4 per channel and block (the
 // group size a multiple of 128, of 64 or of 32; larger groups repeat theirs),
@@ -110,6 +112,13 @@ __device__ __forceinline__ int32_t nibbles(uint32_t w, int h, uint32_t zrep) {
     } else {
         return (int32_t)((h ? w : w << 4) & 0xF0F0F0F0u);
     }
+}
+
+// What an INT32 sum of such operands is multiplied by, from a scale's bits in the upper
+// half of a dword.
+template <bool kZeros>
+__device__ __forceinline__ float scale_of(uint32_t bits) {
+    return kZeros ? __uint_as_float(bits) : __uint_as_float(bits) * 0.0625f;
 }
 
 // --------------------------------------------------------------- product, few rows
@@ -206,7 +215,7 @@ __global__ __launch_bounds__(kRowWaves * 64) void w4_rows_kernel(
         for (int t = 0; t < NT; ++t) {
             const uint32_t wv[4] = {st.w[t].x, st.w[t].y, st.w[t].z, st.w[t].w};
             auto add = [&](const v4i &c, uint32_t sbits) {
-                const float s = __uint_as_float(sbits << 16);
+                const float s = scale_of<kZeros>(sbits << 16);
 #pragma unroll
                 for (int i = 0; i < Q; ++i) sum[t][i] = __builtin_fmaf(s, (float)c[i], sum[t][i]);
             };
@@ -253,7 +262,6 @@ __global__ __launch_bounds__(kRowWaves * 64) void w4_rows_kernel(
 #pragma unroll
     for (int d = 0; d < kDepth; ++d) load_next(ring[d]);
 
-    const float post = kZeros ? 1.0f : 0.0625f;
     auto clear = [&]() {
 #pragma unroll
         for (int t = 0; t < NT; ++t)
@@ -288,7 +296,7 @@ __global__ __launch_bounds__(kRowWaves * 64) void w4_rows_kernel(
                 float v = 0.0f;
                 for (int w = 0; w < KS; ++w) v += at[w * (NT * Q * 64)];
                 if (m < M && c < N) {
-                    v = xs[m] * (v * post);
+                    v = xs[m] * v;
                     if (obf)
                         static_cast<uint16_t *>(y)[(int64_t)m * N + c] = f32_to_bf16_rne(v);
                     else
@@ -442,7 +450,7 @@ __device__ __forceinline__ void w4_gemm_tile(GemmLds<KP, S, kZeros, kARows> &lds
         uint32_t z[P];
 #pragma unroll
         for (int p = 0; p < P; ++p) {
-            s[p] = __uint_as_float(p & 1 ? sv[p >> 1] & 0xFFFF0000u : sv[p >> 1] << 16);
+            s[p] = scale_of<kZeros>(p & 1 ? sv[p >> 1] & 0xFFFF0000u : sv[p >> 1] << 16);
             z[p] = kZeros ? ((zv >> (8 * p)) & 0xFFu) * 0x01010101u : 0u;
         }
         // operand j of the block's four (j = 2 half + s, or the 32-column group)
@@ -527,14 +535,13 @@ __device__ __forceinline__ void w4_gemm_tile(GemmLds<KP, S, kZeros, kARows> &lds
     const uint32_t size = obf ? 2u : 4u, rowb = size * (uint32_t)N;
     const auto ry = make_rsrc(static_cast<char *>(y) + (int64_t)wrow * N * size, rowb * (uint32_t)nrows);
     const auto rxs = make_rsrc(xs + wrow, 4u * (uint32_t)nrows);
-    const float post = kZeros ? 1.0f : 0.0625f;
     const int ch = 16 * tile0 + n;
     const uint32_t base = ch < N ? 4u * h * rowb + size * (uint32_t)ch : kOOB;
 #pragma unroll
     for (int o = 0; o < TO; ++o) {
         const uint4 sx = bload16(rxs, 32u * o + 16u * h);
-        const float f[4] = {__uint_as_float(sx.x) * (out[o].x * post), __uint_as_float(sx.y) * (out[o].y * post),
-                            __uint_as_float(sx.z) * (out[o].z * post), __uint_as_float(sx.w) * (out[o].w * post)};
+        const float f[4] = {__uint_as_float(sx.x) * out[o].x, __uint_as_float(sx.y) * out[o].y,
+                            __uint_as_float(sx.z) * out[o].z, __uint_as_float(sx.w) * out[o].w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const uint32_t off = base + (uint32_t)(8 * o + e) * rowb;
