@@ -549,7 +549,7 @@ typedef struct s3d8_block_norm_args {
  * sums in 64 bits keep them from depending on the order of summation.)
  * K is a positive multiple of 16, at most 65536; at most 524288 rows.  Row
  * matrices must be 16-B aligned, fp32 vectors [K] as well; values finite,
- * eps > 0.  Outputs other than h_out = h must not overlap inputs.
+ * eps from 2^-252 to 2^252.  Outputs other than h_out = h must not overlap inputs.
  * Errors: INVALID_ARG, SHAPE, ALIGN, DEVICE, HIP. */
 int32_t s3d8_block_norm(const s3d8_block_norm_args *args, void *stream);
 

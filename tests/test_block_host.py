@@ -194,3 +194,18 @@ def test_encode_ranges_past_the_largest_fp32():
     q_r, s_r, _ = ref.w4_encode(W, 32, False)
     assert np.isfinite(ref.bf16_value(scales)).all()
     assert np.array_equal(scales, s_r) and np.array_equal(packed, ref.pack(q_r))
+
+
+def test_block_norm_eps_range():
+    """1 / sqrt(eps), what a zero row is multiplied by, has to be a finite fp32 number, and not 0."""
+    good = dict(h=A, weight=A, xq=A + 8, xs=A, M=2, K=64, residual_scale=1.0, kind=0, h_type=0, branch_type=0,
+                out_type=2)  # (xq is misaligned, which is refused after eps)
+
+    def call(eps):
+        args = _lib.BlockNormArgs(**good, eps=eps)
+        return _rc("s3d8_block_norm", ctypes.addressof(args), None)
+
+    for eps in (float("inf"), 1e-80, 5e-324, 2.0 ** -252 * (1 - 2.0 ** -52), 2.0 ** 252 * (1 + 2.0 ** -52)):
+        assert call(eps) == INVALID, eps
+    for eps in (2.0 ** -252, 1e-12, 1e-5, 1.0, 2.0 ** 252):
+        assert call(eps) == ALIGN, eps

@@ -557,7 +557,9 @@ int32_t s3d8_block_norm(const s3d8_block_norm_args *args, void *stream) {
     if (a.post_bias && !a.post_weight) return s3d8::fail(S3D8_ERR_INVALID_ARG, "post_bias needs post_weight");
     if (!row_type(a.h_type) || (a.branch && !row_type(a.branch_type)))
         return s3d8::fail(S3D8_ERR_INVALID_ARG, "unknown row type");
-    if (!(a.eps > 0.0)) return s3d8::fail(S3D8_ERR_INVALID_ARG, "eps must be positive");
+    // 1 / sqrt(eps), a zero row's factor, is then between 2^-126 and 2^126 (infinite, it made zeros NaN)
+    if (!(a.eps >= 0x1p-252 && a.eps <= 0x1p252))
+        return s3d8::fail(S3D8_ERR_INVALID_ARG, "eps must be positive (2^-252 to 2^252)");
     int rc = check_rows(a.M, a.K);
     if (rc) return rc;
     rc = check_out(a.out_type, a.rows, a.xq, a.xs);
