@@ -481,7 +481,9 @@ int32_t s3d8_w4_tile(const uint8_t *packed, const uint16_t *scales_bf16, const u
  *   xs           device fp32 [M].
  *   tiled        device, from s3d8_w4_tile, 16-B aligned.
  *   tiled_bytes  its size: exactly s3d8_w4_tiled_bytes(N, K, group, has_zeros),
- *                so that a matrix laid out for other arguments is refused.
+ *                so that a matrix laid out for other arguments is refused where
+ *                they change the size (sizes that round up to the same multiples
+ *                of 16 channels and 128 columns do not: the caller keeps N and K).
  *   group, has_zeros   as the matrix was laid out.
  *   y            out, device [M][N] of fp32 or bf16 (per out_type).
  *   out_type     S3D8_OUT_F32 or S3D8_OUT_BF16.

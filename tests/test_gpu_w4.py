@@ -288,3 +288,19 @@ def test_scales_at_the_ends_of_their_range(gpu, M, group, zeros):
     assert (size * 2.0 ** 90 < 2.0 ** 127).all()
     lin = tiled_on(gpu, q, scales, z, group)
     check(lin.linear(torch.from_numpy(xq).to(gpu), torch.from_numpy(xs).to(gpu)), xq, xs, q, scales, z, group)
+
+
+def test_module_refuses_activations_of_another_width(gpu):
+    """Widths that end in the same block of 128 columns have tiled matrices of one size: the module knows its own."""
+    N, K = 40, 240
+    q, scales, z = matrix(N, K, 64, False)
+    lin = tiled_on(gpu, q, scales, z, 64)
+    for wrong in (144, 224, 256, 272):
+        xq, xs = (torch.from_numpy(t).to(gpu) for t in codes(3, wrong))
+        with pytest.raises(s3d8.S3D8Error):
+            lin.linear(xq, xs)
+        with pytest.raises(s3d8.S3D8Error):
+            lin(torch.zeros((3, wrong), device=gpu))
+    xq, xs = codes(3, K)
+    check(lin.linear(torch.from_numpy(xq).to(gpu), torch.from_numpy(xs).to(gpu)), xq, xs, q, scales, z, 64)
+    assert not lin(torch.zeros((3, K), device=gpu)).any()

@@ -548,8 +548,10 @@ def w4_tile(packed, scales, group: int, zeros=None, tiled=None):
 
 def w4_linear(xq, xs, tiled, N: int, group: int, zeros: bool = False, y=None, out: str = "f32"):
     """Linear layer on a tiled W4 matrix and pre-quantised activations: y [M][N],
-    fp32 or bf16.  ``group`` and ``zeros`` (whether the matrix has zero points)
-    as it was laid out."""
+    fp32 or bf16.  ``N``, ``group``, ``zeros`` (whether the matrix has zero points)
+    and the width of ``xq`` as it was laid out: the size of ``tiled`` shows a
+    mismatch only where it changes the number of 16-channel tiles, of 128-column
+    blocks or of scales per block (a W4Linear knows its width)."""
     _dev_check(tiled, _torch().uint8, "tiled")
     return _w4_linear(xq, xs, tiled, N, group, zeros, y, out)
 
@@ -612,10 +614,17 @@ class W4Linear:
         packed, scales, z = w4_encode(W, group, zeros)
         return cls(packed, scales, group, z, device)
 
+    def _check_width(self, x, func):
+        # the size of the tiled matrix tells widths apart only by their number of 128-column blocks
+        if isinstance(x, _torch().Tensor) and x.dim() == 2 and x.shape[1] != self.K:
+            raise S3D8Error(_lib.S3D8_ERR_INVALID_ARG, func, f"activations of {x.shape[1]} columns, weights of {self.K}")
+
     def linear(self, xq, xs, y=None, out: str = "f32"):
+        self._check_width(xq, "s3d8_w4_linear")
         return _w4_linear(xq, xs, self.tiled, self.N, self.group, self.zeros, y, out)
 
     def __call__(self, x, out: str = "f32"):
+        self._check_width(x, "s3d8_w4_forward")
         return w4_forward(x, self.tiled, self.N, self.group, self.zeros, out=out)
 
 
