@@ -304,3 +304,20 @@ def test_module_refuses_activations_of_another_width(gpu):
     xq, xs = codes(3, K)
     check(lin.linear(torch.from_numpy(xq).to(gpu), torch.from_numpy(xs).to(gpu)), xq, xs, q, scales, z, 64)
     assert not lin(torch.zeros((3, K), device=gpu)).any()
+
+
+def test_tile_refuses_other_shapes(gpu):
+    """As many scales or zero points, but group by group instead of channel by channel; codes in three dimensions."""
+    N, K, group = 48, 256, 64
+    q, scales, z = matrix(N, K, group, True)
+    packed, sc, zz = (torch.from_numpy(t).to(gpu) for t in (ref.pack(q), scales.view(np.int16), z))
+    with pytest.raises(ValueError):
+        s3d8.w4_tile(packed, sc.t().contiguous(), group, zz)
+    with pytest.raises(ValueError):
+        s3d8.w4_tile(packed, sc, group, zz.t().contiguous())
+    with pytest.raises(ValueError):
+        s3d8.w4_tile(packed.view(N, K // 4, 2), sc[:, :2].contiguous(), group, zz[:, :2].contiguous())
+    with pytest.raises(ValueError):
+        s3d8.W4Linear(packed, sc.t().contiguous(), group, zz)
+    tiled = s3d8.w4_tile(packed, sc, group, zz)
+    assert torch.equal(s3d8.w4_tile(packed, sc.flatten(), group, zz.flatten()), tiled)

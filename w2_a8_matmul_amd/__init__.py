@@ -530,12 +530,17 @@ def w4_tile(packed, scales, group: int, zeros=None, tiled=None):
     matrix)."""
     torch = _torch()
     _dev_check(packed, torch.uint8, "packed")
+    if packed.dim() != 2:
+        raise ValueError(f"packed must be [N][K/2], got {tuple(packed.shape)}")
     N, K = packed.shape[0], 2 * packed.shape[1]
     scales = _scales_view(scales)
     groups = N * -(-K // max(group, 1))
     _dev_check(scales, torch.int16, "scales", packed.device, numel=groups)
     if zeros is not None:
         _dev_check(zeros, torch.uint8, "zeros", packed.device, numel=groups)
+    for name, t in (("scales", scales), ("zeros", zeros)):
+        if t is not None and t.dim() == 2 and t.shape[0] != N:
+            raise ValueError(f"{name} must be [N][ceil(K/group)], got {tuple(t.shape)}")
     nbytes = max(w4_tiled_bytes(N, K, group, zeros is not None), 0)
     if tiled is None:
         tiled = torch.empty((nbytes,), dtype=torch.uint8, device=packed.device)
