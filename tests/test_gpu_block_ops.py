@@ -449,3 +449,14 @@ def test_codes_of_rows_past_the_largest_fp32(gpu, K):
         assert u.isinf().any(1).all() and not u.isnan().any()
         for got, want in zip(s3d8.block_norm(dev(h, gpu), dev(w, gpu), bias, kind=kind), s3d8.quant_act(u)):
             same(got, want.cpu().numpy())
+
+
+def test_norm_refuses_a_branch_of_another_shape(gpu):
+    """As many elements in other rows."""
+    h, w = torch.zeros((32, 64), device=gpu), torch.ones(64, device=gpu)
+    for shape in ((64, 32), (16, 128), (1, 2048)):
+        with pytest.raises(ValueError):
+            s3d8.block_norm(h, w, branch=torch.ones(shape, device=gpu))
+    for shape in ((32, 64), (2048,), (4, 8, 64)):  # the rows in a row
+        h1, xq, xs = s3d8.block_norm(h, w, branch=torch.ones(shape, device=gpu))
+        assert (h1 == 1).all() and (xq == 127).all()

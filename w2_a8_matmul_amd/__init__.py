@@ -697,6 +697,8 @@ def block_norm(h, weight, bias=None, *, branch=None, post_weight=None, post_bias
     if branch is not None:
         bt = _row_type(branch, "branch")
         _dev_check(branch, branch.dtype, "branch", dev, numel=M * K)
+        if branch.shape != h.shape and branch.dim() == 2:
+            raise ValueError(f"branch must be [{M}][{K}], got {tuple(branch.shape)}")
         if h_out is None:
             h_out = torch.empty_like(h)
         else:
