@@ -460,3 +460,50 @@ def test_norm_refuses_a_branch_of_another_shape(gpu):
     for shape in ((32, 64), (2048,), (4, 8, 64)):  # the rows in a row
         h1, xq, xs = s3d8.block_norm(h, w, branch=torch.ones(shape, device=gpu))
         assert (h1 == 1).all() and (xq == 127).all()
+
+
+# Rows for every CU (512 on 256 CUs): the fewest threads that hold a row in 7 float4 each.  Every build of that rule:
+# 64 threads with 1, 2, 4, 5, 7 float4, 256 with 2, 4, 5, 7, 512 with 4, 5, 7, 1024 with 4, 5, 7, 16.
+MANY = 520
+MANY_WIDTHS = [256, 272, 1024, 1040, 1792, 2048, 2064, 4096, 4112, 7168, 8192, 8208, 14336, 14352, 16400, 28672, 28688]
+SOME = [0, 1, 2, 100, 255, 256, 257, 400, 511, 512, 518, 519]
+
+
+@pytest.mark.parametrize("K", MANY_WIDTHS)
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+def test_norm_of_many_rows(gpu, kind, K):
+    """Every row like another one that the definition is computed for."""
+    g = rng(7312, K)
+    n = len(SOME)
+    h, br = rows(g, n, K, True), rows(g, n, K, True, 0.5)
+    w, pw = ((1 + 0.1 * g.standard_normal(K)).astype(F) for _ in range(2))
+    b = (0.1 * g.standard_normal(K)).astype(F) if kind == "layer" else None
+    which = np.arange(MANY) % n
+    which[SOME] = np.arange(n)
+    for post, gate, bf in ((True, None, True), (False, F([0.3]), False)):
+        h_r, u_r = ref.block_norm(h, w, b, br, pw if post else None, b if post else None, gate, gate is not None, 0.5,
+                                  kind=kind, h_bf16=bf)
+        for out in ("codes", "bf16", "f32"):
+            to = lambda x: None if x is None else dev(x, gpu)  # noqa: E731
+            got = s3d8.block_norm(dev(h[which], gpu, bf), to(w), to(b), branch=dev(br[which], gpu, True),
+                                  post_weight=to(pw) if post else None, post_bias=to(b) if post else None, gate=to(gate),
+                                  tanh_gate=gate is not None, residual_scale=0.5, kind=kind, out=out)
+            same(got[0], h_r[which])
+            check_rows(out, got[1:] if out == "codes" else got[1], u_r[which])
+
+
+@pytest.mark.parametrize("K", MANY_WIDTHS)
+@pytest.mark.parametrize("bf", [False, True])
+def test_glu_of_many_rows(gpu, bf, K):
+    g = rng(7313, K)
+    n = len(SOME)
+    both = rows(g, n, 2 * K, bf, 2.0)
+    both[1, 5] = -80                            # a row for the 64-bit form
+    both[2, :K], both[2, K:] = 1.25, -0.75      # every value the maximum
+    both[3, :K:2], both[3, K:] = 60.0, 1.0 / 64  # most on a border or at the maximum
+    a = ref.glu(both[:, :K], both[:, K:])
+    which = np.arange(MANY) % n
+    which[SOME] = np.arange(n)
+    d = dev(both[which], gpu, bf)
+    for out in ("codes", "bf16", "f32"):
+        check_rows(out, s3d8.glu_act(d[:, :K], d[:, K:], out=out), a[which])

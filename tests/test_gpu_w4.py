@@ -321,3 +321,20 @@ def test_tile_refuses_other_shapes(gpu):
         s3d8.W4Linear(packed, sc.t().contiguous(), group, zz)
     tiled = s3d8.w4_tile(packed, sc, group, zz)
     assert torch.equal(s3d8.w4_tile(packed, sc.flatten(), group, zz.flatten()), tiled)
+
+
+# every build of the kernel for few rows: tiles per group (1 up to 4096 channels on 256 CUs; 2; 4 past 12288 and 8
+# rows), registers by rows (up to 4, 8, 16), scales per 128 columns and zero points
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("M,N", [(3, 1000), (3, 4500), (7, 1000), (7, 4500), (13, 1000), (13, 4500), (13, 12500)])
+def test_each_few_row_build(gpu, M, N, group, zeros):
+    run(gpu, M, N, 656, group, zeros, "bf16" if zeros else "f32")
+
+
+# the same with several tile groups a team, and with the columns on 4, 8 and 16 waves
+@pytest.mark.parametrize("M,N,K,group,zeros", [(1, 14336, 4096, 64, False), (1, 4096, 4096, 128, True),
+                                               (8, 30000, 1040, 128, False), (16, 30000, 1040, 32, True),
+                                               (12, 50000, 528, 128, False), (2, 100000, 272, 64, True)])
+def test_few_rows_in_rounds(gpu, M, N, K, group, zeros):
+    run(gpu, M, N, K, group, zeros)
