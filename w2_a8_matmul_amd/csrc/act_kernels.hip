@@ -503,8 +503,9 @@ auto row_kernel(int64_t M, int64_t K, int cus, int most, int &threads) {
     const int64_t nv = (n4 + threads - 1) / threads;
     auto pick = [&](auto t) {
         constexpr int T = decltype(t)::value;
+        constexpr int kTwo = T == 512 ? 4 : 2;  // (up to 1024 float4 with 2 to 7 a thread go to 256 threads)
         return nv <= 1   ? Op::template kernel<T, 1>()
-               : nv <= 2 ? Op::template kernel<T, 2>()
+               : nv <= 2 ? Op::template kernel<T, kTwo>()
                : nv <= 4 ? Op::template kernel<T, 4>()
                : nv <= 5 ? Op::template kernel<T, 5>()
                          : Op::template kernel<T, 7>();
