@@ -6,7 +6,10 @@
 // reductions, and is written once.  So the bytes moved are the floor, but the
 // arithmetic is close to it: statistics and values are held in 64 bits so that
 // the codes are the correctly rounded ones, and vector instructions issue most
-// of the time a launch takes (70% and 84% at the large sizes below).
+// of the time a launch takes (70% and 84% at the large sizes below).  Rows of more
+// than 28672 values, 16 float4 to each of 1024 threads, do not fit: 324 to 840 bytes
+// a lane spill to scratch memory, and 64 rows of 53248 in bf16 take 25 us in the
+// norm and 100 us in the gated activation.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -240,8 +243,8 @@ __device__ __forceinline__ void normalise(float4 (&v)[NV], int K, double inv_k, 
 }
 
 // exp(x) - 1 = 2^n (p(r) - 1) + (2^n - 1) and its parts: x = n ln 2 + r with ln 2 in two
-// parts, p a polynomial of degree 11 on |r| <= ln 2 / 2 (Chebyshev interpolation,
-// relative error 2^-55.7).
+// parts (Cody and Waite's reduction), p a polynomial of degree 11 on |r| <= ln 2 / 2
+// (Chebyshev interpolation, relative error 2^-55.7).
 struct Exp {
     double less_one, two_n;  // p(r) - 1, 2^n
 };
@@ -281,10 +284,11 @@ __device__ __forceinline__ float tanh_rounded(float g) {
 //
 // Measured, RMS with a branch and its post norm, codes out: 2048 x 4096 in bf16
 // 15.1 us (58.7 MB at 3.9 TB/s), 17.2 with operands in no cache; RMS of one row
-// 2.9 us; layer norm, 1601 x 1280 in fp32 with a gate, 8.9 us.  34 vector
+// 2.9 us; layer norm, 1601 x 1280 in fp32 with a gate to bf16, 8.3 us.  34 vector
 // instructions per element of the first issue 70% of its time, most of them
 // 64-bit (34 us with sums by shuffles through LDS and the same workgroup for every
-// width).  The weights loaded before the sums rather than after them gain at some
+// width).  The last one is a wave per row, fewer than two a SIMD, whose loads, mean,
+// squares, weights and stores follow one another.  The weights loaded before the sums rather than after them gain at some
 // sizes what they lose at others (8192 x 4096: 52.8 us for 56.3, 1601 x 5120: 25.7
 // for 24.9).  More than one row a workgroup (the weights kept in registers, the
 // next row's loads ahead) takes 172 registers and 31 us.
@@ -455,9 +459,11 @@ __device__ __forceinline__ bool glu_codes(const Raw<kBF> (&g4)[NV], const Raw<kB
     return true;
 }
 
-// One workgroup per row.  Measured in bf16, codes out: 2048 x 14336 33 us (147 MB
-// at 4.5 TB/s; 27 vector instructions per element, issuing 84% of the time),
-// 58.7 us with gated() for every element; one row of 14336 in fp32 5.2 us,
+// One workgroup per row.  Measured in bf16, codes out: 2048 x 14336 31-33 us (147 MB
+// at 4.5 TB/s; 27 vector instructions per element, issuing 84% of the time), 58.7 us
+// with gated() for every element, which is what a row with one gate below -64 takes
+// (62 us with one in each row), and rows out in bf16 or fp32 too (47 us in bf16, 176 MB);
+// one row of 14336 in fp32 5.2 us,
 // 5 x 1744 to fp32 2.5 us (both little more than a launch and their latency).
 template <int T, int NV, bool kBF>
 __global__ __launch_bounds__(T) void glu_act_kernel(const void *__restrict__ gate, int64_t ldg,

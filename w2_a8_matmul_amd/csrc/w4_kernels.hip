@@ -136,9 +136,11 @@ __device__ __forceinline__ float scale_of(uint32_t bits) {
 //
 // Bound by the weight stream where there is one: 8 x 4096 -> 128256 with groups
 // of 128 moves 275 MB in 50.8 us (5.4 TB/s, what a copy of 1 GiB reaches is
-// 5.2), 1 x 4096 -> 14336 31 MB in 9.2 us (3.4 TB/s: as long again to start, to
-// fill the pipe and to join the waves' sums); 1 x 4096 -> 1024 takes 4.5 us,
-// nearly all of it the launch and one memory round trip after another.
+// 5.2), 1 x 4096 -> 14336 31 MB in 9.2 us (3.4 TB/s: 448 groups on 256 CUs take two
+// rounds, and each join waits for its token scales, which the next group's
+// loads are ahead of, so that the ring drains); 1 x 4096 -> 1024 takes 4.5 us, nearly
+// all of it the launch and two memory round trips, the operands' and at the
+// end the token scale's, on 64 of the CUs.
 constexpr int kRowWaves = 16;
 
 template <int NT, int Q, int P, bool kZeros>
@@ -328,9 +330,12 @@ __global__ __launch_bounds__(kRowWaves * 64) void w4_rows_kernel(
 // The 32 x 32 products take half the issue slots of 16 x 16 ones per
 // multiplication, and their K = 32 serves 32-column groups at full rate.
 // 2048 x 4096 -> 14336 takes 159 us with groups of 64 (1.51 POP/s; 157 to 187 by
-// card and by how long it has been running), 132 with 128, 230 with 32 and zero points: at 64, vector
-// instructions issue 96% of the time and the matrix cores run 37% of it, LDS has
-// no bank conflict.
+// card and by how long it has been running), 190 to 212 with zero points (four registers spill, and
+// the scratch loads that bring two back in every step wait for the copies of the
+// next block), 132 with 128, 230 with 32 and zero points: at 64, vector instructions issue 96% of
+// the time and the matrix cores run 37% of it, LDS has no bank conflict.  At the end
+// the token scales of each quad of rows are loaded between the stores, a wait for
+// each: a fixed cost that counts where a CU has about one tile.
 //
 // K order.  Product operands hold 16 consecutive columns in lane half h of a row
 // or channel.  With P = 1 or 2 those are chunk 2 h + s of a 64-column half
@@ -614,7 +619,9 @@ void launch_rows(const W4Args &a, int P, bool zeros, int cus, hipStream_t stream
 // Workgroup tiles of the GEMM: rows and channels, column ranges (waves split
 // between them), and the time of a step of `ranges` blocks and of everything
 // else, in ns, from K = 4096 with one workgroup on a CU (a second one beside
-// it gains little: a workgroup keeps its SIMDs' issue busy).
+// it gains little: a workgroup keeps its SIMDs' issue busy).  They are those of groups of
+// 64 without zero points and rank the tiles; as times they are low for zero points:
+// 1600 x 5120 -> 1280 with groups of 128 is put at 20.8 us and takes 28.
 struct GemmTile {
     int rows, channels, ranges, step_ns, fixed_ns;
 };
@@ -706,7 +713,8 @@ int check_linear(const int8_t *xq, const float *xs, int64_t M, int64_t K, int64_
 // Up to 16 rows.  Tiles per group: one while a CU has no more than one (4096 -> 1024 at
 // one token 4.3 us, 4.6 with two), else two (4096 -> 14336: 9.4 us, 9.8 with one, 9.3
 // with four; 8192: 6.7, 7.4, 7.8), or four where the activations that each group reads
-// again are many (16 tokens, 14336: 10.5, 11.8 with two).
+// again are many (16 tokens, 14336: 10.5, 11.8 with two; the build for groups of 32 or 96
+// with zero points does not fit the registers: 87 spill, and it takes 31 to 37 us).
 void launch_few(const W4Args &a, int P, bool zeros, int cus, hipStream_t stream) {
     const int64_t tiles = ((int64_t)a.N + 15) / 16;
     const int nt = tiles <= cus ? 1 : a.M > 8 && tiles > 3 * cus ? 4 : 2;
