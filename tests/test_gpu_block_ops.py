@@ -454,10 +454,10 @@ def test_codes_of_rows_past_the_largest_fp32(gpu, K):
 def test_norm_refuses_a_branch_of_another_shape(gpu):
     """As many elements in other rows."""
     h, w = torch.zeros((32, 64), device=gpu), torch.ones(64, device=gpu)
-    for shape in ((64, 32), (16, 128), (1, 2048)):
+    for shape in ((64, 32), (16, 128), (1024, 2)):
         with pytest.raises(ValueError):
             s3d8.block_norm(h, w, branch=torch.ones(shape, device=gpu))
-    for shape in ((32, 64), (2048,), (4, 8, 64)):  # the rows in a row
+    for shape in ((32, 64), (2048,), (1, 2048), (4, 8, 64)):  # the rows in a row
         h1, xq, xs = s3d8.block_norm(h, w, branch=torch.ones(shape, device=gpu))
         assert (h1 == 1).all() and (xq == 127).all()
 

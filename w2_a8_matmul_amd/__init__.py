@@ -181,6 +181,12 @@ _FORMATS = {"s3d8": 0, "3d8": 1}
 _OUTS = {"f32": 0, "bf16": 1}
 
 
+def _other_matrix(t, rows) -> bool:
+    """A matrix of other rows than it should have (a vector, also as a matrix of
+    one row or column, or more dimensions are taken as the rows in a row)."""
+    return t.dim() == 2 and t.shape[0] != rows and 1 not in t.shape
+
+
 def _variant(fmt: str, out: str = "f32"):
     if fmt not in _FORMATS or out not in _OUTS:
         raise ValueError(f"fmt must be one of {list(_FORMATS)}, out one of {list(_OUTS)}")
@@ -539,7 +545,7 @@ def w4_tile(packed, scales, group: int, zeros=None, tiled=None):
     if zeros is not None:
         _dev_check(zeros, torch.uint8, "zeros", packed.device, numel=groups)
     for name, t in (("scales", scales), ("zeros", zeros)):
-        if t is not None and t.dim() == 2 and t.shape[0] != N:
+        if t is not None and _other_matrix(t, N):
             raise ValueError(f"{name} must be [N][ceil(K/group)], got {tuple(t.shape)}")
     nbytes = max(w4_tiled_bytes(N, K, group, zeros is not None), 0)
     if tiled is None:
@@ -697,7 +703,7 @@ def block_norm(h, weight, bias=None, *, branch=None, post_weight=None, post_bias
     if branch is not None:
         bt = _row_type(branch, "branch")
         _dev_check(branch, branch.dtype, "branch", dev, numel=M * K)
-        if branch.shape != h.shape and branch.dim() == 2:
+        if branch.shape != h.shape and _other_matrix(branch, M):
             raise ValueError(f"branch must be [{M}][{K}], got {tuple(branch.shape)}")
         if h_out is None:
             h_out = torch.empty_like(h)
