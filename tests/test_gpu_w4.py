@@ -322,7 +322,8 @@ def test_tile_refuses_other_shapes(gpu):
     tiled = s3d8.w4_tile(packed, sc, group, zz)
     assert torch.equal(s3d8.w4_tile(packed, sc.flatten(), group, zz.flatten()), tiled)
     tiled = s3d8.w4_tile(packed, sc[:, :1].contiguous(), K, zz[:, :1].contiguous())  # one scale a channel
-    assert torch.equal(s3d8.w4_tile(packed, sc[:, :1].reshape(1, N), K, zz[:, :1].reshape(1, N)), tiled)
+    assert torch.equal(s3d8.w4_tile(packed, sc[:, :1].reshape(1, N).contiguous(), K,
+                                    zz[:, :1].reshape(1, N).contiguous()), tiled)
 
 
 # every build of the kernel for few rows: tiles per group (1 up to 4096 channels on 256 CUs; 2; 4 past 12288 and 8
