@@ -100,6 +100,32 @@ __device__ __forceinline__ float wave_max(float v) {
     return __uint_as_float(max(a, b));
 }
 
+// Workgroup barrier for LDS alone: loads from memory stay in flight.
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// exp(x) - 1 = 2^n (p(r) - 1) + (2^n - 1) and its parts: x = n ln 2 + r with ln 2 in two
+// parts (Cody and Waite's reduction), p a polynomial of degree 11 on |r| <= ln 2 / 2
+// (Chebyshev interpolation, relative error 2^-55.7).
+struct Exp {
+    double less_one, two_n;  // p(r) - 1, 2^n
+};
+__device__ __forceinline__ Exp exp_parts(double x) {
+    const double n = __builtin_rint(x * 0x1.71547652b82fep+0);
+    const double r = __builtin_fma(n, -0x1.a39ef35793c76p-33, __builtin_fma(n, -0x1.62e42fee00000p-1, x));
+    double e = 0x1.af631d203b4edp-26;
+    e = __builtin_fma(e, r, 0x1.28b405992d897p-22);
+    e = __builtin_fma(e, r, 0x1.71ddf5748bd71p-19);
+    e = __builtin_fma(e, r, 0x1.a01991ac6b2ddp-16);
+    e = __builtin_fma(e, r, 0x1.a01a01b1437f6p-13);
+    e = __builtin_fma(e, r, 0x1.6c16c187fbea9p-10);
+    e = __builtin_fma(e, r, 0x1.111111110f225p-7);
+    e = __builtin_fma(e, r, 0x1.555555554f0cep-5);
+    e = __builtin_fma(e, r, 0x1.555555555555ap-3);
+    e = __builtin_fma(e, r, 0x1.0000000000011p-1);
+    e = __builtin_fma(e, r, 1.0);
+    return {e * r, __builtin_amdgcn_ldexp(1.0, (int)n)};
+}
+
 // --------------------------------------------------------------- GEMM tiles
 
 constexpr int kXcds = 8;
