@@ -572,6 +572,146 @@ int32_t s3d8_block_norm(const s3d8_block_norm_args *args, void *stream);
 int32_t s3d8_glu_act(const void *gate, int64_t ld_gate, const void *up, int64_t ld_up, int64_t M, int64_t K,
                      int32_t in_type, int32_t out_type, void *rows, int8_t *xq, float *xs, void *stream);
 
+/* ------------------------------------------------------------ heads and tokens */
+
+/* How a rotary position's frequencies are stretched for long contexts. */
+#define S3D8_ROPE_PLAIN 0
+#define S3D8_ROPE_LINEAR 1
+#define S3D8_ROPE_LLAMA3 2
+#define S3D8_ROPE_YARN 3
+
+/* Radians per position of each pair of a rotary position, on the host, in 64 bits:
+ *   f_j = base^(-2 j / rotary_dim),  j = 0 .. rotary_dim / 2 - 1, and with a share e_j
+ *   of it stretched:  f_j (1 - e_j) + f_j / factor * e_j,
+ *   PLAIN   e = 0.
+ *   LINEAR  e = 1 (positions interpolated).
+ *   LLAMA3  e_j = 1 - clamp((t_j - low) / (high - low), 0, 1), t_j = original_length *
+ *           f_j / (2 pi) the turns of pair j over the original length.
+ *   YARN    e_j = clamp((j - a) / (b - a), 0, 1), a = max(floor(p(high)), 0), b =
+ *           min(ceil(p(low)), rotary_dim - 1), p(t) = rotary_dim * ln(original_length /
+ *           (2 pi t)) / (2 ln base) the pair that makes t turns; b - a at least 0.001.
+ *   rotary_dim        entries of a head that are turned, even, 2 to 256.
+ *   factor            at least 1 (not read for PLAIN).
+ *   original_length, low, high   positive, low < high, in turns (LLAMA3 and YARN).
+ *   frequencies       out, host double [rotary_dim / 2].
+ *   attention_factor  out, host double [1]: the factor on cosine and sine, 0.1 ln(factor)
+ *                     + 1 for YARN, else 1.
+ * Touches no GPU.  Errors: INVALID_ARG, SHAPE. */
+int32_t s3d8_rope_frequencies(int64_t rotary_dim, double base, int32_t scaling, double factor, double original_length,
+                              double low, double high, double *frequencies, double *attention_factor);
+
+/* Arguments of s3d8_head_rope.  Every pointer is device memory.  Heads are D
+ * values in a row; the head h of token m begins at m * row + h * head elements. */
+typedef struct s3d8_head_rope_args {
+    const void *q, *k;          /* M x q_heads and M x k_heads heads, in_type; k NULL: none   */
+    void *q_out, *k_out;        /* out, out_type; may be q and k with their type and strides  */
+    const float *q_weight;      /* [D]: the norm of query heads, or NULL (none)               */
+    const float *k_weight;      /* [D]: of key heads, or NULL                                 */
+    const void *positions;      /* int32 or int64 [M]; NULL with rotary_dim 0                 */
+    const double *frequencies;  /* [rotary_dim / 2], radians per position                     */
+    int64_t M, q_heads, k_heads, D, rotary_dim;
+    int64_t q_row, q_head, k_row, k_head, q_out_row, q_out_head, k_out_row, k_out_head;
+    float eps;
+    float factor;               /* on cosine and sine                                         */
+    int32_t in_type, out_type;  /* S3D8_ROWS_F32 or S3D8_ROWS_BF16                            */
+    int32_t positions_64;       /* positions are int64                                        */
+    int32_t interleaved;        /* pairs (2j, 2j + 1), else (j, j + rotary_dim / 2)           */
+} s3d8_head_rope_args;
+
+/* The RMS norm of each query and key head and its rotary position, in one launch.
+ * Per head x of the token at position s:
+ *   n = (x * r) * w,  r = 1 / sqrt(sum(x^2) / D + eps)   (n = x without a weight),
+ *   (a, b) -> (a c - b s', b c + a s') for the pairs of the first rotary_dim entries,
+ *   c and s' the cosine and sine of s * f_j, times factor; the others stay.
+ * The angle and its reduction are in 64 bits, every other step in fp32.  D even, at
+ * most 256; rotary_dim even, at most D, 0 for none (a weight is then needed); strides at
+ * least a head's size (of what has more than one row or head); pointers aligned to an
+ * element.  Where D, rotary_dim and strides are multiples of 8, 8 and 4 and pointers
+ * aligned to 4 elements, four pairs are loaded at a time, else one.  At most 524288
+ * tokens and 4096 heads of each kind; squares summed within fp32's range; outputs other
+ * than the input itself must not overlap inputs.
+ * Errors: INVALID_ARG, SHAPE, ALIGN, DEVICE, HIP. */
+int32_t s3d8_head_rope(const s3d8_head_rope_args *args, void *stream);
+
+/* Arguments of s3d8_cross_attention.  Every pointer is device memory. */
+typedef struct s3d8_cross_attention_args {
+    const uint16_t *q;        /* bf16 [B][Lq][heads][D]                                          */
+    const uint16_t *k, *v;    /* bf16 [B][Lk][kv_heads][D], or [1]... with `shared`              */
+    const int32_t *kv_lens;   /* [B] ([1] with `shared`): keys of each sequence, or NULL (Lk)    */
+    const uint8_t *mask;      /* nonzero where query i of sequence b sees key j, or NULL (all)   */
+    uint16_t *o;              /* out, bf16 [B][Lq][heads][D], contiguous                         */
+    int8_t *xq;               /* out, int8 [B Lq][heads D]: the codes of o's rows, or NULL       */
+    float *xs;                /* out, fp32 [B Lq]: their scales; goes with xq                    */
+    void *workspace;
+    int64_t workspace_bytes;
+    int64_t B, Lq, Lk, heads, kv_heads, D;
+    int64_t q_seq, q_row, q_head;               /* strides in elements                           */
+    int64_t k_seq, k_row, k_head, v_seq, v_row, v_head;
+    int64_t mask_seq, mask_row;                 /* in bytes; 0 where one row is for all          */
+    float scale;
+    int32_t shared;           /* k, v and kv_lens are of one sequence, read by all B             */
+} s3d8_cross_attention_args;
+
+/* Attention of B sequences of Lq query tokens to the Lk states of an encoder, of
+ * which the first kv_lens[b] exist.  Query head h reads key head h / (heads / kv_heads):
+ *   o = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale * q . k_j), over the keys j < kv_lens[b]
+ *   that the mask lets the query see; 0 where there are none.
+ * Products, sums and exponentials in fp32 (a running maximum taken off), p rounded to
+ * bf16 where it is multiplied with v; o rounded to bf16.  With xq and xs also the codes that
+ * s3d8_quant_act makes of the rows of o, for the output projection.
+ *   D            a multiple of 16, at most 128; heads a multiple of kv_heads.
+ *   strides      multiples of 8, k_row and v_row at least D and below 2^23 where Lk > 1;
+ *                q, k, v 16-B aligned.
+ *   kv_lens      0 to Lk (values outside are taken as 0 and Lk).  What lies in k and v
+ *                past a sequence's length is not used, and what the mask hides from
+ *                a query is not in its sum, whatever it holds.
+ *   workspace    s3d8_cross_attention_workspace_bytes(args, CU count) bytes, 16-B aligned; NULL
+ *                where that is 0.  It holds nothing between calls.
+ *   At most 65535 sequences, 2^24 tokens and keys each, 4096 heads, and B Lq heads at most
+ *   2^30; with xq at most 524288 rows, of at most 65536 entries; o, xq 16-B aligned.
+ * Errors: INVALID_ARG, SHAPE, ALIGN, DEVICE, HIP. */
+int32_t s3d8_cross_attention(const s3d8_cross_attention_args *args, void *stream);
+
+/* Workspace bytes of s3d8_cross_attention on a device of num_cus compute units: the
+ * mask as bits, and partial sums where the keys are split over workgroups.  Of the
+ * pointers only whether mask is NULL is looked at.  -1 on bad sizes. */
+int64_t s3d8_cross_attention_workspace_bytes(const s3d8_cross_attention_args *args, int32_t num_cus);
+
+/* Arguments of s3d8_sample.  Every pointer is device memory. */
+typedef struct s3d8_sample_args {
+    const void *logits;        /* [M][V], fp32 or bf16                          */
+    const float *u;            /* [M]: uniform random numbers from [0, 1)       */
+    const float *temperature;  /* [M], or NULL: temperature_all for every row   */
+    const int32_t *top_k;      /* [M], or NULL: top_k_all                       */
+    const float *top_p;        /* [M], or NULL: top_p_all                       */
+    const float *min_p;        /* [M], or NULL: min_p_all                       */
+    int32_t *token;            /* out, [M]                                      */
+    float *prob;               /* out, [M], or NULL                             */
+    int64_t M, V, row;         /* row: elements between rows, at least V        */
+    float temperature_all;
+    int32_t top_k_all;
+    float top_p_all, min_p_all;
+    int32_t type;              /* S3D8_ROWS_F32 or S3D8_ROWS_BF16               */
+} s3d8_sample_args;
+
+/* The next token of each row, from a random number.  Weights are whole numbers, so
+ * that their sums have one value: with m the row's largest logit,
+ *   W_i = rne(2^44 exp((l_i - m) / temperature))   (the exponential in 64 bits),
+ * W_i = 2^44 for l_i = m, 0 for l_i = -infinity; a NaN counts as -infinity.  In the order
+ * of falling logits, equal ones by rising index, tokens are kept
+ *   top_k   the first top_k (0 or less: all);
+ *   top_p   of these, while the sum of those before is less than max(1, ceil(top_p S)), S
+ *           the sum of these (1 or more: all);
+ *   min_p   of these, with W_i >= ceil(min_p 2^44).
+ * With T the sum of the kept weights, the token is the first in the order of the index at
+ * which the sum of kept weights is over min(floor(u T), T - 1); prob is its W / T.
+ * A temperature of 0 or less keeps the largest logit alone, the first of equals.  A row
+ * of -infinity (and NaN) throughout has token -1 and prob 0.
+ * Temperatures over 2^100 count as 2^100, NaN as 0, top_p and min_p outside [0, 1] (NaN: 0) as
+ * its ends; the values for all rows are refused there.  V at most 262144, M at most 524288.
+ * Errors: INVALID_ARG, SHAPE, ALIGN, DEVICE, HIP. */
+int32_t s3d8_sample(const s3d8_sample_args *args, void *stream);
+
 /* Matrix-core rate probe: a measurement utility for reading the GEMM's
  * INT8 rate against what the matrix cores sustain, not part of the method.
  * `workgroups` workgroups of 256 threads (4 waves) each run `iters` rounds

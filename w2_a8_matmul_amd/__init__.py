@@ -17,6 +17,11 @@ Beside it: the same linear layer on plain 4-bit weights with group scales
 (``w4_linear``, ``W4Linear``), and what stands between the linears of a block,
 ending in the INT8 codes they read: ``block_norm`` (norms around a block, gate,
 residual sum) and ``glu_act`` (SiLU-gated activation).
+
+Between the projections of heads, and after the vocabulary projection:
+``head_rope`` (norm of query and key heads, rotary position; ``Rope`` holds its
+frequencies), ``cross_attention`` (attention to an encoder's states) and
+``sample`` (the next token from its logits and a random number).
 """
 from __future__ import annotations
 
@@ -32,6 +37,7 @@ __all__ = [
     "PackedLinear", "hbm_read_probe", "mfma_rate_probe", "encode_device", "forward_batch",
     "linear_splitk", "splitk_auto", "splitk_workspace_bytes",
     "w4_encode", "w4_tiled_bytes", "w4_tile", "w4_linear", "w4_forward", "W4Linear", "block_norm", "glu_act",
+    "Rope", "head_rope", "cross_attention", "sample",
 ]
 
 
@@ -754,3 +760,233 @@ def glu_act(gate, up, out: str = "codes", rows=None, xq=None, xs=None):
     _enqueue("s3d8_glu_act", dev, gate.data_ptr(), gate.stride(0) if M > 1 else K, up.data_ptr(),
              up.stride(0) if M > 1 else K, M, K, t, _ROWS[out], _ptr(rows), _ptr(xq), _ptr(xs))
     return (xq, xs) if rows is None else rows
+
+
+# ------------------------------------------------------------------ heads and tokens
+_SCALINGS = {"none": 0, "linear": 1, "llama3": 2, "yarn": 3}
+_LAYOUTS = {"half": 0, "interleaved": 1}
+
+
+class Rope:
+    """The frequencies of a rotary position, kept on a device for head_rope.
+
+    ``rotary_dim``: the entries of a head that are turned, in pairs (j, j + rotary_dim / 2)
+    ("half") or (2 j, 2 j + 1) ("interleaved").  ``scaling`` stretches them for long
+    contexts (see s3d8_rope_frequencies): "linear" by ``factor``; "llama3" by ``factor``
+    below ``low`` turns over ``original_length`` positions, not above ``high``; "yarn"
+    between the pairs of ``beta_slow`` and ``beta_fast`` turns, with cosine and sine times
+    ``attention_factor`` (0.1 ln(factor) + 1 unless given).  ``frequencies``: float64
+    [rotary_dim / 2] on ``device``."""
+
+    def __init__(self, rotary_dim: int, base: float = 10000.0, *, layout: str = "half", scaling: str = "none",
+                 factor: float = 1.0, original_length: float = 8192, low: float = 1.0, high: float = 4.0,
+                 beta_fast: float = 32.0, beta_slow: float = 1.0, attention_factor=None, device="cuda"):
+        torch = _torch()
+        if layout not in _LAYOUTS:
+            raise ValueError(f"layout must be one of {list(_LAYOUTS)}")
+        if scaling not in _SCALINGS:
+            raise ValueError(f"scaling must be one of {list(_SCALINGS)}")
+        if scaling == "yarn":
+            low, high = beta_slow, beta_fast
+        self.rotary_dim, self.layout = int(rotary_dim), layout
+        f = np.empty(max(self.rotary_dim // 2, 1), np.float64)
+        own = ctypes.c_double()
+        call("s3d8_rope_frequencies", self.rotary_dim, base, _SCALINGS[scaling], factor, original_length, low, high,
+             _np_ptr(f), ctypes.byref(own))
+        self.factor = own.value if attention_factor is None else float(attention_factor)
+        self.frequencies = torch.as_tensor(f).to(device)
+
+
+def _heads(t, name, dtype=None, shape=None, device=None):
+    """A device tensor [M][heads][D] with the entries of a head in a row: its row
+    and head strides."""
+    if not isinstance(t, _torch().Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA/HIP torch tensor")
+    if dtype is not None and t.dtype is not dtype:
+        raise TypeError(f"{name} must have dtype {dtype}, got {t.dtype}")
+    if t.dim() != 3 or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} must be {list(shape) if shape is not None else '[M][heads][D]'}, got {tuple(t.shape)}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the other arguments on {device}")
+    M, H, D = t.shape
+    row, head, one = t.stride()
+    if one != 1 and D > 1:
+        raise ValueError(f"the entries of a head of {name} must be contiguous")
+    return (row if M > 1 else 0), (head if H > 1 else 0)
+
+
+def head_rope(q, k=None, positions=None, rope=None, *, q_weight=None, k_weight=None, eps: float = 1e-5,
+              out: str = "bf16", q_out=None, k_out=None):
+    """The RMS norm of each query and key head and its rotary position, in one
+    launch (see s3d8_head_rope).  ``q``, ``k``: fp32 or bf16 [M][heads][D] with any
+    row and head strides, e.g. parts of one [M][(heads + 2 kv_heads) D] matrix;
+    ``positions``: int32 or int64 [M], with ``rope`` (a Rope); ``q_weight``,
+    ``k_weight``: fp32 [D], the norms' (none without).  ``out``: "bf16" or "f32";
+    ``q_out``, ``k_out`` (rows of a cache, or q and k themselves) take the results.
+
+    Returns (q', k'), or q' without ``k``."""
+    torch = _torch()
+    o = _out_type(out)
+    t = _row_type(q, "q")
+    strides = [*_heads(q, "q")]
+    M, H, D = q.shape
+    dev = q.device
+    dtype = torch.bfloat16 if o else torch.float32
+    Hk = 0
+    if k is not None:
+        if not isinstance(k, torch.Tensor) or k.dim() != 3:
+            raise TypeError("k must be a CUDA/HIP torch tensor [M][heads][D]")
+        Hk = k.shape[1]
+        strides += _heads(k, "k", q.dtype, (M, Hk, D), dev)
+    elif k_out is not None or k_weight is not None:
+        raise ValueError("k_out and k_weight go with k")
+    else:
+        strides += (0, 0)
+    if q_out is None:
+        q_out = torch.empty(M, H, D, dtype=dtype, device=dev)
+    strides += _heads(q_out, "q_out", dtype, (M, H, D), dev)
+    if k is not None:
+        if k_out is None:
+            k_out = torch.empty(M, Hk, D, dtype=dtype, device=dev)
+        strides += _heads(k_out, "k_out", dtype, (M, Hk, D), dev)
+    else:
+        strides += (0, 0)
+    if q_weight is not None:
+        _dev_check(q_weight, torch.float32, "q_weight", dev, numel=D)
+    if k_weight is not None:
+        _dev_check(k_weight, torch.float32, "k_weight", dev, numel=D)
+    if (positions is None) != (rope is None):
+        raise ValueError("positions and rope go together")
+    wide, frequencies, rotary_dim, factor, side_by_side = False, None, 0, 1.0, False
+    if rope is not None:
+        wide = isinstance(positions, torch.Tensor) and positions.dtype is torch.int64
+        _dev_check(positions, torch.int64 if wide else torch.int32, "positions", dev, numel=M)
+        frequencies, rotary_dim, factor = rope.frequencies, rope.rotary_dim, rope.factor
+        side_by_side = rope.layout == "interleaved"
+        _dev_check(frequencies, torch.float64, "rope.frequencies", dev, numel=rotary_dim // 2)
+    _enqueue("s3d8_head_rope", dev,
+             _lib.HEAD_ROPE_ARGS(q.data_ptr(), _ptr(k), q_out.data_ptr(), _ptr(k_out), _ptr(q_weight), _ptr(k_weight),
+                                 _ptr(positions), _ptr(frequencies), M, H, Hk, D, rotary_dim, *strides, eps, factor, t, o,
+                                 wide, side_by_side))
+    return q_out if k is None else (q_out, k_out)
+
+
+_attention_bytes = {}
+
+
+def cross_attention(q, k, v, *, kv_lens=None, mask=None, scale=None, out: str = "bf16", o=None, xq=None, xs=None):
+    """Attention of query tokens to an encoder's states (see s3d8_cross_attention).
+
+    ``q``: bf16 [B][Lq][heads][D]; ``k``, ``v``: bf16 [B][Lk][kv_heads][D], or [1]... for
+    states that all sequences share; any strides that are multiples of 8, the entries of
+    a head in a row.  ``kv_lens``: int32 [B] ([1] if shared), the states of each sequence
+    (all Lk without).  ``mask``: bool [B or 1][Lq or 1][Lk], true where a token sees a
+    state.  A token that sees none has 0.  ``scale``: 1 / sqrt(D) unless given.
+
+    Returns o bf16 [B][Lq][heads][D], or its INT8 codes and scales for the output
+    projection (xq [B Lq][heads D], xs [B Lq]) with ``out="codes"``."""
+    torch = _torch()
+    if out not in ("bf16", "codes"):
+        raise ValueError("out must be one of ['bf16', 'codes']")
+    bf16 = torch.bfloat16
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA/HIP torch tensor")
+        if t.dtype is not bf16:
+            raise TypeError(f"{name} must have dtype {bf16}, got {t.dtype}")
+        if t.dim() != 4 or (t.stride(3) != 1 and t.shape[3] > 1):
+            raise ValueError(f"{name} must be [B][L][heads][D], the entries of a head contiguous")
+    dev = q.device
+    if k.device != dev or v.device != dev:
+        raise ValueError("q, k and v must be on one device")
+    B, Lq, H, D = q.shape
+    Bk, Lk, Hk, Dk = k.shape
+    if v.shape != k.shape or Dk != D or (Bk != B and Bk != 1):
+        raise ValueError(f"k and v must be [{B} or 1][Lk][kv_heads][{D}], got {tuple(k.shape)} and {tuple(v.shape)}")
+    shared = Bk == 1 and B > 1
+    strides = []
+    for t in (q, k, v):
+        strides += [s if n > 1 else 0 for s, n in zip(t.stride()[:3], t.shape)]
+    if kv_lens is not None:
+        _dev_check(kv_lens, torch.int32, "kv_lens", dev, numel=Bk)
+    mask_seq = mask_row = 0
+    if mask is not None:
+        if not isinstance(mask, torch.Tensor) or not mask.is_cuda:
+            raise TypeError("mask must be a CUDA/HIP torch tensor")
+        if mask.dtype is not torch.bool:
+            raise TypeError(f"mask must have dtype torch.bool, got {mask.dtype}")
+        if mask.device != dev:
+            raise ValueError(f"mask is on {mask.device}, the other arguments on {dev}")
+        if mask.dim() != 3 or mask.shape[0] not in (1, B) or mask.shape[1] not in (1, Lq) or mask.shape[2] != Lk or (
+                mask.stride(2) != 1 and Lk > 1):
+            raise ValueError(f"mask must be [{B} or 1][{Lq} or 1][{Lk}], its rows contiguous, got {tuple(mask.shape)}")
+        mask_seq = mask.stride(0) if mask.shape[0] > 1 else 0
+        mask_row = mask.stride(1) if mask.shape[1] > 1 else 0
+    if o is None:
+        o = torch.empty(B, Lq, H, D, dtype=bf16, device=dev)
+    else:
+        _dev_check(o, bf16, "o", dev, numel=B * Lq * H * D)
+    if out == "codes":
+        xq, xs = _codes_out(xq, xs, B * Lq, H * D, dev)
+    elif xq is not None or xs is not None:
+        raise ValueError("xq and xs go with out='codes'")
+    if scale is None:
+        scale = D ** -0.5 if D else 1.0
+    sizes = (B, Lq, Lk, H, Hk, D, *strides, mask_seq, mask_row, scale, shared)
+    key = (B, Lq, Lk, H, Hk, D, shared, mask is not None, mask_seq != 0, mask_row != 0, dev.index)
+    nbytes = _attention_bytes.get(key)
+    if nbytes is None:
+        cus = torch.cuda.get_device_properties(dev).multi_processor_count
+        nbytes = lib().s3d8_cross_attention_workspace_bytes(
+            _lib.CROSS_ATTENTION_ARGS(0, 0, 0, 0, _ptr(mask), 0, 0, 0, 0, 0, *sizes), cus)
+        if len(_attention_bytes) >= 4096:
+            _attention_bytes.clear()
+        _attention_bytes[key] = nbytes
+    workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes > 0 else None
+    _enqueue("s3d8_cross_attention", dev,
+             _lib.CROSS_ATTENTION_ARGS(q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(kv_lens), _ptr(mask), o.data_ptr(),
+                                       _ptr(xq), _ptr(xs), _ptr(workspace), max(nbytes, 0), *sizes))
+    return o if out == "bf16" else (xq, xs)
+
+
+def sample(logits, u, *, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, token=None, prob=None):
+    """The next token of each row of logits, from a random number (see s3d8_sample).
+
+    ``logits``: fp32 or bf16 [M][V], rows contiguous, any distance apart; ``u``: fp32 [M],
+    uniform from [0, 1); ``temperature`` (0: the largest logit), ``top_k`` (0: all), ``top_p``
+    (1: all), ``min_p`` (0: all): a number, or a device tensor [M] (fp32, ``top_k`` int32).
+
+    Returns (token int32 [M], prob fp32 [M]), the probability among the tokens kept;
+    -1 and 0 for a row of -infinity."""
+    torch = _torch()
+    t = _row_type(logits, "logits")
+    if not logits.is_cuda:
+        raise TypeError("logits must be a CUDA/HIP torch tensor")
+    if logits.dim() != 2 or (logits.stride(1) != 1 and logits.shape[1] > 1):
+        raise ValueError("logits must be [M][V] with contiguous rows")
+    M, V = logits.shape
+    dev = logits.device
+    _dev_check(u, torch.float32, "u", dev, numel=M)
+    pointers, numbers = [], []
+    for name, x, dtype in (("temperature", temperature, torch.float32), ("top_k", top_k, torch.int32),
+                           ("top_p", top_p, torch.float32), ("min_p", min_p, torch.float32)):
+        if isinstance(x, torch.Tensor):
+            _dev_check(x, dtype, name, dev, numel=M)
+            pointers.append(x.data_ptr())
+            numbers.append(0)
+        else:
+            pointers.append(0)
+            numbers.append(x)
+    numbers[1] = min(int(numbers[1]), 0x7FFFFFFF)
+    if token is None:
+        token = torch.empty(M, dtype=torch.int32, device=dev)
+    else:
+        _dev_check(token, torch.int32, "token", dev, numel=M)
+    if prob is None:
+        prob = torch.empty(M, dtype=torch.float32, device=dev)
+    else:
+        _dev_check(prob, torch.float32, "prob", dev, numel=M)
+    _enqueue("s3d8_sample", dev,
+             _lib.SAMPLE_ARGS(logits.data_ptr(), u.data_ptr(), *pointers, token.data_ptr(), prob.data_ptr(), M, V,
+                              logits.stride(0) if M > 1 else V, *numbers, t))
+    return token, prob

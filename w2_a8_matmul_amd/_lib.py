@@ -26,6 +26,7 @@ _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
 _U64 = ctypes.c_uint64
+_D = ctypes.c_double
 
 # name -> (restype, argtypes); mirrors include/s3d8.h
 SIGNATURES = {
@@ -62,6 +63,11 @@ SIGNATURES = {
     "s3d8_w4_forward": (_I32, [_P, _I64, _I64, _I64, _P, _I64, _I64, _I32, _P, _I32, _P, _P, _P]),
     "s3d8_block_norm": (_I32, [_P, _P]),
     "s3d8_glu_act": (_I32, [_P, _I64, _P, _I64, _I64, _I64, _I32, _I32, _P, _P, _P, _P]),
+    "s3d8_rope_frequencies": (_I32, [_I64, _D, _I32, _D, _D, _D, _D, _P, _P]),
+    "s3d8_head_rope": (_I32, [_P, _P]),
+    "s3d8_cross_attention": (_I32, [_P, _P]),
+    "s3d8_cross_attention_workspace_bytes": (_I64, [_P, _I32]),
+    "s3d8_sample": (_I32, [_P, _P]),
     "s3d8_splitk_auto": (_I32, [_I64, _I64, _I64, _I32]),
     "s3d8_splitk_workspace_bytes": (_I64, [_I64, _I64, _I64, _I32]),
 }
@@ -84,6 +90,40 @@ class BlockNormArgs(ctypes.Structure):
 # the same struct packed into bytes (0.6 us against 2.5 us for filling a Structure)
 BLOCK_NORM_ARGS = struct.Struct("11Q2qdf6i4x").pack
 assert struct.calcsize("11Q2qdf6i4x") == ctypes.sizeof(BlockNormArgs)
+
+
+class HeadRopeArgs(ctypes.Structure):
+    """s3d8_head_rope_args of include/s3d8.h."""
+    _fields_ = [(f, _P) for f in ("q", "k", "q_out", "k_out", "q_weight", "k_weight", "positions", "frequencies")]
+    _fields_ += [(f, _I64) for f in ("M", "q_heads", "k_heads", "D", "rotary_dim", "q_row", "q_head", "k_row", "k_head",
+                                     "q_out_row", "q_out_head", "k_out_row", "k_out_head")]
+    _fields_ += [("eps", ctypes.c_float), ("factor", ctypes.c_float)]
+    _fields_ += [(f, _I32) for f in ("in_type", "out_type", "positions_64", "interleaved")]
+
+
+class CrossAttentionArgs(ctypes.Structure):
+    """s3d8_cross_attention_args of include/s3d8.h."""
+    _fields_ = [(f, _P) for f in ("q", "k", "v", "kv_lens", "mask", "o", "xq", "xs", "workspace")]
+    _fields_ += [(f, _I64) for f in ("workspace_bytes", "B", "Lq", "Lk", "heads", "kv_heads", "D", "q_seq", "q_row",
+                                     "q_head", "k_seq", "k_row", "k_head", "v_seq", "v_row", "v_head", "mask_seq",
+                                     "mask_row")]
+    _fields_ += [("scale", ctypes.c_float), ("shared", _I32)]
+
+
+class SampleArgs(ctypes.Structure):
+    """s3d8_sample_args of include/s3d8.h."""
+    _fields_ = [(f, _P) for f in ("logits", "u", "temperature", "top_k", "top_p", "min_p", "token", "prob")]
+    _fields_ += [("M", _I64), ("V", _I64), ("row", _I64), ("temperature_all", ctypes.c_float), ("top_k_all", _I32),
+                 ("top_p_all", ctypes.c_float), ("min_p_all", ctypes.c_float), ("type", _I32)]
+
+
+# the same structs packed into bytes, as above
+HEAD_ROPE_ARGS = struct.Struct("8Q13q2f4i").pack
+CROSS_ATTENTION_ARGS = struct.Struct("9Q18qfi").pack
+SAMPLE_ARGS = struct.Struct("8Q3qfiffi4x").pack
+assert struct.calcsize("8Q13q2f4i") == ctypes.sizeof(HeadRopeArgs)
+assert struct.calcsize("9Q18qfi") == ctypes.sizeof(CrossAttentionArgs)
+assert struct.calcsize("8Q3qfiffi4x") == ctypes.sizeof(SampleArgs)
 
 _lib = None
 

@@ -458,9 +458,27 @@ __global__ __launch_bounds__(T) void glu_act_kernel(const void *__restrict__ gat
     row_out<T, NV>(v, row, K, out_type, rows, xq, xs, maxima[2]);
 }
 
+// Codes and scales of bf16 rows, as s3d8_quant_act makes them.
+template <int T, int NV>
+__global__ __launch_bounds__(T) void row_codes_kernel(const void *__restrict__ rows, int K, int8_t *__restrict__ xq,
+                                                      float *__restrict__ xs) {
+    __shared__ float maxima[T / 64];
+    const int64_t row = blockIdx.x;
+    Raw<true> r[NV];
+    load_row<T, NV, true>(r, rows, row * K, K >> 2);
+    float4 v[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) v[j] = values(r[j]);
+    row_out<T, NV>(v, row, K, S3D8_ROWS_CODES, nullptr, xq, xs, maxima);
+}
+
 // --------------------------------------------------------------- host
 
 // Kernels by workgroup and row width.
+struct RowCodes {
+    template <int T, int NV>
+    static constexpr auto kernel() { return &row_codes_kernel<T, NV>; }
+};
 template <bool kLayer>
 struct BlockNorm {
     template <int T, int NV>
@@ -522,6 +540,12 @@ int check_out(int32_t out_type, const void *rows, const int8_t *xq, const float 
 }
 
 }  // namespace
+
+void s3d8::codes_of_rows(const void *rows, int64_t M, int64_t K, int8_t *xq, float *xs, int cus, void *stream) {
+    int threads = 0;
+    const auto fn = row_kernel<RowCodes>(M, K, cus, 7, threads);
+    hipLaunchKernelGGL(fn, dim3((unsigned)M), dim3(threads), 0, (hipStream_t)stream, rows, (int)K, xq, xs);
+}
 
 extern "C" {
 

@@ -1,0 +1,353 @@
+// Query and key heads between their projections and attention, for gfx950: the RMS
+// norm of each head and its rotary position, queries and keys in one launch.
+//
+// A head is read once into the registers of 8 to 64 lanes, its squares are summed
+// there, and it is written once.  Angles are position * frequency in 64 bits, reduced
+// to a part of a turn before anything is rounded to fp32, so that far positions keep
+// their phase; a workgroup computes cosine and sine once per token and pair and
+// takes them from LDS for all of the token's heads.
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <type_traits>
+
+#include "s3d8.h"
+#include "s3d8_device.h"
+#include "s3d8_internal.h"
+
+namespace {
+
+constexpr int kMaxHead = 256;
+constexpr int64_t kMaxTokens = 1 << 19;
+constexpr int64_t kMaxStride = int64_t(1) << 40;
+constexpr int kTokens = 4;      // most tokens a workgroup takes
+constexpr int kThreads = 256;
+
+// Cosine and sine of `angle` radians, each times `factor`, as fp32.  The angle goes to
+// turns and their fraction in 64 bits, from there to the nearest quarter turn and a
+// rest of at most an eighth, on which the Taylor series to the ninth and eighth
+// degree are off by less than 2^-27.
+__device__ __forceinline__ float2 turned(double angle, float factor) {
+    const double t = angle * 0x1.45f306dc9c883p-3;  // 1 / (2 pi)
+    const double r = 4.0 * (t - __builtin_rint(t));
+    const double quarter = __builtin_rint(r);
+    const float x = (float)((r - quarter) * 0x1.921fb54442d18p+0);  // pi / 2
+    const float z = x * x;
+    float s = __builtin_fmaf(z, 1.0f / 362880, -1.0f / 5040);
+    s = __builtin_fmaf(z, s, 1.0f / 120);
+    s = __builtin_fmaf(z, s, -1.0f / 6);
+    s = __builtin_fmaf(z * x, s, x);
+    float c = __builtin_fmaf(z, 1.0f / 40320, -1.0f / 720);
+    c = __builtin_fmaf(z, c, 1.0f / 24);
+    c = __builtin_fmaf(z, c, -0.5f);
+    c = __builtin_fmaf(z, c, 1.0f);
+    const int q = (int)quarter & 3;
+    const float cq = q & 1 ? s : c, sq = q & 1 ? c : s;
+    return make_float2(factor * (q == 1 || q == 2 ? -cq : cq), factor * (q >= 2 ? -sq : sq));
+}
+
+// V values from element `at` of fp32 or bf16 rows, and to them (V = 4: aligned to 4 elements).
+template <int V, bool kBF>
+__device__ __forceinline__ void load(float (&x)[V], const void *p, int64_t at) {
+    if constexpr (kBF) {
+        const uint16_t *e = static_cast<const uint16_t *>(p) + at;
+        if constexpr (V == 4) {
+            const uint2 u = *reinterpret_cast<const uint2 *>(e);
+            x[0] = __uint_as_float(u.x << 16);
+            x[1] = __uint_as_float(u.x & 0xFFFF0000u);
+            x[2] = __uint_as_float(u.y << 16);
+            x[3] = __uint_as_float(u.y & 0xFFFF0000u);
+        } else {
+            x[0] = bf16_to_f32(*e);
+        }
+    } else {
+        const float *e = static_cast<const float *>(p) + at;
+        if constexpr (V == 4) {
+            const float4 u = *reinterpret_cast<const float4 *>(e);
+            x[0] = u.x;
+            x[1] = u.y;
+            x[2] = u.z;
+            x[3] = u.w;
+        } else {
+            x[0] = *e;
+        }
+    }
+}
+template <int V>
+__device__ __forceinline__ void store(void *p, int64_t at, const float (&x)[V], bool bf) {
+    if (bf) {
+        __bf16 *e = static_cast<__bf16 *>(p) + at;
+        if constexpr (V == 4) {
+            typedef __bf16 bf4 __attribute__((ext_vector_type(4)));
+            *reinterpret_cast<bf4 *>(e) = bf4{(__bf16)x[0], (__bf16)x[1], (__bf16)x[2], (__bf16)x[3]};
+        } else {
+            *e = (__bf16)x[0];
+        }
+    } else {
+        float *e = static_cast<float *>(p) + at;
+        if constexpr (V == 4)
+            *reinterpret_cast<float4 *>(e) = make_float4(x[0], x[1], x[2], x[3]);
+        else
+            *e = x[0];
+    }
+}
+
+// Sum over groups of G lanes (a power of two), in every lane of the group.
+template <int G>
+__device__ __forceinline__ float group_sum(float v) {
+    auto dpp = [](float x, auto ctrl) {
+        return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(x), decltype(ctrl)::value, 0xF,
+                                                                     0xF, false));
+    };
+    v += dpp(v, std::integral_constant<int, 0xB1>());
+    v += dpp(v, std::integral_constant<int, 0x4E>());
+    v += dpp(v, std::integral_constant<int, 0x141>());
+    if constexpr (G >= 16) v += dpp(v, std::integral_constant<int, 0x140>());
+    if constexpr (G >= 32) v += __shfl_xor(v, 16);
+    if constexpr (G >= 64) v += __shfl_xor(v, 32);
+    return v;
+}
+
+// One group of G lanes per head: lane i holds the V pairs of chunks i, i + G, ...,
+// NC of them, a chunk being V elements at `first` and V at `second`.  In the turned
+// part these are the two sides of V pairs (half layout: rot / 2 apart;
+// interleaved: 2 V elements in a row, whose pairs are side by side); past it 2 V
+// elements in a row that stay as they are.
+template <int V, int G, int NC, bool kBF>
+__global__ __launch_bounds__(kThreads) void head_rope_kernel(const s3d8_head_rope_args a, int tokens, int heads) {
+    __shared__ float2 turn[kTokens * kMaxHead / 2];
+    constexpr int kGroups = kThreads / G;
+    const int lane = threadIdx.x % G, group = threadIdx.x / G;
+    const int D = (int)a.D, half = (int)a.rotary_dim / 2, all = (int)(a.q_heads + a.k_heads);
+    const int64_t token0 = (int64_t)blockIdx.x * tokens;
+    const int head0 = blockIdx.y * heads;
+    const int nt = (int)min((int64_t)tokens, a.M - token0), nh = min(heads, all - head0);
+    const bool side_by_side = a.interleaved != 0;
+
+    int first[NC], second[NC];
+    bool in[NC], turns[NC];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        const int p = (lane + c * G) * V;  // the chunk's first pair
+        in[c] = 2 * p < D;
+        turns[c] = p < half;
+        first[c] = turns[c] && !side_by_side ? p : 2 * p;
+        second[c] = first[c] + (turns[c] && !side_by_side ? half : V);
+    }
+    struct Head {
+        float x[NC][2][V];
+    };
+    auto load_head = [&](int item, Head &h) {
+        const int64_t token = token0 + item / nh;
+        const int head = head0 + item % nh;
+        const bool q = head < a.q_heads;
+        const void *p = q ? a.q : a.k;
+        const int64_t at = q ? token * a.q_row + head * a.q_head : token * a.k_row + (head - a.q_heads) * a.k_head;
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+            if (in[c]) {
+                load<V, kBF>(h.x[c][0], p, at + first[c]);
+                load<V, kBF>(h.x[c][1], p, at + second[c]);
+            }
+    };
+    const int items = nt * nh;
+    Head next, qw, kw;  // weights: as they lie in a head
+    if (group < items) load_head(group, next);
+    auto load_weight = [&](const float *w, Head &h) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                h.x[c][0][v] = w && in[c] ? w[first[c] + v] : 0.0f;
+                h.x[c][1][v] = w && in[c] ? w[second[c] + v] : 0.0f;
+            }
+    };
+    load_weight(a.q_weight, qw);
+    load_weight(a.k_weight, kw);
+    if (half) {
+        for (int i = threadIdx.x; i < nt * half; i += kThreads) {
+            const int64_t token = token0 + i / half;
+            const double pos = a.positions_64 ? (double)static_cast<const int64_t *>(a.positions)[token]
+                                              : (double)static_cast<const int32_t *>(a.positions)[token];
+            turn[i] = turned(pos * a.frequencies[i % half], a.factor);
+        }
+        __syncthreads();
+    }
+    for (int item = group; item < items; item += kGroups) {
+        Head h = next;
+        if (item + kGroups < items) load_head(item + kGroups, next);
+        const int t = item / nh, head = head0 + item % nh;
+        const bool q = head < a.q_heads;
+        if (q ? a.q_weight : a.k_weight) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+                if (in[c])
+#pragma unroll
+                    for (int s = 0; s < 2; ++s)
+#pragma unroll
+                        for (int v = 0; v < V; ++v) sum = __builtin_fmaf(h.x[c][s][v], h.x[c][s][v], sum);
+            const float r = __builtin_amdgcn_rsqf(group_sum<G>(sum) / (float)D + a.eps);
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+                if (in[c])
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        h.x[c][0][v] = h.x[c][0][v] * r * (q ? qw : kw).x[c][0][v];
+                        h.x[c][1][v] = h.x[c][1][v] * r * (q ? qw : kw).x[c][1][v];
+                    }
+        }
+        void *p = q ? a.q_out : a.k_out;
+        const int64_t token = token0 + t;
+        const int64_t at = q ? token * a.q_out_row + head * a.q_out_head
+                             : token * a.k_out_row + (head - a.q_heads) * a.k_out_head;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            if (!in[c]) continue;
+            if (turns[c]) {
+                const float2 *cs = turn + t * half + (lane + c * G) * V;
+                auto rotate = [](float &x, float &y, float2 f) {
+                    const float u = x * f.x - y * f.y;
+                    y = y * f.x + x * f.y;
+                    x = u;
+                };
+                if (V > 1 && side_by_side) {
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {  // pair v: elements 2 v and 2 v + 1 of the 2 V in a row
+                        float *e = &h.x[c][0][0] + 2 * v;
+                        rotate(e[0], e[1], cs[v]);
+                    }
+                } else {
+#pragma unroll
+                    for (int v = 0; v < V; ++v) rotate(h.x[c][0][v], h.x[c][1][v], cs[v]);
+                }
+            }
+            store<V>(p, at + first[c], h.x[c][0], a.out_type == S3D8_ROWS_BF16);
+            store<V>(p, at + second[c], h.x[c][1], a.out_type == S3D8_ROWS_BF16);
+        }
+    }
+}
+
+using HeadRopeFn = void (*)(s3d8_head_rope_args, int, int);
+
+// Four pairs a lane where the two sides of every four lie in fours of elements
+// (wide loads), else a pair a lane.
+template <bool kBF>
+HeadRopeFn head_rope_build(bool fours, int64_t D, int &lanes) {
+    if (!fours) {
+        lanes = 64;
+        return D <= 128 ? head_rope_kernel<1, 64, 1, kBF> : head_rope_kernel<1, 64, 2, kBF>;
+    }
+    lanes = D <= 64 ? 8 : D <= 128 ? 16 : 32;
+    return D <= 64    ? head_rope_kernel<4, 8, 1, kBF>
+           : D <= 128 ? head_rope_kernel<4, 16, 1, kBF>
+                      : head_rope_kernel<4, 32, 1, kBF>;
+}
+
+bool row_type(int32_t t) { return t == S3D8_ROWS_F32 || t == S3D8_ROWS_BF16; }
+
+// Row and head strides of M x heads heads of D, and the pointer's alignment to an element.
+int check_heads(const void *p, int64_t M, int64_t heads, int64_t D, int64_t row, int64_t head, int32_t type) {
+    if (reinterpret_cast<uintptr_t>(p) & (type == S3D8_ROWS_F32 ? 3 : 1))
+        return s3d8::fail(S3D8_ERR_ALIGN, "heads must be aligned to an element");
+    if ((heads > 1 && head < D) || (M > 1 && row < D) || head < 0 || row < 0 || head > kMaxStride || row > kMaxStride)
+        return s3d8::fail(S3D8_ERR_INVALID_ARG, "row and head strides must be at least the head's size (and at most 2^40)");
+    return S3D8_OK;
+}
+
+bool by_fours(const void *p, int64_t row, int64_t head, int32_t type) {
+    return (reinterpret_cast<uintptr_t>(p) & (type == S3D8_ROWS_F32 ? 15 : 7)) == 0 && row % 4 == 0 && head % 4 == 0;
+}
+
+}  // namespace
+
+extern "C" {
+
+int32_t s3d8_rope_frequencies(int64_t rotary_dim, double base, int32_t scaling, double factor, double original_length,
+                              double low, double high, double *frequencies, double *attention_factor) {
+    if (!frequencies || !attention_factor) return s3d8::fail(S3D8_ERR_INVALID_ARG, "null pointer argument");
+    if (rotary_dim <= 0 || rotary_dim % 2 || rotary_dim > kMaxHead)
+        return s3d8::fail(S3D8_ERR_SHAPE, "rotary_dim must be even, from 2 to 256");
+    if (!(base > 1.0 && base <= 1e30)) return s3d8::fail(S3D8_ERR_INVALID_ARG, "base must be over 1 (and at most 1e30)");
+    if (scaling < S3D8_ROPE_PLAIN || scaling > S3D8_ROPE_YARN)
+        return s3d8::fail(S3D8_ERR_INVALID_ARG, "unknown kind of scaling");
+    if (scaling != S3D8_ROPE_PLAIN && !(factor >= 1.0 && factor <= 1e9))
+        return s3d8::fail(S3D8_ERR_INVALID_ARG, "factor must be at least 1 (and at most 1e9)");
+    const bool by_length = scaling == S3D8_ROPE_LLAMA3 || scaling == S3D8_ROPE_YARN;
+    if (by_length && !(original_length >= 1.0 && original_length <= 1e12 && low > 0.0 && low < high && high <= 1e9))
+        return s3d8::fail(S3D8_ERR_INVALID_ARG, "original_length must be positive, and low and high turns 0 < low < high");
+    const double pi = 3.14159265358979323846;
+    double first = 0.0, last = 0.0;
+    if (scaling == S3D8_ROPE_YARN) {  // the pairs that make `high` and `low` turns over the original length
+        auto pair = [&](double turns) {
+            return (double)rotary_dim * std::log(original_length / (turns * 2.0 * pi)) / (2.0 * std::log(base));
+        };
+        first = std::fmax(std::floor(pair(high)), 0.0);
+        last = std::fmin(std::ceil(pair(low)), (double)(rotary_dim - 1));
+    }
+    for (int64_t j = 0; j < rotary_dim / 2; ++j) {
+        const double f = std::pow(base, -2.0 * (double)j / (double)rotary_dim);
+        double stretch = 0.0;  // share of the frequency divided by factor
+        if (scaling == S3D8_ROPE_LINEAR) stretch = 1.0;
+        if (scaling == S3D8_ROPE_LLAMA3)
+            stretch = 1.0 - std::fmin(std::fmax((original_length * f / (2.0 * pi) - low) / (high - low), 0.0), 1.0);
+        if (scaling == S3D8_ROPE_YARN)
+            stretch = std::fmin(std::fmax(((double)j - first) / std::fmax(last - first, 0.001), 0.0), 1.0);
+        frequencies[j] = f * (1.0 - stretch) + (stretch > 0.0 ? f / factor * stretch : 0.0);
+    }
+    *attention_factor = scaling == S3D8_ROPE_YARN ? 0.1 * std::log(factor) + 1.0 : 1.0;
+    s3d8::clear_error();
+    return S3D8_OK;
+}
+
+int32_t s3d8_head_rope(const s3d8_head_rope_args *args, void *stream) {
+    if (!args || !args->q || !args->q_out) return s3d8::fail(S3D8_ERR_INVALID_ARG, "null pointer argument");
+    s3d8_head_rope_args a = *args;
+    if ((a.k != nullptr) != (a.k_out != nullptr) || (a.k != nullptr) != (a.k_heads != 0))
+        return s3d8::fail(S3D8_ERR_INVALID_ARG, "k, k_out and k_heads go together");
+    if (!a.k && a.k_weight) return s3d8::fail(S3D8_ERR_INVALID_ARG, "k_weight needs k");
+    if (a.M <= 0 || a.q_heads <= 0 || a.k_heads < 0 || a.D <= 0 || a.rotary_dim < 0)
+        return s3d8::fail(S3D8_ERR_INVALID_ARG, "sizes must be positive");
+    if (a.D % 2 || a.D > kMaxHead) return s3d8::fail(S3D8_ERR_SHAPE, "heads must be of an even size up to 256");
+    if (a.rotary_dim % 2 || a.rotary_dim > a.D)
+        return s3d8::fail(S3D8_ERR_SHAPE, "rotary_dim must be even and at most the head's size");
+    if (a.M > kMaxTokens || a.q_heads > 4096 || a.k_heads > 4096)
+        return s3d8::fail(S3D8_ERR_SHAPE, "more than 524288 tokens or 4096 heads are not supported");
+    if (a.rotary_dim && (!a.positions || !a.frequencies))
+        return s3d8::fail(S3D8_ERR_INVALID_ARG, "rotary_dim needs positions and frequencies");
+    if (!a.rotary_dim && !a.q_weight && !a.k_weight)
+        return s3d8::fail(S3D8_ERR_INVALID_ARG, "neither a norm nor a rotary position");
+    if (!row_type(a.in_type) || !row_type(a.out_type)) return s3d8::fail(S3D8_ERR_INVALID_ARG, "unknown row type");
+    if (!(a.eps >= 0x1p-126f && a.eps <= 0x1p126f))
+        return s3d8::fail(S3D8_ERR_INVALID_ARG, "eps must be positive (2^-126 to 2^126)");
+    if (!(std::fabs(a.factor) <= 0x1p100f)) return s3d8::fail(S3D8_ERR_INVALID_ARG, "factor must be finite (at most 2^100)");
+    int rc = check_heads(a.q, a.M, a.q_heads, a.D, a.q_row, a.q_head, a.in_type);
+    if (!rc) rc = check_heads(a.q_out, a.M, a.q_heads, a.D, a.q_out_row, a.q_out_head, a.out_type);
+    if (!rc && a.k) rc = check_heads(a.k, a.M, a.k_heads, a.D, a.k_row, a.k_head, a.in_type);
+    if (!rc && a.k) rc = check_heads(a.k_out, a.M, a.k_heads, a.D, a.k_out_row, a.k_out_head, a.out_type);
+    if (rc) return rc;
+    if ((reinterpret_cast<uintptr_t>(a.q_weight) | reinterpret_cast<uintptr_t>(a.k_weight)) & 3 ||
+        reinterpret_cast<uintptr_t>(a.frequencies) & 7 || reinterpret_cast<uintptr_t>(a.positions) & (a.positions_64 ? 7 : 3))
+        return s3d8::fail(S3D8_ERR_ALIGN, "weights, frequencies and positions must be aligned to an element");
+    int cus = 0;
+    rc = s3d8::check_device(&cus);
+    if (rc) return rc;
+    const bool fours = a.D % 8 == 0 && a.rotary_dim % 8 == 0 && by_fours(a.q, a.q_row, a.q_head, a.in_type) &&
+                       by_fours(a.q_out, a.q_out_row, a.q_out_head, a.out_type) &&
+                       (!a.k || (by_fours(a.k, a.k_row, a.k_head, a.in_type) &&
+                                 by_fours(a.k_out, a.k_out_row, a.k_out_head, a.out_type)));
+    int lanes = 0;
+    const HeadRopeFn fn =
+        a.in_type == S3D8_ROWS_BF16 ? head_rope_build<true>(fours, a.D, lanes) : head_rope_build<false>(fours, a.D, lanes);
+    const int groups = kThreads / lanes, heads = (int)(a.q_heads + a.k_heads);
+    // Many heads: kTokens tokens with all their heads a workgroup, so that an angle is computed once.
+    // Few: a head a group, on as many CUs as there are.
+    const bool many = a.M * heads >= (int64_t)groups * cus * 4;
+    const int tokens = many ? kTokens : 1, per = many ? heads : groups;
+    hipLaunchKernelGGL(fn, dim3((unsigned)((a.M + tokens - 1) / tokens), (unsigned)((heads + per - 1) / per)), dim3(kThreads),
+                       0, (hipStream_t)stream, a, tokens, per);
+    return s3d8::launch_status();
+}
+
+}  // extern "C"
