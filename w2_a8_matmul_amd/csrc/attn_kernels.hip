@@ -13,12 +13,16 @@
 namespace {
 
 typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
 typedef short s4 __attribute__((ext_vector_type(4)));
 typedef float f16v __attribute__((ext_vector_type(16)));
 
 constexpr int kKeys = 64;       // keys in a block
 constexpr int kRows = 32;       // query rows of a wave
 constexpr int kMaxSplits = 64;
+// The maximum that is taken off the scores is only raised when a score is past it by this power
+// of 2: p up to 2^8 is as exact in bf16 and fp32 as p up to 1, and most blocks scale nothing.
+constexpr float kSlack = 8.0f;
 
 // What the kernels read: a pair is a sequence and a key head, whose R = T * G rows are
 // its T query tokens (of all sequences, where they share their states) times the G query
@@ -48,7 +52,11 @@ __device__ __forceinline__ int value_place(int c, int r) {
     return CPR == 16 ? c ^ ((r & 3) << 2) : CPR == 8 ? c ^ (((r >> 1) & 1) << 2) : c;
 }
 
-__device__ __forceinline__ float other_half_max(float x) { return fmaxf(x, __shfl_xor(x, 32)); }
+// The larger of a lane's value and that of the lane 32 further.
+__device__ __forceinline__ float halves_max(float x) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
 
 // sum_j p_j v_j of one row over the keys from `begin` to `end` that it sees: entries
 // `lane` and `lane` + 64.
@@ -107,7 +115,7 @@ __global__ __launch_bounds__(64 * kW, 2) void attn_kernel(const Attn a) {
         if (16 * s + 8 * h < a.D) u = *reinterpret_cast<const uint4 *>(qp + 16 * s + 8 * h);
         qf[s] = __builtin_bit_cast(bf8, u);
     }
-    const uint64_t *words = a.words ? a.words + b * a.word_seq + i * a.word_row : nullptr;
+    const int64_t word_at = b * a.word_seq + i * a.word_row;
 
     // the lane's part of each copy of a tile into LDS
     constexpr int kCopies = CPR / kW;
@@ -120,16 +128,19 @@ __global__ __launch_bounds__(64 * kW, 2) void attn_kernel(const Attn a) {
         voff[n] = 8 * vc < a.D ? (uint32_t)r * (uint32_t)a.v_row * 2 + vc * 16 : kOOB;
     }
     const uint16_t *kp = a.k + seq * a.k_seq + head * a.k_head, *vp = a.v + seq * a.v_seq + head * a.v_head;
-    auto copy = [&](int block, int buf) {
+    auto copy_keys = [&](int block) {
         const int rows = min(kKeys, len - block * kKeys) - 1;
-        const v4i kr = rsrc_words(kp + (int64_t)block * kKeys * a.k_row, (uint32_t)(rows * a.k_row + a.D) * 2);
-        const v4i vr = rsrc_words(vp + (int64_t)block * kKeys * a.v_row, (uint32_t)(rows * a.v_row + a.D) * 2);
+        const v4i r = rsrc_words(kp + (int64_t)block * kKeys * a.k_row, (uint32_t)(rows * a.k_row + a.D) * 2);
 #pragma unroll
         for (int n = 0; n < kCopies; ++n)
-            load_to_lds16_so(S3D8_LDS_OFFSET(&tiles[buf][0][(wave + n * kW) * 64]), koff[n], 0, kr);
+            load_to_lds16_so(S3D8_LDS_OFFSET(&tiles[0][block & 1][(wave + n * kW) * 64]), koff[n], 0, r);
+    };
+    auto copy_values = [&](int block) {
+        const int rows = min(kKeys, len - block * kKeys) - 1;
+        const v4i r = rsrc_words(vp + (int64_t)block * kKeys * a.v_row, (uint32_t)(rows * a.v_row + a.D) * 2);
 #pragma unroll
         for (int n = 0; n < kCopies; ++n)
-            load_to_lds16_so(S3D8_LDS_OFFSET(&tiles[buf][1][(wave + n * kW) * 64]), voff[n], 0, vr);
+            load_to_lds16_so(S3D8_LDS_OFFSET(&tiles[1][block & 1][(wave + n * kW) * 64]), voff[n], 0, r);
     };
 
     f16v acc[ND];
@@ -138,96 +149,140 @@ __global__ __launch_bounds__(64 * kW, 2) void attn_kernel(const Attn a) {
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[d][r] = 0.0f;
     float most = -FLT_MAX, sum = 0.0f;  // of scaled scores, in powers of 2; this lane's part of the sum
-    uint64_t next_word = ~0ull;
-    if (first < last) {
-        if (words) next_word = words[first * a.word_block];
-        copy(first, 0);
-    }
-    for (int block = first; block < last; ++block) {
-        const int buf = (block - first) & 1;
-        wait_vmcnt_barrier<0>();
-        uint64_t word = next_word;
-        if (block + 1 < last) {
-            if (words) next_word = words[(block + 1) * a.word_block];
-            copy(block + 1, buf ^ 1);
-        }
-        const int inside = len - block * kKeys;
-        if (inside < kKeys) word &= (1ull << inside) - 1;
-        if (__ballot(word != 0) == 0) continue;
 
-        // scores, transposed: key by register, row by lane
-        f16v s[2];
-        const char *keys = reinterpret_cast<const char *>(tiles[buf][0]);
+    // a score operand (32 keys, 16 entries) and a value operand (32 entries, 16 keys; transposed by the
+    // read: entry by lane, four keys in a row) of a block
+    auto key_operand = [&](int block, int i) {
+        const int n = i / 2, r = i % 2 * 32 + col;
+        return *reinterpret_cast<const bf8 *>(reinterpret_cast<const char *>(tiles[0][block & 1]) +
+                                              (r * CPR + key_place<CPR>(2 * n + h, r)) * 16);
+    };
+    auto value_operand = [&](int block, int i) {
+        const int n = i / ND, d = i % ND;
+        struct Two {
+            s4 x[2];
+        } two;
 #pragma unroll
-        for (int kt = 0; kt < 2; ++kt) {
-#pragma unroll
-            for (int r = 0; r < 16; ++r) s[kt][r] = 0.0f;
-#pragma unroll
-            for (int n = 0; n < NK; ++n) {
-                const int r = kt * 32 + col;
-                const bf8 kf = *reinterpret_cast<const bf8 *>(keys + (r * CPR + key_place<CPR>(2 * n + h, r)) * 16);
-                s[kt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[n], s[kt], 0, 0, 0);
-            }
+        for (int j = 0; j < 2; ++j) {
+            const int r = 16 * n + 8 * j + 4 * h + ((lane & 15) >> 2);
+            const int c = 4 * d + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+            two.x[j] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (__attribute__((address_space(3))) s4 *)(reinterpret_cast<const char *>(tiles[1][block & 1]) +
+                                                         (r * CPR + value_place<CPR>(c, r)) * 16 + 8 * (lane & 1)));
         }
-        if (__ballot(word != ~0ull)) {
-            const uint64_t mine = word >> (4 * h);
-#pragma unroll
-            for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const uint32_t bits = (uint32_t)(mine >> (32 * kt));
-                    s[kt][r] = bits >> (8 * (r / 4) + r % 4) & 1 ? s[kt][r] : -INFINITY;
-                }
-        }
+        return __builtin_bit_cast(bf8, two);
+    };
+    auto word_of = [&](int block, uint64_t word) {
+        const int inside = len - block * kKeys;
+        return inside < kKeys ? word & ((1ull << max(inside, 0)) - 1) : word;
+    };
+    auto load_word = [&](int block) { return a.words[word_at + block * a.word_block]; };
+    auto most_of = [&](const f16v(&s)[2]) {
         float m = s[0][0];
 #pragma unroll
         for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
             for (int r = 0; r < 16; ++r) m = fmaxf(m, s[kt][r]);
-        m = fmaxf(most, other_half_max(m) * a.scale);
-        if (__ballot(m > most)) {
-            const float f = __builtin_amdgcn_exp2f(most - m);
-            most = m;
-            sum *= f;
-#pragma unroll
-            for (int d = 0; d < ND; ++d)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) acc[d][r] *= f;
+        return m;
+    };
+
+    // Scores are transposed: key by register, row by lane.  Block n is weighed and added while the
+    // scores of block n + 1 are computed: their products run beside the exponentials, and the
+    // largest of them is found beside the products with the values.
+    if (first < last) {
+        uint64_t word = ~0ull, next_word = ~0ull;
+        if (a.words) word = load_word(first);
+        copy_keys(first);
+        copy_values(first);
+        wait_vmcnt_barrier<0>();
+        word = word_of(first, word);
+        if (first + 1 < last) {
+            if (a.words) next_word = load_word(first + 1);
+            copy_keys(first + 1);
         }
-        bf8 pf[2][2];
+        f16v s[2], t[2];
 #pragma unroll
-        for (int kt = 0; kt < 2; ++kt)
+        for (int r = 0; r < 16; ++r) s[0][r] = s[1][r] = 0.0f;
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kt][r], a.scale, -most));
-                sum += p;
-                pf[kt][r / 8][r % 8] = (__bf16)p;
+        for (int i = 0; i < 2 * NK; ++i)
+            s[i % 2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(key_operand(first, i), qf[i / 2], s[i % 2], 0, 0, 0);
+        float m = most_of(s);
+
+        auto step = [&](int block, f16v(&s)[2], f16v(&t)[2]) {
+            wait_vmcnt_barrier<0>();
+            const uint64_t after = word_of(block + 1, next_word);
+            if (block + 2 < last) {
+                if (a.words) next_word = load_word(block + 2);
+                copy_keys(block + 2);
             }
-        // values, transposed by the read: entry by lane, four keys in a row
-        const char *values = reinterpret_cast<const char *>(tiles[buf][1]);
+            if (block + 1 < last) copy_values(block + 1);
+            if (__ballot(word != ~0ull)) {
+                const uint64_t mine = word >> (4 * h);
 #pragma unroll
-        for (int kt = 0; kt < 2; ++kt)
+                for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int d = 0; d < ND; ++d) {
-                    s4 part[2];
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const int r = 32 * kt + 16 * n + 8 * j + 4 * h + ((lane & 15) >> 2);
-                        const int c = 4 * d + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
-                        part[j] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                            (__attribute__((address_space(3))) s4 *)(values + (r * CPR + value_place<CPR>(c, r)) * 16 +
-                                                                     8 * (lane & 1)));
+                    for (int r = 0; r < 16; ++r) {
+                        const uint32_t bits = (uint32_t)(mine >> (32 * kt));
+                        s[kt][r] = bits >> (8 * (r / 4) + r % 4) & 1 ? s[kt][r] : -INFINITY;
                     }
-                    struct Two {
-                        s4 x[2];
-                    } two = {{part[0], part[1]}};
-                    acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf8, two), pf[kt][n], acc[d], 0, 0, 0);
+                m = most_of(s);
+            }
+            word = after;
+            m = halves_max(m) * a.scale;
+            if (__ballot(m > most + kSlack)) {
+                m = fmaxf(most, m);
+                const float f = __builtin_amdgcn_exp2f(most - m);
+                most = m;
+                sum *= f;
+#pragma unroll
+                for (int d = 0; d < ND; ++d)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) acc[d][r] *= f;
+            }
+            constexpr int kAhead = 4;  // operands in flight
+            bf8 operand[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) operand[i] = key_operand(block + 1, i);
+            uint32_t pf[16];
+#pragma unroll
+            for (int r = 0; r < 16; ++r) t[0][r] = t[1][r] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 2 * NK; ++i) {
+                __builtin_amdgcn_sched_barrier(0);
+                t[i % 2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(operand[i % kAhead], qf[i / 2], t[i % 2], 0, 0, 0);
+                operand[i % kAhead] = i + kAhead < 2 * NK ? key_operand(block + 1, i + kAhead)
+                                                          : value_operand(block, i + kAhead - 2 * NK);
+#pragma unroll
+                for (int e = i * 16 / (2 * NK); e < (i + 1) * 16 / (2 * NK); ++e) {
+                    bf2 pair;
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+                        pair[x] = (__bf16)__builtin_amdgcn_exp2f(__builtin_fmaf(s[e / 8][2 * (e % 8) + x], a.scale, -most));
+                    sum = __builtin_amdgcn_fdot2_f32_bf16(pair, bf2{(__bf16)1.0f, (__bf16)1.0f}, sum, false);
+                    pf[e] = __builtin_bit_cast(uint32_t, pair);
                 }
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            }
+            m = t[0][0];
+#pragma unroll
+            for (int i = 0; i < 4 * ND; ++i) {
+                __builtin_amdgcn_sched_barrier(0);
+                const uint4 p = make_uint4(pf[i / ND * 4], pf[i / ND * 4 + 1], pf[i / ND * 4 + 2], pf[i / ND * 4 + 3]);
+                acc[i % ND] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(operand[(i + 2 * NK) % kAhead], __builtin_bit_cast(bf8, p),
+                                                                      acc[i % ND], 0, 0, 0);
+                if (i + kAhead < 4 * ND) operand[(i + 2 * NK) % kAhead] = value_operand(block, i + kAhead);
+#pragma unroll
+                for (int e = i * 32 / (4 * ND); e < (i + 1) * 32 / (4 * ND); ++e) m = fmaxf(m, t[e / 16][e % 16]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        for (int block = first;;) {
+            step(block, s, t);
+            if (++block >= last) break;
+            step(block, t, s);
+            if (++block >= last) break;
+        }
     }
-    if (words) {
+    if (a.words) {
         // A hidden key has p = 0, but the product with an infinite or NaN value of it is NaN. Rows that
         // are not finite are summed again, one by one, over what they see.
         float z = 0.0f;
@@ -241,7 +296,7 @@ __global__ __launch_bounds__(64 * kW, 2) void attn_kernel(const Attn a) {
             const int lost = __builtin_ctzll(bad);
             bad &= bad - 1;
             float e[2] = {0.0f, 0.0f};
-            visible_sum(a, __shfl((long long)(qp - a.q), lost), kp, vp, __shfl((long long)(words - a.words), lost),
+            visible_sum(a, __shfl((long long)(qp - a.q), lost), kp, vp, __shfl((long long)word_at, lost),
                         __shfl(most, lost), first * kKeys, min(last * kKeys, len), e);
 #pragma unroll
             for (int d = 0; d < ND; ++d)
@@ -285,35 +340,62 @@ __global__ __launch_bounds__(64 * kW, 2) void attn_kernel(const Attn a) {
         }
 }
 
-// Partial sums of the splits joined: 4 entries a thread.
-__global__ __launch_bounds__(256) void attn_join_kernel(const Attn a) {
-    const int64_t quads = a.D / 4, rows = (int64_t)a.pairs * a.R;
-    const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (n >= rows * quads) return;
-    const int64_t at = n / quads;
-    const int e = (int)(n % quads) * 4;
-    const float *ms = a.part + a.splits * rows * a.D;
-    float most = -FLT_MAX;
-    for (int s = 0; s < a.splits; ++s) most = fmaxf(most, ms[2 * (s * rows + at)]);
-    float4 x = make_float4(0, 0, 0, 0);
-    float sum = 0.0f;
-#pragma unroll 4
-    for (int s = 0; s < a.splits; ++s) {
-        const float2 u = *reinterpret_cast<const float2 *>(ms + 2 * (s * rows + at));
-        const float4 y = *reinterpret_cast<const float4 *>(a.part + (s * rows + at) * a.D + e);
-        const float f = __builtin_amdgcn_exp2f(u.x - most);
-        sum = __builtin_fmaf(f, u.y, sum);
-        x.x = __builtin_fmaf(f, y.x, x.x);
-        x.y = __builtin_fmaf(f, y.y, x.y);
-        x.z = __builtin_fmaf(f, y.z, x.z);
-        x.w = __builtin_fmaf(f, y.w, x.w);
+// Partial sums of the splits joined: 4 entries of a row a thread, kLanes threads of a
+// row's entries sharing its splits, so that a row's loads are all on their way at once (one
+// thread for all of them: 10 us instead of 3 for 32 rows of 26 splits).
+struct Partial {
+    float most, sum;
+    float4 x;
+    __device__ __forceinline__ void join(float m, float n, float4 y) {
+        const float top = fmaxf(most, m), f = __builtin_amdgcn_exp2f(most - top), g = __builtin_amdgcn_exp2f(m - top);
+        most = top;
+        sum = __builtin_fmaf(f, sum, g * n);
+        x.x = __builtin_fmaf(f, x.x, g * y.x);
+        x.y = __builtin_fmaf(f, x.y, g * y.y);
+        x.z = __builtin_fmaf(f, x.z, g * y.z);
+        x.w = __builtin_fmaf(f, x.w, g * y.w);
     }
+};
+template <int kLanes>
+__global__ __launch_bounds__(256) void attn_join_kernel(const Attn a) {
+    constexpr int kRowsHere = 8 / kLanes, kAtOnce = 4;
+    __shared__ Partial parts[256];
+    const int e = (threadIdx.x & 31) * 4, lane = (threadIdx.x >> 5) % kLanes, here = (threadIdx.x >> 5) / kLanes;
+    const int64_t rows = (int64_t)a.pairs * a.R, at = (int64_t)blockIdx.x * kRowsHere + here;
+    const bool in = at < rows && e < a.D;
+    const float *ms = a.part + a.splits * rows * a.D;
+    Partial p{-FLT_MAX, 0.0f, make_float4(0, 0, 0, 0)};
+    if (in)
+        for (int s0 = lane; s0 < a.splits; s0 += kAtOnce * kLanes) {
+            float2 u[kAtOnce];
+            float4 y[kAtOnce];
+#pragma unroll
+            for (int n = 0; n < kAtOnce; ++n) {
+                const int s = min(s0 + n * kLanes, a.splits - 1);
+                u[n] = *reinterpret_cast<const float2 *>(ms + 2 * (s * rows + at));
+                y[n] = *reinterpret_cast<const float4 *>(a.part + (s * rows + at) * a.D + e);
+            }
+#pragma unroll
+            for (int n = 0; n < kAtOnce; ++n)
+                if (s0 + n * kLanes < a.splits) p.join(u[n].x, u[n].y, y[n]);
+        }
+    if constexpr (kLanes > 1) {
+        parts[threadIdx.x] = p;
+        __syncthreads();
+        if (lane) return;
+#pragma unroll
+        for (int n = 1; n < kLanes; ++n) {
+            const Partial &o = parts[threadIdx.x + 32 * n];
+            p.join(o.most, o.sum, o.x);
+        }
+    }
+    if (!in) return;
     const int pair = (int)(at / a.R), row = (int)(at % a.R), seq = pair / a.Hk, head = pair % a.Hk, t = row / a.G, g = row % a.G;
     const int64_t token = a.shared ? t : (int64_t)seq * a.Lq + t;
-    const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+    const float f = p.sum == 0.0f ? 0.0f : 1.0f / p.sum;
     typedef __bf16 bf4 __attribute__((ext_vector_type(4)));
     *reinterpret_cast<bf4 *>(a.o + ((token * a.Hk + head) * a.G + g) * a.D + e) =
-        bf4{(__bf16)(x.x * f), (__bf16)(x.y * f), (__bf16)(x.z * f), (__bf16)(x.w * f)};
+        bf4{(__bf16)(p.x.x * f), (__bf16)(p.x.y * f), (__bf16)(p.x.z * f), (__bf16)(p.x.w * f)};
 }
 
 // The mask as bits: a wave takes a row's eight blocks of 64 keys.
@@ -466,9 +548,13 @@ int32_t s3d8_cross_attention(const s3d8_cross_attention_args *args, void *stream
     const auto fn = p.waves == 1 ? attn_build<1>(a.D) : attn_build<4>(a.D);
     hipLaunchKernelGGL(fn, dim3((unsigned)(p.pairs * p.tiles * p.splits)), dim3((unsigned)(64 * p.waves)), 0,
                        (hipStream_t)stream, d);
-    if (p.splits > 1)
-        hipLaunchKernelGGL(attn_join_kernel, dim3((unsigned)((p.pairs * p.R * (a.D / 4) + 255) / 256)), dim3(256), 0,
-                           (hipStream_t)stream, d);
+    if (p.splits > 1) {
+        const int64_t rows = p.pairs * p.R;
+        if (p.splits > 4)
+            hipLaunchKernelGGL(attn_join_kernel<8>, dim3((unsigned)rows), dim3(256), 0, (hipStream_t)stream, d);
+        else
+            hipLaunchKernelGGL(attn_join_kernel<1>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, (hipStream_t)stream, d);
+    }
     if (a.xq) s3d8::codes_of_rows(a.o, a.B * a.Lq, a.heads * a.D, a.xq, a.xs, cus, stream);
     return s3d8::launch_status();
 }
