@@ -687,6 +687,8 @@ typedef struct s3d8_sample_args {
     const float *min_p;        /* [M], or NULL: min_p_all                       */
     int32_t *token;            /* out, [M]                                      */
     float *prob;               /* out, [M], or NULL                             */
+    void *workspace;
+    int64_t workspace_bytes;
     int64_t M, V, row;         /* row: elements between rows, at least V        */
     float temperature_all;
     int32_t top_k_all;
@@ -709,8 +711,14 @@ typedef struct s3d8_sample_args {
  * of -infinity (and NaN) throughout has token -1 and prob 0.
  * Temperatures over 2^100 count as 2^100, NaN as 0, top_p and min_p outside [0, 1] (NaN: 0) as
  * its ends; the values for all rows are refused there.  V at most 262144, M at most 524288.
+ *   workspace    s3d8_sample_workspace_bytes(args, CU count) bytes, 16-B aligned.  It holds
+ *                nothing between calls.
  * Errors: INVALID_ARG, SHAPE, ALIGN, DEVICE, HIP. */
 int32_t s3d8_sample(const s3d8_sample_args *args, void *stream);
+
+/* Workspace bytes of s3d8_sample on a device of num_cus compute units, from the sizes, the
+ * type, the values for all rows and which pointers are NULL.  -1 on bad sizes. */
+int64_t s3d8_sample_workspace_bytes(const s3d8_sample_args *args, int32_t num_cus);
 
 /* Matrix-core rate probe: a measurement utility for reading the GEMM's
  * INT8 rate against what the matrix cores sustain, not part of the method.

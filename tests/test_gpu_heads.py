@@ -403,6 +403,54 @@ def test_sample_large_vocabulary(gpu):
     check_sample(gpu, logits, u, 1.0, 200000, 0.9, 0.0)
 
 
+@pytest.mark.parametrize("M,V,dtype", [(3, 128256, F32), (3, 128256, BF16), (40, 20011, F32), (300, 9001, F32)])
+@pytest.mark.parametrize("order", ["none", "rising", "falling", "ends"])
+def test_sample_orders_of_logits(gpu, M, V, dtype, order):
+    """Rows cut into parts or whole, with the largest logits spread, at one end, or one in each segment's last places;
+    limits from one token to more than are listed; a sample of the rows against the plain form, and every row's
+    token with a list of limits against the same limits one by one."""
+    g = gen(8750, M, V)
+    logits = (2 * g.standard_normal((M, V))).astype(np.float32)
+    if order in ("rising", "falling"):
+        logits.sort(1)
+        logits = np.ascontiguousarray(logits[:, ::-1]) if order == "falling" else logits
+    elif order == "ends":
+        logits[:, 2047::2048] += 12
+    u = g.random(M, dtype=np.float32)
+    l, du = dev(logits, gpu, dtype), dev(u, gpu)
+    ks = np.array([1, 7, 50, 200, 1000, 1024, 1025, 4000, 0], np.int32)[np.arange(M) % 9]
+    listed, prob = s3d8.sample(l, du, top_k=dev(ks, gpu), top_p=0.9, min_p=0.001, temperature=0.8)
+    rows = l.float().cpu().numpy()
+    for k in np.unique(ks):
+        at = np.flatnonzero(ks == k)
+        token, share = s3d8.sample(l, du, top_k=int(k), top_p=0.9, min_p=0.001, temperature=0.8)
+        assert torch.equal(token[at], listed[at]) and torch.equal(share[at], prob[at])
+        assert int(token[at[0]]) == ref.sample(rows[at[0]], u[at[0]], 0.8, int(k), 0.9, 0.001)[0]
+
+
+def test_sample_many_equal_logits(gpu):
+    """More equal logits than a list holds, in a part and in the step where top-p ends."""
+    g = gen(8760)
+    V = 60000
+    logits = np.zeros((4, V), np.float32)
+    logits[1, ::7] = 3
+    logits[2, 30000:] = -np.inf
+    logits[3] = np.where(g.random(V) < 0.5, np.float32(1), np.float32(0.999))
+    u = g.random(4, dtype=np.float32)
+    for k, p, mp in [(50, 1.0, 0.0), (0, 0.9, 0.0), (1000, 0.5, 0.0), (0, 0.3, 0.9995), (0, 1.0, 1.0)]:
+        check_sample(gpu, logits, u, 1.0, k, p, mp)
+
+
+def test_sample_more_rows_than_a_set(gpu):
+    g = gen(8770)
+    M, V = 2500, 130
+    logits = (3 * g.standard_normal((M, V))).astype(np.float32)
+    u, T = g.random(M, dtype=np.float32), (0.5 + g.random(M)).astype(np.float32)
+    k, p = g.integers(0, 20, M).astype(np.int32), (0.5 + 0.6 * g.random(M)).astype(np.float32)
+    check_sample(gpu, logits, u, T, k, p, 0.0)
+    check_sample(gpu, logits, u, T, 0, p, 0.0, BF16)
+
+
 def test_sample_follows_the_distribution(gpu):
     """Over evenly spaced random numbers, tokens come up as often as their probability says, to one number each."""
     p = np.array([0.4, 0.3, 0.2, 0.1])

@@ -131,10 +131,23 @@ def sample_args(**kw):
     (dict(temperature_all=-0.5), 1), (dict(temperature_all=float("nan")), 1), (dict(temperature_all=float("inf")), 1),
     (dict(top_k_all=-1), 1), (dict(top_p_all=1.5), 1), (dict(top_p_all=-0.1), 1), (dict(top_p_all=float("nan")), 1),
     (dict(min_p_all=1.5), 1), (dict(min_p_all=float("nan")), 1), (dict(logits=A16 + 2), 3), (dict(logits=A16 + 1, type=1), 3),
-    (dict(u=A16 + 1), 3), (dict(top_k=A16 + 2), 3), (dict(prob=A16 + 2), 3)])
+    (dict(u=A16 + 1), 3), (dict(top_k=A16 + 2), 3), (dict(prob=A16 + 2), 3), (dict(workspace=A16 + 8), 3)])
 def test_sample_refusals(kw, status):
     assert rc("s3d8_sample", sample_args(**kw)) == status
     assert _lib.lib().s3d8_last_error()
+
+
+def test_sample_workspace():
+    def size(cus=256, **kw):
+        a = sample_args(**kw)
+        return _lib.lib().s3d8_sample_workspace_bytes(ctypes.byref(a), cus)
+
+    assert size(V=0) == -1 and size(V=262145) == -1 and size(type=2) == -1 and size(cus=0) == -1
+    assert _lib.lib().s3d8_sample_workspace_bytes(None, 256) == -1
+    assert 0 < size() < size(top_k=A16)                          # rows with and without a top-k
+    assert size(top_k_all=50) != size() and size(top_k_all=100) == size()
+    assert size(M=1024, V=128256) == size(M=100000, V=128256)    # sets of 1024 rows share it
+    assert size(V=128256, top_k_all=2000) < 1024                 # done by rows alone
 
 
 @pytest.mark.parametrize("name", ["s3d8_head_rope", "s3d8_cross_attention", "s3d8_sample"])

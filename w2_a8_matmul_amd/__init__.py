@@ -871,7 +871,19 @@ def head_rope(q, k=None, positions=None, rope=None, *, q_weight=None, k_weight=N
     return q_out if k is None else (q_out, k_out)
 
 
-_attention_bytes = {}
+_workspace_bytes = {}
+
+
+def _workspace(name, dev, key, args) -> int:
+    """Workspace bytes of an entry point on a device, remembered by what they depend on."""
+    key = (name, dev.index, key)
+    nbytes = _workspace_bytes.get(key)
+    if nbytes is None:
+        nbytes = getattr(lib(), name)(args(), _torch().cuda.get_device_properties(dev).multi_processor_count)
+        if len(_workspace_bytes) >= 4096:
+            _workspace_bytes.clear()
+        _workspace_bytes[key] = nbytes
+    return nbytes
 
 
 def cross_attention(q, k, v, *, kv_lens=None, mask=None, scale=None, out: str = "bf16", o=None, xq=None, xs=None):
@@ -933,15 +945,9 @@ def cross_attention(q, k, v, *, kv_lens=None, mask=None, scale=None, out: str = 
     if scale is None:
         scale = D ** -0.5 if D else 1.0
     sizes = (B, Lq, Lk, H, Hk, D, *strides, mask_seq, mask_row, scale, shared)
-    key = (B, Lq, Lk, H, Hk, D, shared, mask is not None, mask_seq != 0, mask_row != 0, dev.index)
-    nbytes = _attention_bytes.get(key)
-    if nbytes is None:
-        cus = torch.cuda.get_device_properties(dev).multi_processor_count
-        nbytes = lib().s3d8_cross_attention_workspace_bytes(
-            _lib.CROSS_ATTENTION_ARGS(0, 0, 0, 0, _ptr(mask), 0, 0, 0, 0, 0, *sizes), cus)
-        if len(_attention_bytes) >= 4096:
-            _attention_bytes.clear()
-        _attention_bytes[key] = nbytes
+    nbytes = _workspace("s3d8_cross_attention_workspace_bytes", dev,
+                        (B, Lq, Lk, H, Hk, D, shared, mask is not None, mask_seq != 0, mask_row != 0),
+                        lambda: _lib.CROSS_ATTENTION_ARGS(0, 0, 0, 0, _ptr(mask), 0, 0, 0, 0, 0, *sizes))
     workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes > 0 else None
     _enqueue("s3d8_cross_attention", dev,
              _lib.CROSS_ATTENTION_ARGS(q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(kv_lens), _ptr(mask), o.data_ptr(),
@@ -986,7 +992,12 @@ def sample(logits, u, *, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, token=N
         prob = torch.empty(M, dtype=torch.float32, device=dev)
     else:
         _dev_check(prob, torch.float32, "prob", dev, numel=M)
+    tail = (M, V, logits.stride(0) if M > 1 else V, *numbers, t)
+    # what the workspace's size depends on
+    nbytes = _workspace("s3d8_sample_workspace_bytes", dev, (M, V, t, numbers[1], pointers[1] != 0, pointers[2] != 0),
+                        lambda: _lib.SAMPLE_ARGS(0, 0, *pointers, 0, 0, 0, 0, *tail))
+    workspace = torch.empty(max(nbytes, 0), dtype=torch.uint8, device=dev)
     _enqueue("s3d8_sample", dev,
-             _lib.SAMPLE_ARGS(logits.data_ptr(), u.data_ptr(), *pointers, token.data_ptr(), prob.data_ptr(), M, V,
-                              logits.stride(0) if M > 1 else V, *numbers, t))
+             _lib.SAMPLE_ARGS(logits.data_ptr(), u.data_ptr(), *pointers, token.data_ptr(), prob.data_ptr(),
+                              workspace.data_ptr(), workspace.numel(), *tail))
     return token, prob

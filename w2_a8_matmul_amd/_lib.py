@@ -68,6 +68,7 @@ SIGNATURES = {
     "s3d8_cross_attention": (_I32, [_P, _P]),
     "s3d8_cross_attention_workspace_bytes": (_I64, [_P, _I32]),
     "s3d8_sample": (_I32, [_P, _P]),
+    "s3d8_sample_workspace_bytes": (_I64, [_P, _I32]),
     "s3d8_splitk_auto": (_I32, [_I64, _I64, _I64, _I32]),
     "s3d8_splitk_workspace_bytes": (_I64, [_I64, _I64, _I64, _I32]),
 }
@@ -112,18 +113,19 @@ class CrossAttentionArgs(ctypes.Structure):
 
 class SampleArgs(ctypes.Structure):
     """s3d8_sample_args of include/s3d8.h."""
-    _fields_ = [(f, _P) for f in ("logits", "u", "temperature", "top_k", "top_p", "min_p", "token", "prob")]
-    _fields_ += [("M", _I64), ("V", _I64), ("row", _I64), ("temperature_all", ctypes.c_float), ("top_k_all", _I32),
+    _fields_ = [(f, _P) for f in ("logits", "u", "temperature", "top_k", "top_p", "min_p", "token", "prob",
+                                   "workspace")]
+    _fields_ += [("workspace_bytes", _I64), ("M", _I64), ("V", _I64), ("row", _I64), ("temperature_all", ctypes.c_float), ("top_k_all", _I32),
                  ("top_p_all", ctypes.c_float), ("min_p_all", ctypes.c_float), ("type", _I32)]
 
 
 # the same structs packed into bytes, as above
 HEAD_ROPE_ARGS = struct.Struct("8Q13q2f4i").pack
 CROSS_ATTENTION_ARGS = struct.Struct("9Q18qfi").pack
-SAMPLE_ARGS = struct.Struct("8Q3qfiffi4x").pack
+SAMPLE_ARGS = struct.Struct("9Q4qfiffi4x").pack
 assert struct.calcsize("8Q13q2f4i") == ctypes.sizeof(HeadRopeArgs)
 assert struct.calcsize("9Q18qfi") == ctypes.sizeof(CrossAttentionArgs)
-assert struct.calcsize("8Q3qfiffi4x") == ctypes.sizeof(SampleArgs)
+assert struct.calcsize("9Q4qfiffi4x") == ctypes.sizeof(SampleArgs)
 
 _lib = None
 

@@ -20,6 +20,13 @@ __device__ __forceinline__ uint16_t f32_to_bf16_rne(float f) {
     return (uint16_t)((u + 0x7FFFu + ((u >> 16) & 1u)) >> 16);
 }
 
+// A pointer to device memory, where the compiler does not see that it is one (members of a struct):
+// its loads and stores are then global ones, which a wait for LDS does not wait for.
+template <class T>
+__device__ __forceinline__ __attribute__((address_space(1))) T *global(T *p) {
+    return (__attribute__((address_space(1))) T *)p;
+}
+
 // Raw buffer loads (buffer_load_dwordx4): an offset at or past the buffer
 // size returns zeros without touching memory, so predicated-off lanes need no
 // branch around the load.  kOOB is past every buffer (sizes are < 2^31).
