@@ -8,6 +8,7 @@
 // takes them from LDS for all of the token's heads.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <type_traits>
@@ -21,8 +22,8 @@ namespace {
 constexpr int kMaxHead = 256;
 constexpr int64_t kMaxTokens = 1 << 19;
 constexpr int64_t kMaxStride = int64_t(1) << 40;
-constexpr int kTokens = 4;      // most tokens a workgroup takes
 constexpr int kThreads = 256;
+constexpr int kHeads = 2;       // heads that a group of lanes takes, where there are many
 
 // Cosine and sine of `angle` radians, each times `factor`, as fp32.  The angle goes to
 // turns and their fraction in 64 bits, from there to the nearest quarter turn and a
@@ -47,49 +48,52 @@ __device__ __forceinline__ float2 turned(double angle, float factor) {
     return make_float2(factor * (q == 1 || q == 2 ? -cq : cq), factor * (q >= 2 ? -sq : sq));
 }
 
-// V values from element `at` of fp32 or bf16 rows, and to them (V = 4: aligned to 4 elements).
+// V values from element `at` of fp32 or bf16 rows, and to them: aligned to V elements or 16 bytes.
+template <class T, int N>
+using Vec = T __attribute__((ext_vector_type(N)));
+
 template <int V, bool kBF>
 __device__ __forceinline__ void load(float (&x)[V], const void *p, int64_t at) {
-    if constexpr (kBF) {
-        const uint16_t *e = static_cast<const uint16_t *>(p) + at;
-        if constexpr (V == 4) {
-            const uint2 u = *reinterpret_cast<const uint2 *>(e);
-            x[0] = __uint_as_float(u.x << 16);
-            x[1] = __uint_as_float(u.x & 0xFFFF0000u);
-            x[2] = __uint_as_float(u.y << 16);
-            x[3] = __uint_as_float(u.y & 0xFFFF0000u);
-        } else {
-            x[0] = bf16_to_f32(*e);
+    if constexpr (kBF && V > 1) {
+        const auto u = *global(reinterpret_cast<const Vec<uint32_t, V / 2> *>(static_cast<const uint16_t *>(p) + at));
+#pragma unroll
+        for (int v = 0; v < V / 2; ++v) {
+            const uint32_t w = u[v];
+            x[2 * v] = __uint_as_float(w << 16);
+            x[2 * v + 1] = __uint_as_float(w & 0xFFFF0000u);
         }
+    } else if constexpr (kBF) {
+        x[0] = bf16_to_f32(global(static_cast<const uint16_t *>(p))[at]);
+    } else if constexpr (V > 1) {
+        const auto u = *global(reinterpret_cast<const Vec<float, V> *>(static_cast<const float *>(p) + at));
+#pragma unroll
+        for (int v = 0; v < V; ++v) x[v] = u[v];
     } else {
-        const float *e = static_cast<const float *>(p) + at;
-        if constexpr (V == 4) {
-            const float4 u = *reinterpret_cast<const float4 *>(e);
-            x[0] = u.x;
-            x[1] = u.y;
-            x[2] = u.z;
-            x[3] = u.w;
-        } else {
-            x[0] = *e;
-        }
+        x[0] = global(static_cast<const float *>(p))[at];
     }
 }
 template <int V>
 __device__ __forceinline__ void store(void *p, int64_t at, const float (&x)[V], bool bf) {
     if (bf) {
-        __bf16 *e = static_cast<__bf16 *>(p) + at;
-        if constexpr (V == 4) {
-            typedef __bf16 bf4 __attribute__((ext_vector_type(4)));
-            *reinterpret_cast<bf4 *>(e) = bf4{(__bf16)x[0], (__bf16)x[1], (__bf16)x[2], (__bf16)x[3]};
+        if constexpr (V > 1) {
+            Vec<__bf16, V> u;
+#pragma unroll
+            for (int v = 0; v < V; ++v) u[v] = (__bf16)x[v];
+            *global(reinterpret_cast<Vec<__bf16, V> *>(static_cast<__bf16 *>(p) + at)) = u;
         } else {
-            *e = (__bf16)x[0];
+            global(static_cast<__bf16 *>(p))[at] = (__bf16)x[0];
+        }
+    } else if constexpr (V > 1) {
+        constexpr int kN = V < 4 ? V : 4;
+#pragma unroll
+        for (int n = 0; n < V; n += kN) {
+            Vec<float, kN> u;
+#pragma unroll
+            for (int v = 0; v < kN; ++v) u[v] = x[n + v];
+            *global(reinterpret_cast<Vec<float, kN> *>(static_cast<float *>(p) + at + n)) = u;
         }
     } else {
-        float *e = static_cast<float *>(p) + at;
-        if constexpr (V == 4)
-            *reinterpret_cast<float4 *>(e) = make_float4(x[0], x[1], x[2], x[3]);
-        else
-            *e = x[0];
+        global(static_cast<float *>(p))[at] = x[0];
     }
 }
 
@@ -114,15 +118,18 @@ __device__ __forceinline__ float group_sum(float v) {
 // part these are the two sides of V pairs (half layout: rot / 2 apart;
 // interleaved: 2 V elements in a row, whose pairs are side by side); past it 2 V
 // elements in a row that stay as they are.
+// A workgroup takes `heads` heads in a row, queries and keys of a token one after the other, of as
+// many tokens as that may be.
 template <int V, int G, int NC, bool kBF>
-__global__ __launch_bounds__(kThreads) void head_rope_kernel(const s3d8_head_rope_args a, int tokens, int heads) {
-    __shared__ float2 turn[kTokens * kMaxHead / 2];
+__global__ __launch_bounds__(kThreads) void head_rope_kernel(const s3d8_head_rope_args a, int heads) {
+    extern __shared__ float2 turn[];
+    __shared__ __attribute__((aligned(16))) float weights[2 * kMaxHead];
     constexpr int kGroups = kThreads / G;
     const int lane = threadIdx.x % G, group = threadIdx.x / G;
     const int D = (int)a.D, half = (int)a.rotary_dim / 2, all = (int)(a.q_heads + a.k_heads);
-    const int64_t token0 = (int64_t)blockIdx.x * tokens;
-    const int head0 = blockIdx.y * heads;
-    const int nt = (int)min((int64_t)tokens, a.M - token0), nh = min(heads, all - head0);
+    const int64_t head0 = (int64_t)blockIdx.x * heads, token0 = head0 / all;
+    const int skip = (int)(head0 - token0 * all);  // heads of its first token that are another's
+    const int items = (int)min((int64_t)heads, a.M * all - head0);
     const bool side_by_side = a.interleaved != 0;
 
     int first[NC], second[NC];
@@ -138,48 +145,56 @@ __global__ __launch_bounds__(kThreads) void head_rope_kernel(const s3d8_head_rop
     struct Head {
         float x[NC][2][V];
     };
-    auto load_head = [&](int item, Head &h) {
-        const int64_t token = token0 + item / nh;
-        const int head = head0 + item % nh;
-        const bool q = head < a.q_heads;
-        const void *p = q ? a.q : a.k;
-        const int64_t at = q ? token * a.q_row + head * a.q_head : token * a.k_row + (head - a.q_heads) * a.k_head;
+    // a head's place: token0 + t, and its number among the token's
+    struct Place {
+        int t, head;
+    };
+    const int more = kGroups / all, rest = kGroups - more * all;
+    auto after = [&](Place p) {
+        p.t += more;
+        p.head += rest;
+        if (p.head >= all) {
+            p.head -= all;
+            ++p.t;
+        }
+        return p;
+    };
+    auto load_head = [&](Place p, Head &h) {
+        const int64_t token = token0 + p.t;
+        const bool q = p.head < a.q_heads;
+        const int64_t at = q ? token * a.q_row + p.head * a.q_head : token * a.k_row + (p.head - a.q_heads) * a.k_head;
 #pragma unroll
         for (int c = 0; c < NC; ++c)
             if (in[c]) {
-                load<V, kBF>(h.x[c][0], p, at + first[c]);
-                load<V, kBF>(h.x[c][1], p, at + second[c]);
+                load<V, kBF>(h.x[c][0], q ? a.q : a.k, at + first[c]);
+                load<V, kBF>(h.x[c][1], q ? a.q : a.k, at + second[c]);
             }
     };
-    const int items = nt * nh;
-    Head next, qw, kw;  // weights: as they lie in a head
-    if (group < items) load_head(group, next);
-    auto load_weight = [&](const float *w, Head &h) {
-#pragma unroll
-        for (int c = 0; c < NC; ++c)
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                h.x[c][0][v] = w && in[c] ? w[first[c] + v] : 0.0f;
-                h.x[c][1][v] = w && in[c] ? w[second[c] + v] : 0.0f;
-            }
-    };
-    load_weight(a.q_weight, qw);
-    load_weight(a.k_weight, kw);
-    if (half) {
-        for (int i = threadIdx.x; i < nt * half; i += kThreads) {
-            const int64_t token = token0 + i / half;
-            const double pos = a.positions_64 ? (double)static_cast<const int64_t *>(a.positions)[token]
-                                              : (double)static_cast<const int32_t *>(a.positions)[token];
-            turn[i] = turned(pos * a.frequencies[i % half], a.factor);
-        }
-        __syncthreads();
+    Head next;
+    Place place{(skip + group) / all, (skip + group) % all};
+    if (group < items) load_head(place, next);
+    // weights and cosines in LDS, once for the workgroup's heads
+    if (a.q_weight)
+        for (int i = threadIdx.x; i < D; i += kThreads) weights[i] = global(a.q_weight)[i];
+    if (a.k_weight)
+        for (int i = threadIdx.x; i < D; i += kThreads) weights[kMaxHead + i] = global(a.k_weight)[i];
+    const int tokens = (skip + items - 1) / all + 1;
+    for (int i = threadIdx.x; i < tokens * half; i += kThreads) {
+        const int64_t token = token0 + i / half;
+        const double pos = a.positions_64 ? (double)global(static_cast<const int64_t *>(a.positions))[token]
+                                          : (double)global(static_cast<const int32_t *>(a.positions))[token];
+        turn[i] = turned(pos * global(a.frequencies)[i % half], a.factor);
     }
+    lds_barrier();
+    const float inv_d = 1.0f / (float)D;
     for (int item = group; item < items; item += kGroups) {
         Head h = next;
-        if (item + kGroups < items) load_head(item + kGroups, next);
-        const int t = item / nh, head = head0 + item % nh;
+        const int t = place.t, head = place.head;
+        place = after(place);
+        if (item + kGroups < items) load_head(place, next);
         const bool q = head < a.q_heads;
         if (q ? a.q_weight : a.k_weight) {
+            const float *w = weights + (q ? 0 : kMaxHead);
             float sum = 0.0f;
 #pragma unroll
             for (int c = 0; c < NC; ++c)
@@ -188,14 +203,16 @@ __global__ __launch_bounds__(kThreads) void head_rope_kernel(const s3d8_head_rop
                     for (int s = 0; s < 2; ++s)
 #pragma unroll
                         for (int v = 0; v < V; ++v) sum = __builtin_fmaf(h.x[c][s][v], h.x[c][s][v], sum);
-            const float r = __builtin_amdgcn_rsqf(group_sum<G>(sum) / (float)D + a.eps);
+            const float r = __builtin_amdgcn_rsqf(__builtin_fmaf(group_sum<G>(sum), inv_d, a.eps));
 #pragma unroll
             for (int c = 0; c < NC; ++c)
                 if (in[c])
 #pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        h.x[c][0][v] = h.x[c][0][v] * r * (q ? qw : kw).x[c][0][v];
-                        h.x[c][1][v] = h.x[c][1][v] * r * (q ? qw : kw).x[c][1][v];
+                    for (int s = 0; s < 2; ++s) {
+                        using W = Vec<float, V < 4 ? V : 4>;
+                        const W *ws = reinterpret_cast<const W *>(w + (s ? second[c] : first[c]));
+#pragma unroll
+                        for (int v = 0; v < V; ++v) h.x[c][s][v] = h.x[c][s][v] * r * ws[v / 4][v % 4];
                     }
         }
         void *p = q ? a.q_out : a.k_out;
@@ -208,8 +225,8 @@ __global__ __launch_bounds__(kThreads) void head_rope_kernel(const s3d8_head_rop
             if (turns[c]) {
                 const float2 *cs = turn + t * half + (lane + c * G) * V;
                 auto rotate = [](float &x, float &y, float2 f) {
-                    const float u = x * f.x - y * f.y;
-                    y = y * f.x + x * f.y;
+                    const float u = __builtin_fmaf(x, f.x, -(y * f.y));
+                    y = __builtin_fmaf(y, f.x, x * f.y);
                     x = u;
                 };
                 if (V > 1 && side_by_side) {
@@ -229,15 +246,22 @@ __global__ __launch_bounds__(kThreads) void head_rope_kernel(const s3d8_head_rop
     }
 }
 
-using HeadRopeFn = void (*)(s3d8_head_rope_args, int, int);
+using HeadRopeFn = void (*)(s3d8_head_rope_args, int);
 
-// Four pairs a lane where the two sides of every four lie in fours of elements
-// (wide loads), else a pair a lane.
+// The build for V pairs a lane, and the lanes of a head.
 template <bool kBF>
-HeadRopeFn head_rope_build(bool fours, int64_t D, int &lanes) {
-    if (!fours) {
+HeadRopeFn head_rope_build(int pairs, int64_t D, int &lanes) {
+    if (pairs == 1) {
         lanes = 64;
         return D <= 128 ? head_rope_kernel<1, 64, 1, kBF> : head_rope_kernel<1, 64, 2, kBF>;
+    }
+    if (pairs == 2) {
+        lanes = D <= 128 ? 32 : 64;
+        return D <= 128 ? head_rope_kernel<2, 32, 1, kBF> : head_rope_kernel<2, 64, 1, kBF>;
+    }
+    if (kBF && pairs == 8) {
+        lanes = D <= 128 ? 8 : 16;
+        return D <= 128 ? head_rope_kernel<8, 8, 1, true> : head_rope_kernel<8, 16, 1, true>;
     }
     lanes = D <= 64 ? 8 : D <= 128 ? 16 : 32;
     return D <= 64    ? head_rope_kernel<4, 8, 1, kBF>
@@ -256,8 +280,10 @@ int check_heads(const void *p, int64_t M, int64_t heads, int64_t D, int64_t row,
     return S3D8_OK;
 }
 
-bool by_fours(const void *p, int64_t row, int64_t head, int32_t type) {
-    return (reinterpret_cast<uintptr_t>(p) & (type == S3D8_ROWS_F32 ? 15 : 7)) == 0 && row % 4 == 0 && head % 4 == 0;
+// Whether heads can be read (or written) V elements at a time.
+bool by(int V, const void *p, int64_t row, int64_t head, int32_t type) {
+    const uintptr_t bytes = std::min(V * (type == S3D8_ROWS_F32 ? 4 : 2), 16);
+    return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0 && row % V == 0 && head % V == 0;
 }
 
 }  // namespace
@@ -333,20 +359,22 @@ int32_t s3d8_head_rope(const s3d8_head_rope_args *args, void *stream) {
     int cus = 0;
     rc = s3d8::check_device(&cus);
     if (rc) return rc;
-    const bool fours = a.D % 8 == 0 && a.rotary_dim % 8 == 0 && by_fours(a.q, a.q_row, a.q_head, a.in_type) &&
-                       by_fours(a.q_out, a.q_out_row, a.q_out_head, a.out_type) &&
-                       (!a.k || (by_fours(a.k, a.k_row, a.k_head, a.in_type) &&
-                                 by_fours(a.k_out, a.k_out_row, a.k_out_head, a.out_type)));
+    // The most pairs a lane that fall together: loads of 16 bytes where they can be.
+    int pairs = a.in_type == S3D8_ROWS_BF16 ? 8 : 4;
+    while (pairs > 1 && !(a.D % (2 * pairs) == 0 && a.rotary_dim % (2 * pairs) == 0 && by(pairs, a.q, a.q_row, a.q_head, a.in_type) &&
+                          by(pairs, a.q_out, a.q_out_row, a.q_out_head, a.out_type) &&
+                          (!a.k || (by(pairs, a.k, a.k_row, a.k_head, a.in_type) &&
+                                    by(pairs, a.k_out, a.k_out_row, a.k_out_head, a.out_type)))))
+        pairs /= 2;
     int lanes = 0;
     const HeadRopeFn fn =
-        a.in_type == S3D8_ROWS_BF16 ? head_rope_build<true>(fours, a.D, lanes) : head_rope_build<false>(fours, a.D, lanes);
-    const int groups = kThreads / lanes, heads = (int)(a.q_heads + a.k_heads);
-    // Many heads: kTokens tokens with all their heads a workgroup, so that an angle is computed once.
-    // Few: a head a group, on as many CUs as there are.
-    const bool many = a.M * heads >= (int64_t)groups * cus * 4;
-    const int tokens = many ? kTokens : 1, per = many ? heads : groups;
-    hipLaunchKernelGGL(fn, dim3((unsigned)((a.M + tokens - 1) / tokens), (unsigned)((heads + per - 1) / per)), dim3(kThreads),
-                       0, (hipStream_t)stream, a, tokens, per);
+        a.in_type == S3D8_ROWS_BF16 ? head_rope_build<true>(pairs, a.D, lanes) : head_rope_build<false>(pairs, a.D, lanes);
+    // A head a group while that does not fill the device eight times over, else kHeads.
+    const int64_t groups = kThreads / lanes, all = a.q_heads + a.k_heads, total = a.M * all;
+    const int64_t heads = groups * (total >= groups * cus * 8 ? kHeads : 1);
+    const int64_t tokens = (heads + all - 2) / all + 1;  // that so many heads in a row can belong to
+    hipLaunchKernelGGL(fn, dim3((unsigned)((total + heads - 1) / heads)), dim3(kThreads),
+                       (size_t)(tokens * (a.rotary_dim / 2) * sizeof(float2)), (hipStream_t)stream, a, (int)heads);
     return s3d8::launch_status();
 }
 
