@@ -5,7 +5,6 @@
 #include <cfloat>
 #include <cmath>
 #include <cstdint>
-#include <cstdlib>
 
 #include "s3d8.h"
 #include "s3d8_device.h"
@@ -19,7 +18,7 @@ typedef short s4 __attribute__((ext_vector_type(4)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef float f16v __attribute__((ext_vector_type(16)));
 
-constexpr int kKeys = 64;       // keys in a block
+constexpr int kKeys = 64;       // keys in a word of the mask
 constexpr int kRows = 32;       // query rows of a wave
 constexpr int kMaxSplits = 64;
 constexpr int kListed = 1024;   // most blocks of a split among which those that a tile sees are listed
@@ -85,15 +84,17 @@ __device__ __forceinline__ void visible_sum(const Attn &a, int64_t q_at, const u
     }
 }
 
-// A workgroup of kR x kK waves: kR over rows, RT tiles of 32 rows each; kK over keys, each on every
-// kK-th block of the split's keys with tiles in LDS of its own, joined at the end.
-template <int NK, int ND, int RT, int kR, int kK>
-__global__ __launch_bounds__(64 * kR * kK, RT == 1 ? 2 : 1) void attn_kernel(const Attn a) {
-    constexpr int Dp = 32 * ND;         // entries of a row in LDS
+// A workgroup of kR x kK waves: kR over rows, 32 each; kK over keys, each on every kK-th block of
+// the split's keys with tiles in LDS of its own, joined at the end.  KB keys in a block.
+template <int NK, int ND, int kR, int kK, int KB>
+__global__ __launch_bounds__(64 * kR * kK, 2) void attn_kernel(const Attn a) {
+    constexpr int Dp = 32 * ND;      // entries of a row in LDS
     constexpr int CPR = Dp / 8;
-    constexpr int kTile = kKeys * CPR;  // chunks
-    static_assert(16 * NK <= Dp && CPR % kR == 0, "");
-    __shared__ __attribute__((aligned(1024))) uint4 tiles[kK][2][2][kTile];
+    constexpr int kTile = KB * CPR;  // chunks
+    constexpr int KT = KB / 32, kScores = KT * NK, kSums = KB / 16 * ND;  // products for a block
+    constexpr int kCopies = kTile / 64 / kR;
+    static_assert(16 * NK <= Dp && kTile % (64 * kR) == 0, "");
+    __shared__ __attribute__((aligned(1024))) uint4 tiles[kK][2][2][kTile];  // keys and values, two blocks of each
     __shared__ uint64_t seen[kListed / 64];
     __shared__ uint16_t list[kListed];
 
@@ -105,35 +106,22 @@ __global__ __launch_bounds__(64 * kR * kK, RT == 1 ? 2 : 1) void attn_kernel(con
 
     int len = a.lens ? global(a.lens)[a.shared ? 0 : seq] : a.Lk;
     len = max(0, min(len, a.Lk));
-    const int blocks = (len + kKeys - 1) / kKeys;
+    const int blocks = (len + KB - 1) / KB;
     const int begin = (int)((int64_t)blocks * split / a.splits), end = (int)((int64_t)blocks * (split + 1) / a.splits);
 
-    // this lane's rows (past the last: the last again, not stored)
-    struct Row {
-        int row, b, i, head;
-    };
-    auto row_of = [&](int rt) {
-        const int row = ((tile * kR + wr) * RT + rt) * kRows + col;
-        const int rr = min(row, a.R - 1), t = rr / a.G;
-        return Row{row, a.shared ? t / a.Lq : seq, a.shared ? t % a.Lq : t, head * a.G + rr % a.G};
-    };
-    bf8 qf[RT][NK];
-    int64_t q_at[RT], word_at[RT];
+    // this lane's row (past the last: the last again, not stored)
+    const int row = (tile * kR + wr) * kRows + col, rr = min(row, a.R - 1), t = rr / a.G;
+    const int b = a.shared ? t / a.Lq : seq, i = a.shared ? t % a.Lq : t, q_head = head * a.G + rr % a.G;
+    const int64_t q_at = b * a.q_seq + i * a.q_row + q_head * a.q_head, word_at = b * a.word_seq + i * a.word_row;
+    bf8 qf[NK];
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-        const Row r = row_of(rt);
-        q_at[rt] = r.b * a.q_seq + r.i * a.q_row + r.head * a.q_head;
-        word_at[rt] = r.b * a.word_seq + r.i * a.word_row;
-#pragma unroll
-        for (int s = 0; s < NK; ++s) {
-            v4u u = {0, 0, 0, 0};
-            if (16 * s + 8 * h < a.D) u = *global(reinterpret_cast<const v4u *>(a.q + q_at[rt] + 16 * s + 8 * h));
-            qf[rt][s] = __builtin_bit_cast(bf8, u);
-        }
+    for (int s = 0; s < NK; ++s) {
+        v4u u = {0, 0, 0, 0};
+        if (16 * s + 8 * h < a.D) u = *global(reinterpret_cast<const v4u *>(a.q + q_at + 16 * s + 8 * h));
+        qf[s] = __builtin_bit_cast(bf8, u);
     }
 
     // the lane's part of each copy of a tile into LDS
-    constexpr int kCopies = CPR / kR;
     uint32_t koff[kCopies], voff[kCopies];
 #pragma unroll
     for (int n = 0; n < kCopies; ++n) {
@@ -145,13 +133,20 @@ __global__ __launch_bounds__(64 * kR * kK, RT == 1 ? 2 : 1) void attn_kernel(con
     const uint16_t *kp = a.k + seq * a.k_seq + head * a.k_head, *vp = a.v + seq * a.v_seq + head * a.v_head;
     // (no block: a buffer of no bytes, zeros)
     auto copy = [&](const uint16_t *p, int64_t stride, int block, const uint4 *to, const uint32_t (&off)[kCopies]) {
-        const int rows = min(kKeys, len - block * kKeys) - 1;
-        const v4i r = rsrc_words(p + (int64_t)block * kKeys * stride, block < end ? (uint32_t)(rows * stride + a.D) * 2 : 0);
+        const int rows = min(KB, len - block * KB) - 1;
+        const v4i r = rsrc_words(p + (int64_t)block * KB * stride, block < end ? (uint32_t)(rows * stride + a.D) * 2 : 0);
 #pragma unroll
         for (int n = 0; n < kCopies; ++n) load_to_lds16_so(S3D8_LDS_OFFSET(to + (wr + n * kR) * 64), off[n], 0, r);
     };
-    auto copy_keys = [&](int block, int buf) { copy(kp, a.k_row, block, tiles[wk][0][buf], koff); };
-    auto copy_values = [&](int block, int buf) { copy(vp, a.v_row, block, tiles[wk][1][buf], voff); };
+    auto copy_keys = [&](int block, int slot) { copy(kp, a.k_row, block, tiles[wk][0][slot], koff); };
+    auto copy_values = [&](int block, int slot) { copy(vp, a.v_row, block, tiles[wk][1][slot], voff); };
+
+    // the mask's bits of a block, of 64 keys a word
+    auto load_word = [&](int64_t at, int block) {
+        const uint64_t w = global(a.words)[at + block * KB / kKeys * a.word_block];
+        return KB == kKeys ? w : w >> (block * KB % kKeys);
+    };
+    constexpr uint64_t kAll = KB == 64 ? ~0ull : (1ull << (KB % 64)) - 1;
 
     // With a mask, the blocks that any row of the tile sees, by the words of the tile's tokens: a lane a
     // block, a wave every kR kK-th token.
@@ -160,16 +155,14 @@ __global__ __launch_bounds__(64 * kR * kK, RT == 1 ? 2 : 1) void attn_kernel(con
     if (sparse) {
         for (int n = threadIdx.x; n < kListed / 64; n += 64 * kR * kK) seen[n] = 0;
         __syncthreads();
-        const int r0 = tile * kR * RT * kRows, t0 = r0 / a.G, t1 = min(r0 + kR * RT * kRows - 1, a.R - 1) / a.G;
+        const int r0 = tile * kR * kRows, t0 = r0 / a.G, t1 = min(r0 + kR * kRows - 1, a.R - 1) / a.G;
         for (int n = 0; n < count; n += 64) {
             const int block = min(begin + n + lane, end - 1);
             uint64_t any = 0;
 #pragma unroll 4
-            for (int t = t0 + wave; t <= t1; t += kR * kK) {
-                const int b = a.shared ? t / a.Lq : seq, i = a.shared ? t % a.Lq : t;
-                any |= global(a.words)[b * a.word_seq + i * a.word_row + block * a.word_block];
-            }
-            const uint64_t bits = __ballot(any != 0 && n + lane < count);
+            for (int t = t0 + wave; t <= t1; t += kR * kK)
+                any |= load_word((a.shared ? t / a.Lq : seq) * a.word_seq + (a.shared ? t % a.Lq : t) * a.word_row, block);
+            const uint64_t bits = __ballot((any & kAll) != 0 && n + lane < count);
             if (lane == 0) atomicOr((unsigned long long *)&seen[n / 64], (unsigned long long)bits);
         }
         __syncthreads();
@@ -191,26 +184,21 @@ __global__ __launch_bounds__(64 * kR * kK, RT == 1 ? 2 : 1) void attn_kernel(con
         return begin + (sparse ? __builtin_amdgcn_readfirstlane((int)list[n]) : n);
     };
 
-    f16v acc[RT][ND];
-    float most[RT], sum[RT];  // of scaled scores, in powers of 2; this lane's part of the sum
+    f16v acc[ND];
+    float most = -FLT_MAX, sum = 0.0f;  // of scaled scores, in powers of 2; this lane's part of the sum
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-        most[rt] = -FLT_MAX;
-        sum[rt] = 0.0f;
+    for (int d = 0; d < ND; ++d)
 #pragma unroll
-        for (int d = 0; d < ND; ++d)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) acc[rt][d][r] = 0.0f;
-    }
+        for (int r = 0; r < 16; ++r) acc[d][r] = 0.0f;
 
     // a score operand (32 keys, 16 entries) and a value operand (32 entries, 16 keys; transposed by the
     // read: entry by lane, four keys in a row) of a block
-    auto key_operand = [&](int buf, int i) {
-        const int n = i / 2, r = i % 2 * 32 + col;
-        return *reinterpret_cast<const bf8 *>(reinterpret_cast<const char *>(tiles[wk][0][buf]) +
+    auto key_operand = [&](int slot, int i) {
+        const int n = i / KT, r = i % KT * 32 + col;
+        return *reinterpret_cast<const bf8 *>(reinterpret_cast<const char *>(tiles[wk][0][slot]) +
                                               (r * CPR + key_place<CPR>(2 * n + h, r)) * 16);
     };
-    auto value_operand = [&](int buf, int i) {
+    auto value_operand = [&](int slot, int i) {
         const int n = i / ND, d = i % ND;
         struct Two {
             s4 x[2];
@@ -220,29 +208,20 @@ __global__ __launch_bounds__(64 * kR * kK, RT == 1 ? 2 : 1) void attn_kernel(con
             const int r = 16 * n + 8 * j + 4 * h + ((lane & 15) >> 2);
             const int c = 4 * d + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
             two.x[j] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (__attribute__((address_space(3))) s4 *)(reinterpret_cast<const char *>(tiles[wk][1][buf]) +
+                (__attribute__((address_space(3))) s4 *)(reinterpret_cast<const char *>(tiles[wk][1][slot]) +
                                                          (r * CPR + value_place<CPR>(c, r)) * 16 + 8 * (lane & 1)));
         }
         return __builtin_bit_cast(bf8, two);
     };
-    struct Words {
-        uint64_t w[RT];
-    };
-    auto load_words = [&](int block) {
-        Words u;
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
-            u.w[rt] = a.words && block < end ? global(a.words)[word_at[rt] + block * a.word_block] : ~0ull;
-        return u;
-    };
+    auto word_of = [&](int block) { return a.words && block < end ? load_word(word_at, block) & kAll : kAll; };
     auto inside = [&](int block) {  // the bits of the keys that exist
-        const int n = block < end ? len - block * kKeys : 0;
-        return n < kKeys ? (1ull << max(n, 0)) - 1 : ~0ull;
+        const int n = block < end ? len - block * KB : 0;
+        return n < KB ? (1ull << max(n, 0)) - 1 : kAll;
     };
-    auto most_of = [&](const f16v(&s)[2]) {
+    auto most_of = [&](const f16v(&s)[KT]) {
         float m = s[0][0];
 #pragma unroll
-        for (int kt = 0; kt < 2; ++kt)
+        for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
             for (int r = 0; r < 16; ++r) m = fmaxf(m, s[kt][r]);
         return m;
@@ -254,108 +233,85 @@ __global__ __launch_bounds__(64 * kR * kK, RT == 1 ? 2 : 1) void attn_kernel(con
     const int steps = (count + kK - 1) / kK;
     if (steps > 0) {
         int block = block_at(0), next = block_at(1);
-        Words words = load_words(block), next_words = load_words(next);
+        uint64_t word = word_of(block), next_word = word_of(next);
         copy_keys(block, 0);
         copy_values(block, 0);
         wait_vmcnt_barrier<0>();
         copy_keys(next, 1);
-        f16v s[RT][2], t[RT][2];
-        float m[RT];
+        f16v s[KT], t[KT];
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
+        for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) s[rt][0][r] = s[rt][1][r] = 0.0f;
+            for (int r = 0; r < 16; ++r) s[kt][r] = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 2 * NK; ++i) {
-            const bf8 kf = key_operand(0, i);
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt)
-                s[rt][i % 2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[rt][i / 2], s[rt][i % 2], 0, 0, 0);
-        }
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) m[rt] = most_of(s[rt]);
+        for (int i = 0; i < kScores; ++i)
+            s[i % KT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(key_operand(0, i), qf[i / KT], s[i % KT], 0, 0, 0);
+        float m = most_of(s);
 
-        auto step = [&](int n, int buf, f16v(&s)[RT][2], f16v(&t)[RT][2]) {
-            const int later = block_at(n + 2);
+        auto step = [&](int n, int slot, f16v(&s)[KT], f16v(&t)[KT]) {
+            const int later = block_at(n + 2), other = slot ^ 1;
             wait_vmcnt_barrier<0>();
-            const uint64_t here = inside(block);
-            const Words now = words;
-            words = next_words;
-            next_words = load_words(later);
-            copy_keys(later, buf);
-            copy_values(next, buf ^ 1);
+            const uint64_t bits = word & inside(block);
+            word = next_word;
+            next_word = word_of(later);
+            copy_keys(later, slot);  // this block's keys were read a step ago, the last one's values too
+            copy_values(next, other);
             block = next;
             next = later;
+            if (__ballot(bits != kAll)) {
+                const uint64_t mine = bits >> (4 * h);
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-                const uint64_t word = now.w[rt] & here;
-                if (__ballot(word != ~0ull)) {
-                    const uint64_t mine = word >> (4 * h);
+                for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-                    for (int kt = 0; kt < 2; ++kt)
+                    for (int r = 0; r < 16; ++r)
+                        s[kt][r] = (uint32_t)(mine >> (32 * kt)) >> (8 * (r / 4) + r % 4) & 1 ? s[kt][r] : -INFINITY;
+                m = most_of(s);
+            }
+            m = halves_max(m) * a.scale;
+            if (__ballot(m > most + kSlack)) {
+                m = fmaxf(most, m);
+                const float f = __builtin_amdgcn_exp2f(most - m);
+                most = m;
+                sum *= f;
 #pragma unroll
-                        for (int r = 0; r < 16; ++r) {
-                            const uint32_t bits = (uint32_t)(mine >> (32 * kt));
-                            s[rt][kt][r] = bits >> (8 * (r / 4) + r % 4) & 1 ? s[rt][kt][r] : -INFINITY;
-                        }
-                    m[rt] = most_of(s[rt]);
-                }
-                m[rt] = halves_max(m[rt]) * a.scale;
-                if (__ballot(m[rt] > most[rt] + kSlack)) {
-                    const float top = fmaxf(most[rt], m[rt]);
-                    const float f = __builtin_amdgcn_exp2f(most[rt] - top);
-                    most[rt] = top;
-                    sum[rt] *= f;
+                for (int d = 0; d < ND; ++d)
 #pragma unroll
-                    for (int d = 0; d < ND; ++d)
-#pragma unroll
-                        for (int r = 0; r < 16; ++r) acc[rt][d][r] *= f;
-                }
+                    for (int r = 0; r < 16; ++r) acc[d][r] *= f;
             }
             constexpr int kAhead = 4;  // operands in flight
             bf8 operand[kAhead];
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i) operand[i] = key_operand(buf ^ 1, i);
-            uint32_t pf[RT][16];
+            for (int i = 0; i < kAhead; ++i) operand[i] = key_operand(other, i);
+            uint32_t pf[KB / 4];
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt)
+            for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) t[rt][0][r] = t[rt][1][r] = 0.0f;
+                for (int r = 0; r < 16; ++r) t[kt][r] = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 2 * NK; ++i) {
+            for (int i = 0; i < kScores; ++i) {
+                __builtin_amdgcn_sched_barrier(0);
+                t[i % KT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(operand[i % kAhead], qf[i / KT], t[i % KT], 0, 0, 0);
+                operand[i % kAhead] = i + kAhead < kScores ? key_operand(other, i + kAhead) : value_operand(slot, i + kAhead - kScores);
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                    __builtin_amdgcn_sched_barrier(0);
-                    t[rt][i % 2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(operand[i % kAhead], qf[rt][i / 2], t[rt][i % 2], 0, 0, 0);
-                    if (rt == RT - 1)
-                        operand[i % kAhead] = i + kAhead < 2 * NK ? key_operand(buf ^ 1, i + kAhead)
-                                                                  : value_operand(buf, i + kAhead - 2 * NK);
+                for (int e = i * (KB / 4) / kScores; e < (i + 1) * (KB / 4) / kScores; ++e) {
+                    bf2 two;
 #pragma unroll
-                    for (int e = i * 16 / (2 * NK); e < (i + 1) * 16 / (2 * NK); ++e) {
-                        bf2 two;
-#pragma unroll
-                        for (int x = 0; x < 2; ++x)
-                            two[x] = (__bf16)__builtin_amdgcn_exp2f(
-                                __builtin_fmaf(s[rt][e / 8][2 * (e % 8) + x], a.scale, -most[rt]));
-                        sum[rt] = __builtin_amdgcn_fdot2_f32_bf16(two, bf2{(__bf16)1.0f, (__bf16)1.0f}, sum[rt], false);
-                        pf[rt][e] = __builtin_bit_cast(uint32_t, two);
-                    }
+                    for (int x = 0; x < 2; ++x)
+                        two[x] = (__bf16)__builtin_amdgcn_exp2f(__builtin_fmaf(s[e / 8][2 * (e % 8) + x], a.scale, -most));
+                    sum = __builtin_amdgcn_fdot2_f32_bf16(two, bf2{(__bf16)1.0f, (__bf16)1.0f}, sum, false);
+                    pf[e] = __builtin_bit_cast(uint32_t, two);
                 }
             }
+            m = t[0][0];
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) m[rt] = t[rt][0][0];
+            for (int i = 0; i < kSums; ++i) {
+                __builtin_amdgcn_sched_barrier(0);
+                const uint4 p = make_uint4(pf[i / ND * 4], pf[i / ND * 4 + 1], pf[i / ND * 4 + 2], pf[i / ND * 4 + 3]);
+                acc[i % ND] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(operand[(i + kScores) % kAhead], __builtin_bit_cast(bf8, p),
+                                                                      acc[i % ND], 0, 0, 0);
+                if (i + kAhead < kSums) operand[(i + kScores) % kAhead] = value_operand(slot, i + kAhead);
 #pragma unroll
-            for (int i = 0; i < 4 * ND; ++i) {
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                    __builtin_amdgcn_sched_barrier(0);
-                    const uint4 p = make_uint4(pf[rt][i / ND * 4], pf[rt][i / ND * 4 + 1], pf[rt][i / ND * 4 + 2], pf[rt][i / ND * 4 + 3]);
-                    acc[rt][i % ND] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(operand[(i + 2 * NK) % kAhead],
-                                                                              __builtin_bit_cast(bf8, p), acc[rt][i % ND], 0, 0, 0);
-                    if (rt == RT - 1 && i + kAhead < 4 * ND) operand[(i + 2 * NK) % kAhead] = value_operand(buf, i + kAhead);
-#pragma unroll
-                    for (int e = i * 32 / (4 * ND); e < (i + 1) * 32 / (4 * ND); ++e) m[rt] = fmaxf(m[rt], t[rt][e / 16][e % 16]);
-                }
+                for (int e = i * (KB / 2) / kSums; e < (i + 1) * (KB / 2) / kSums; ++e) m = fmaxf(m, t[e / 16][e % 16]);
             }
             __builtin_amdgcn_sched_barrier(0);
         };
@@ -370,111 +326,96 @@ __global__ __launch_bounds__(64 * kR * kK, RT == 1 ? 2 : 1) void attn_kernel(con
     if (a.words) {
         // A hidden key has p = 0, but the product with an infinite or NaN value of it is NaN. Rows that
         // are not finite are summed again, one by one, over what they see.
+        float z = 0.0f;
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-            float z = 0.0f;
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) z = __builtin_fmaf(acc[d][r], 0.0f, z);
+        uint64_t bad = __ballot(z != z);
+        bad = (bad | bad >> 32) & 0xFFFFFFFFull;
+        while (bad) {
+            const int lost = __builtin_ctzll(bad);
+            bad &= bad - 1;
+            float e[2] = {0.0f, 0.0f};
+            for (int n = 0, block; (block = block_at(n)) < end; ++n)
+                visible_sum(a, __shfl((long long)q_at, lost), kp, vp, __shfl((long long)word_at, lost), __shfl(most, lost),
+                            block * KB, min((block + 1) * KB, len), e);
 #pragma unroll
             for (int d = 0; d < ND; ++d)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) z = __builtin_fmaf(acc[rt][d][r], 0.0f, z);
-            uint64_t bad = __ballot(z != z);
-            bad = (bad | bad >> 32) & 0xFFFFFFFFull;
-            while (bad) {
-                const int lost = __builtin_ctzll(bad);
-                bad &= bad - 1;
-                float e[2] = {0.0f, 0.0f};
-                for (int n = 0, block; (block = block_at(n)) < end; ++n)
-                    visible_sum(a, __shfl((long long)q_at[rt], lost), kp, vp, __shfl((long long)word_at[rt], lost),
-                                __shfl(most[rt], lost), block * kKeys, min((block + 1) * kKeys, len), e);
-#pragma unroll
-                for (int d = 0; d < ND; ++d)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        const float x = __shfl(e[d / 2], (32 * d + 8 * (r / 4) + 4 * h + r % 4) & 63);
-                        if (col == lost) acc[rt][d][r] = x;
-                    }
-            }
+                for (int r = 0; r < 16; ++r) {
+                    const float x = __shfl(e[d / 2], (32 * d + 8 * (r / 4) + 4 * h + r % 4) & 63);
+                    if (col == lost) acc[d][r] = x;
+                }
         }
     }
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) sum[rt] += __shfl_xor(sum[rt], 32);
+    sum += __shfl_xor(sum, 32);
 
     if constexpr (kK > 1) {
         // the waves over keys joined, one after the other, through the tiles' LDS
-        float4 *room = reinterpret_cast<float4 *>(tiles) + wr * (64 * (4 * ND * RT + 1));
-        static_assert(kR * 64 * (4 * ND * RT + 1) * 16 <= (int)sizeof(tiles), "");
+        float4 *room = reinterpret_cast<float4 *>(tiles) + wr * (64 * (4 * ND + 1));
+        static_assert(kR * 64 * (4 * ND + 1) * 16 <= (int)sizeof(tiles), "");
         for (int g = 1; g < kK; ++g) {
             __syncthreads();
             if (wk == g) {
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt)
+                for (int d = 0; d < ND; ++d)
 #pragma unroll
-                    for (int d = 0; d < ND; ++d)
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            room[((rt * ND + d) * 4 + q) * 64 + lane] = make_float4(
-                                acc[rt][d][4 * q], acc[rt][d][4 * q + 1], acc[rt][d][4 * q + 2], acc[rt][d][4 * q + 3]);
-                room[RT * ND * 4 * 64 + lane] = make_float4(most[0], sum[0], most[RT - 1], sum[RT - 1]);
+                    for (int q = 0; q < 4; ++q)
+                        room[(d * 4 + q) * 64 + lane] =
+                            make_float4(acc[d][4 * q], acc[d][4 * q + 1], acc[d][4 * q + 2], acc[d][4 * q + 3]);
+                room[ND * 4 * 64 + lane] = make_float4(most, sum, 0.0f, 0.0f);
             }
             __syncthreads();
             if (wk == 0) {
-                const float4 ms = room[RT * ND * 4 * 64 + lane];
+                const float4 ms = room[ND * 4 * 64 + lane];
+                const float top = fmaxf(most, ms.x), f = __builtin_amdgcn_exp2f(most - top), o = __builtin_amdgcn_exp2f(ms.x - top);
+                most = top;
+                sum = __builtin_fmaf(f, sum, o * ms.y);
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                    const float om = rt ? ms.z : ms.x, os = rt ? ms.w : ms.y, top = fmaxf(most[rt], om);
-                    const float f = __builtin_amdgcn_exp2f(most[rt] - top), o = __builtin_amdgcn_exp2f(om - top);
-                    most[rt] = top;
-                    sum[rt] = __builtin_fmaf(f, sum[rt], o * os);
+                for (int d = 0; d < ND; ++d)
 #pragma unroll
-                    for (int d = 0; d < ND; ++d)
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const float4 x = room[((rt * ND + d) * 4 + q) * 64 + lane];
-                            acc[rt][d][4 * q] = __builtin_fmaf(f, acc[rt][d][4 * q], o * x.x);
-                            acc[rt][d][4 * q + 1] = __builtin_fmaf(f, acc[rt][d][4 * q + 1], o * x.y);
-                            acc[rt][d][4 * q + 2] = __builtin_fmaf(f, acc[rt][d][4 * q + 2], o * x.z);
-                            acc[rt][d][4 * q + 3] = __builtin_fmaf(f, acc[rt][d][4 * q + 3], o * x.w);
-                        }
-                }
+                    for (int q = 0; q < 4; ++q) {
+                        const float4 x = room[(d * 4 + q) * 64 + lane];
+                        acc[d][4 * q] = __builtin_fmaf(f, acc[d][4 * q], o * x.x);
+                        acc[d][4 * q + 1] = __builtin_fmaf(f, acc[d][4 * q + 1], o * x.y);
+                        acc[d][4 * q + 2] = __builtin_fmaf(f, acc[d][4 * q + 2], o * x.z);
+                        acc[d][4 * q + 3] = __builtin_fmaf(f, acc[d][4 * q + 3], o * x.w);
+                    }
             }
         }
         if (wk) return;
     }
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-        const Row u = row_of(rt);
-        if (u.row >= a.R) continue;
-        if (a.splits > 1) {
-            const int64_t at = ((int64_t)split * a.pairs + pair) * a.R + u.row;
-            const auto p = global(a.part) + at * a.D;
-#pragma unroll
-            for (int d = 0; d < ND; ++d)
-#pragma unroll
-                for (int r = 0; r < 16; r += 4) {
-                    const int e = 32 * d + 2 * r + 4 * h;
-                    const v4f x = {acc[rt][d][r], acc[rt][d][r + 1], acc[rt][d][r + 2], acc[rt][d][r + 3]};
-                    if (e < a.D) *(__attribute__((address_space(1))) v4f *)(p + e) = x;
-                }
-            if (h == 0) {
-                const auto ms = global(a.part) + (int64_t)a.splits * a.pairs * a.R * a.D + 2 * at;
-                ms[0] = most[rt];
-                ms[1] = sum[rt];
-            }
-            continue;
-        }
-        const float f = sum[rt] == 0.0f ? 0.0f : 1.0f / sum[rt];
-        const auto o = global(a.o) + (((int64_t)u.b * a.Lq + u.i) * a.Hk * a.G + u.head) * a.D;
+    if (row >= a.R) return;
+    if (a.splits > 1) {
+        const int64_t at = ((int64_t)split * a.pairs + pair) * a.R + row;
+        const auto p = global(a.part) + at * a.D;
 #pragma unroll
         for (int d = 0; d < ND; ++d)
 #pragma unroll
             for (int r = 0; r < 16; r += 4) {
-                typedef __bf16 bf4 __attribute__((ext_vector_type(4)));
                 const int e = 32 * d + 2 * r + 4 * h;
-                const bf4 x = {(__bf16)(acc[rt][d][r] * f), (__bf16)(acc[rt][d][r + 1] * f), (__bf16)(acc[rt][d][r + 2] * f),
-                               (__bf16)(acc[rt][d][r + 3] * f)};
-                if (e < a.D) *(__attribute__((address_space(1))) bf4 *)(o + e) = x;
+                const v4f x = {acc[d][r], acc[d][r + 1], acc[d][r + 2], acc[d][r + 3]};
+                if (e < a.D) *(__attribute__((address_space(1))) v4f *)(p + e) = x;
             }
+        if (h == 0) {
+            const auto ms = global(a.part) + (int64_t)a.splits * a.pairs * a.R * a.D + 2 * at;
+            ms[0] = most;
+            ms[1] = sum;
+        }
+        return;
     }
+    const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+    const auto o = global(a.o) + (((int64_t)b * a.Lq + i) * a.Hk * a.G + q_head) * a.D;
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int r = 0; r < 16; r += 4) {
+            typedef __bf16 bf4 __attribute__((ext_vector_type(4)));
+            const int e = 32 * d + 2 * r + 4 * h;
+            const bf4 x = {(__bf16)(acc[d][r] * f), (__bf16)(acc[d][r + 1] * f), (__bf16)(acc[d][r + 2] * f), (__bf16)(acc[d][r + 3] * f)};
+            if (e < a.D) *(__attribute__((address_space(1))) bf4 *)(o + e) = x;
+        }
 }
 
 // Partial sums of the splits joined: 4 entries of a row a thread, kLanes threads of a
@@ -597,27 +538,18 @@ __global__ __launch_bounds__(256) void attn_mask_kernel(const uint8_t *mask, int
 
 // --------------------------------------------------------------- host
 
-// Kernels by head size, and by rows: tiles of 32 a wave, waves over rows, waves over keys.
+// Kernels by head size.
 using AttnFn = void (*)(Attn);
-template <int RT, int kR, int kK>
+template <int kR, int kK, int KB>
 AttnFn attn_build(int64_t D) {
-    return D <= 64   ? attn_kernel<4, 2, RT, kR, kK>
-           : D <= 80 ? attn_kernel<5, 3, RT, kR, kK>
-           : D <= 96 ? attn_kernel<6, 3, RT, kR, kK>
-                     : attn_kernel<8, 4, RT, kR, kK>;
+    return D <= 64   ? attn_kernel<4, 2, kR, kK, KB>
+           : D <= 80 ? attn_kernel<5, 3, kR, kK, KB>
+           : D <= 96 ? attn_kernel<6, 3, kR, kK, KB>
+                     : attn_kernel<8, 4, kR, kK, KB>;
 }
-struct Shape {
-    int rows, waves, keys;
-    AttnFn (*build)(int64_t);
-};
-const Shape kShapes[] = {
-    {32, 1, 1, attn_build<1, 1, 1>},
-    {128, 4, 1, attn_build<1, 4, 1>},
-    {128, 8, 2, attn_build<1, 4, 2>},
-};
 
 struct Plan {
-    const Shape *shape;
+    bool wide;  // tiles of 128 rows, else 64
     int64_t pairs, R, tiles, splits;
     int64_t word_seqs, word_rows, blocks;
     int64_t words, part;  // bytes
@@ -640,13 +572,26 @@ Plan plan(const s3d8_cross_attention_args &a, int cus) {
     p.pairs = (a.shared ? 1 : a.B) * a.kv_heads;
     p.R = (a.shared ? a.B * a.Lq : a.Lq) * G;
     p.blocks = (a.Lk + kKeys - 1) / kKeys;
-    const char *force = getenv("ATTN_SHAPE");
-    p.shape = force ? &kShapes[atoi(force)] : p.R <= 96 ? &kShapes[0] : p.pairs * ((p.R + 127) / 128) > cus ? &kShapes[1] : &kShapes[2];
-    p.tiles = (p.R + p.shape->rows - 1) / p.shape->rows;
-    const int64_t groups = p.pairs * p.tiles, most = p.shape->waves == 1 ? p.blocks : p.blocks / (4 * p.shape->keys);
-    const int64_t slots = p.shape->keys == 1 ? 2 * cus : cus;
-    p.splits = std::max<int64_t>(1, std::min<int64_t>({slots / groups, most, kMaxSplits}));
-    if (const char *f = getenv("ATTN_SPLITS")) p.splits = atoi(f);
+    // Tiles of 128 rows where there is more than one for every CU, else of 64 (2048 tokens, 32 heads on 1601
+    // keys: one of 128 for two CUs 31 us, of 64 for each 26; 2048 on 6404: of 128, two a CU, 205).
+    p.wide = p.pairs * ((p.R + 127) / 128) > cus;
+    const int64_t rows = p.wide ? 128 : 64;
+    p.tiles = (p.R + rows - 1) / rows;
+    // The split of the keys with the least estimated time, in us of 128-entry heads: 0.7 for a block of 64
+    // keys where a CU has one workgroup, 1.05 where it has two; the join's launch, and the sums it reads
+    // (one token on 1601 keys: 23.5 us unsplit, 9.0 in 26; 100 on 1601: 24.1, 17.4 in 4, 21.6 in 8).
+    const int64_t groups = p.pairs * p.tiles;
+    double best = 1e30;
+    for (int64_t s = 1; s <= std::min<int64_t>(p.blocks, kMaxSplits); ++s) {
+        const int64_t rounds = (groups * s + 2 * cus - 1) / (2 * cus), blocks = (p.blocks + s - 1) / s;
+        const double t = (double)(rounds * blocks) * (groups * s <= cus ? 0.7 : 1.05) +
+                         (s > 1 ? 3.0 + 2.9e-6 * (double)(p.pairs * p.R * a.D * s) : 0.0);
+        if (t < best) {
+            best = t;
+            p.splits = s;
+        }
+        if (p.wide) break;
+    }
     if (a.mask) {
         p.word_seqs = a.mask_seq ? a.B : 1;
         p.word_rows = a.mask_row ? a.Lq : 1;
@@ -698,7 +643,7 @@ int32_t s3d8_cross_attention(const s3d8_cross_attention_args *args, void *stream
     const Plan p = plan(a, cus);
     if (p.words + p.part > 0 && (!a.workspace || a.workspace_bytes < p.words + p.part))
         return s3d8::fail(S3D8_ERR_INVALID_ARG, "workspace smaller than s3d8_cross_attention_workspace_bytes");
-    if (p.pairs * p.tiles * p.splits * 64 * p.shape->waves >= int64_t(1) << 32)
+    if (p.pairs * p.tiles * p.splits * 256 >= int64_t(1) << 32)
         return s3d8::fail(S3D8_ERR_SHAPE, "more than 2^32 threads are not supported");
     Attn d{};
     d.q = a.q;
@@ -740,8 +685,8 @@ int32_t s3d8_cross_attention(const s3d8_cross_attention_args *args, void *stream
                            dim3(256), 0, (hipStream_t)stream, a.mask, a.mask_seq, a.mask_row, p.word_rows, (int)a.Lk,
                            (int)p.blocks, words);
     }
-    hipLaunchKernelGGL(p.shape->build(a.D), dim3((unsigned)(p.pairs * p.tiles * p.splits)),
-                       dim3((unsigned)(64 * p.shape->waves)), 0, (hipStream_t)stream, d);
+    const AttnFn fn = p.wide ? attn_build<4, 1, 64>(a.D) : attn_build<2, 2, 32>(a.D);
+    hipLaunchKernelGGL(fn, dim3((unsigned)(p.pairs * p.tiles * p.splits)), dim3(256), 0, (hipStream_t)stream, d);
     if (p.splits > 1) {
         const int64_t rows = p.pairs * p.R;
         if (p.splits > 4)
