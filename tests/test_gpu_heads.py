@@ -238,6 +238,24 @@ def test_cross_attention_mask_of_one_row_for_all(gpu, shape):
     assert torch.equal(s3d8.cross_attention(q, k, v, mask=wide[..., 13:]), full)
 
 
+@pytest.mark.parametrize("Lk", [1, 1025, 1153])
+def test_cross_attention_mask_rows_at_every_alignment(gpu, Lk):
+    g = gen(7850, Lk)
+    B, Lq = 2, 5
+    q, k, v = states(g, gpu, B, Lq, Lk, 2, 2, 32)
+    mask = dev(g.random((B, Lq, Lk)) < 0.6, gpu)
+    want = None
+    for at in range(4):
+        for width in (Lk + at, (Lk + 11) // 4 * 4):
+            wide = torch.ones(B, Lq, width, dtype=torch.bool, device=gpu)
+            wide[..., at:at + Lk] = mask
+            o = s3d8.cross_attention(q, k, v, mask=wide[..., at:at + Lk])
+            want = o if want is None else want
+            assert torch.equal(o, want)
+    o, bound = ref.attention(host(q), host(k), host(v), 32 ** -0.5, mask=host(mask) > 0)
+    close(want, o, bound)
+
+
 def test_cross_attention_strides(gpu):
     """Queries as part of a matrix, states with heads outermost or beside each other: the bits of the plain call."""
     g = gen(7900)
@@ -307,7 +325,7 @@ def check_sample(gpu, logits, u, T, k, p, mp, dtype=F32):
         assert abs(float(prob[m]) - share) <= 2.0 ** -24 * share * 1.01 + 2.0 ** -43
 
 
-@pytest.mark.parametrize("V", [1, 2, 7, 64, 1000, 5003, 40001])
+@pytest.mark.parametrize("V", [1, 2, 7, 64, 1000, 3584, 3585, 5003, 40001])
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_sample(gpu, V, dtype):
     g = gen(8300, V)

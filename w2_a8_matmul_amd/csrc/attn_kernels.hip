@@ -476,10 +476,9 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const Attn a) {
         bf4{(__bf16)(p.x.x * f), (__bf16)(p.x.y * f), (__bf16)(p.x.z * f), (__bf16)(p.x.w * f)};
 }
 
-// The mask as bits: a wave takes kMaskKeys keys of a row, four bytes a lane at once where the rows are
-// aligned to that (kWide), else one.
+// The mask as bits: a wave takes kMaskKeys keys of a row, four bytes a lane at once (at any address).
 constexpr int kMaskKeys = 1024;
-template <bool kWide>
+typedef uint32_t u32_any __attribute__((aligned(1)));
 __global__ __launch_bounds__(256) void attn_mask_kernel(const uint8_t *mask, int64_t mask_seq, int64_t mask_row, int64_t rows,
                                                         int Lk, int blocks, uint64_t *words) {
     const int lane = threadIdx.x & 63;
@@ -488,49 +487,34 @@ __global__ __launch_bounds__(256) void attn_mask_kernel(const uint8_t *mask, int
     const auto p = global(mask + seq * mask_seq + row * mask_row);
     const int first = blockIdx.y * kMaskKeys;
     uint64_t mine = 0;  // lane n: word n
-    if constexpr (kWide) {
-        constexpr int kLoads = kMaskKeys / 256;
-        uint32_t u[kLoads];
+    constexpr int kLoads = kMaskKeys / 256;
+    uint32_t u[kLoads];
 #pragma unroll
-        for (int n = 0; n < kLoads; ++n) {
-            const int key = first + 256 * n + 4 * lane;
-            u[n] = 0;
-            if (key + 4 <= Lk)
-                u[n] = *(const __attribute__((address_space(1))) uint32_t *)(p + key);
-            else
-                for (int i = 0; key + i < Lk; ++i) u[n] |= (uint32_t)p[key + i] << (8 * i);
-        }
+    for (int n = 0; n < kLoads; ++n) {
+        const int key = first + 256 * n + 4 * lane;
+        u[n] = 0;
+        if (key + 4 <= Lk)
+            u[n] = *(const __attribute__((address_space(1))) u32_any *)(p + key);
+        else
+            for (int i = 0; key + i < Lk; ++i) u[n] |= (uint32_t)p[key + i] << (8 * i);
+    }
 #pragma unroll
-        for (int n = 0; n < kLoads; ++n) {
-            // a bit for every byte that is not 0, the four in a row; then the words of 16 lanes
-            uint32_t x = ((u[n] & 0x7F7F7F7Fu) + 0x7F7F7F7Fu | u[n]) >> 7 & 0x01010101u;
-            x = (x | x >> 7 | x >> 14 | x >> 21) & 15u;
-            uint64_t w = (uint64_t)x << (4 * (lane & 15));
-            uint32_t lo = (uint32_t)w, hi = (uint32_t)(w >> 32);
-            auto join = [](uint32_t v) {
-                v |= (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false);
-                v |= (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false);
-                v |= (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, false);
-                return v | (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, false);
-            };
-            lo = join(lo);
-            hi = join(hi);
-            w = (uint64_t)(uint32_t)__shfl((int)hi, (lane & 3) * 16) << 32 | (uint32_t)__shfl((int)lo, (lane & 3) * 16);
-            mine = lane / 4 == n ? w : mine;
-        }
-    } else {
-        constexpr int kLoads = kMaskKeys / 64;
-        uint8_t u[kLoads];
-#pragma unroll
-        for (int n = 0; n < kLoads; ++n) {
-            const int key = first + 64 * n + lane;
-            u[n] = key < Lk ? p[key] : 0;
-        }
-#pragma unroll
-        for (int n = 0; n < kLoads; ++n) {
-            const uint64_t w = __ballot(u[n] != 0);
-            mine = lane == n ? w : mine;
-        }
+    for (int n = 0; n < kLoads; ++n) {
+        // a bit for every byte that is not 0, the four in a row; then the words of 16 lanes
+        uint32_t x = ((u[n] & 0x7F7F7F7Fu) + 0x7F7F7F7Fu | u[n]) >> 7 & 0x01010101u;
+        x = (x | x >> 7 | x >> 14 | x >> 21) & 15u;
+        uint64_t w = (uint64_t)x << (4 * (lane & 15));
+        uint32_t lo = (uint32_t)w, hi = (uint32_t)(w >> 32);
+        auto join = [](uint32_t v) {
+            v |= (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false);
+            v |= (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false);
+            v |= (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, false);
+            return v | (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, false);
+        };
+        lo = join(lo);
+        hi = join(hi);
+        w = (uint64_t)(uint32_t)__shfl((int)hi, (lane & 3) * 16) << 32 | (uint32_t)__shfl((int)lo, (lane & 3) * 16);
+        mine = lane / 4 == n ? w : mine;
     }
     const int block = first / kKeys + lane;
     if (lane < kMaskKeys / kKeys && block < blocks) global(words)[(seq * blocks + block) * rows + row] = mine;
@@ -678,8 +662,7 @@ int32_t s3d8_cross_attention(const s3d8_cross_attention_args *args, void *stream
         d.word_seq = a.mask_seq ? p.blocks * p.word_rows : 0;
         d.word_block = p.word_rows;
         d.word_row = a.mask_row ? 1 : 0;
-        const bool wide = aligned(a.mask, 4) && a.mask_seq % 4 == 0 && a.mask_row % 4 == 0;
-        hipLaunchKernelGGL(wide ? attn_mask_kernel<true> : attn_mask_kernel<false>,
+        hipLaunchKernelGGL(attn_mask_kernel,
                            dim3((unsigned)((p.word_rows + 3) / 4), (unsigned)((a.Lk + kMaskKeys - 1) / kMaskKeys),
                                 (unsigned)p.word_seqs),
                            dim3(256), 0, (hipStream_t)stream, a.mask, a.mask_seq, a.mask_row, p.word_rows, (int)a.Lk,
