@@ -711,8 +711,8 @@ typedef struct s3d8_sample_args {
  * of -infinity (and NaN) throughout has token -1 and prob 0.
  * Temperatures over 2^100 count as 2^100, NaN as 0, top_p and min_p outside [0, 1] (NaN: 0) as
  * its ends; the values for all rows are refused there.  V at most 262144, M at most 524288.
- *   workspace    s3d8_sample_workspace_bytes(args, CU count) bytes, 16-B aligned.  It holds
- *                nothing between calls.
+ *   workspace    s3d8_sample_workspace_bytes(args, CU count) bytes, 16-B aligned; NULL where
+ *                that is 0.  It holds nothing between calls.
  * Errors: INVALID_ARG, SHAPE, ALIGN, DEVICE, HIP. */
 int32_t s3d8_sample(const s3d8_sample_args *args, void *stream);
 

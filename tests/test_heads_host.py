@@ -144,8 +144,10 @@ def test_sample_workspace():
 
     assert size(V=0) == -1 and size(V=262145) == -1 and size(type=2) == -1 and size(cus=0) == -1
     assert _lib.lib().s3d8_sample_workspace_bytes(None, 256) == -1
-    assert 0 < size() < size(top_k=A16)                          # rows with and without a top-k
-    assert size(top_k_all=50) != size() and size(top_k_all=100) == size()
+    assert size() == size(top_k=A16) == size(V=3584) == 0        # a row's tokens are all listed
+    V = 128256
+    assert 0 < size(V=V) < size(V=V, top_k=A16)                  # rows with and without a top-k
+    assert size(V=V, top_k_all=50) != size(V=V) and size(V=V, top_k_all=V) == size(V=V)
     assert size(M=1024, V=128256) == size(M=100000, V=128256)    # sets of 1024 rows share it
     assert size(V=128256, top_k_all=2000) < 1024                 # done by rows alone
 

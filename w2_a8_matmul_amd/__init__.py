@@ -996,8 +996,8 @@ def sample(logits, u, *, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, token=N
     # what the workspace's size depends on
     nbytes = _workspace("s3d8_sample_workspace_bytes", dev, (M, V, t, numbers[1], pointers[1] != 0, pointers[2] != 0),
                         lambda: _lib.SAMPLE_ARGS(0, 0, *pointers, 0, 0, 0, 0, *tail))
-    workspace = torch.empty(max(nbytes, 0), dtype=torch.uint8, device=dev)
+    workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes > 0 else None
     _enqueue("s3d8_sample", dev,
              _lib.SAMPLE_ARGS(logits.data_ptr(), u.data_ptr(), *pointers, token.data_ptr(), prob.data_ptr(),
-                              workspace.data_ptr(), workspace.numel(), *tail))
+                              _ptr(workspace), max(nbytes, 0), *tail))
     return token, prob

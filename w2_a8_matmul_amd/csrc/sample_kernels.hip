@@ -30,7 +30,7 @@ constexpr int64_t kMaxRows = 1 << 19;
 constexpr int64_t kRowsAtOnce = 1024;        // rows of one set of launches (bounds the workspace)
 constexpr int kT = 512;                      // threads of every workgroup; vectors of a segment
 constexpr int kMaxTopK = 1024;
-constexpr int kListed = 4096;                // candidates of a part, tokens of a step
+constexpr int kListed = 3584;                // candidates of a part, tokens of a step, a vocabulary that is listed whole
 constexpr int kRound = 4;                    // segments that are read at once
 constexpr int kDigit = 11, kBins = 1 << kDigit;
 constexpr int kSteps = 64;                   // bins per unit of (largest logit - logit) / temperature
@@ -59,6 +59,7 @@ __device__ __forceinline__ uint32_t place_index(uint64_t p) { return (uint32_t)p
 // What a workgroup reads.  Arrays of the workspace by row and part.
 struct Job {
     s3d8_sample_args a;
+    bool direct;          // the row alone, its tokens all listed
     int parts, cuts;      // parts of a row; the same of the launches that take every weight
     int segments;         // room for segment sums
     uint64_t *first;      // [M][parts] the first place of each part
@@ -225,10 +226,12 @@ struct Sums {
     int listed, matching;
 };
 struct Shared : Sums {
-    uint64_t bins[kBins];
+    union {
+        uint64_t bins[kBins];
+        ulonglong2 few[kFewTokens];  // place and weight
+    };
     uint64_t list[kListed];
-    uint64_t weights[kMaxTopK];
-    ulonglong2 few[kFewTokens];  // place and weight
+    uint64_t weights[kListed];
 };
 
 // Sum of the workgroup's values before this thread's, and of all.
@@ -402,12 +405,8 @@ __device__ __forceinline__ uint64_t sum_of(uint64_t v, Sums &sh) {
 
 // --------------------------------------------------------------- part
 
-// How many of the workgroup's values are at least t (one barrier; `turn` alternates).
-template <int N>
-__device__ __forceinline__ int count_from(const uint32_t (&v)[N], uint32_t t, Sums &sh, int turn) {
-    int n = 0;
-#pragma unroll
-    for (int j = 0; j < N; ++j) n += __builtin_popcountll(__ballot(v[j] >= t));
+// The sum of the waves' counts (one barrier; `turn` alternates).
+__device__ __forceinline__ int block_count(int n, Sums &sh, int turn) {
     if ((threadIdx.x & 63) == 0) sh.waves[turn & 1][threadIdx.x >> 6] = n;
     lds_barrier();
     n = 0;
@@ -415,7 +414,14 @@ __device__ __forceinline__ int count_from(const uint32_t (&v)[N], uint32_t t, Su
     for (int w = 0; w < kT / 64; ++w) n += (int)sh.waves[turn & 1][w];
     return n;
 }
-
+// How many of the workgroup's values are at least t.
+template <int N>
+__device__ __forceinline__ int count_from(const uint32_t (&v)[N], uint32_t t, Sums &sh, int turn) {
+    int n = 0;
+#pragma unroll
+    for (int j = 0; j < N; ++j) n += __builtin_popcountll(__ballot(v[j] >= t));
+    return block_count(n, sh, turn);
+}
 // The largest t, bit by bit but for the last `low`, that at least k of the workgroup's values reach.
 template <int N>
 __device__ __forceinline__ uint32_t block_kth(const uint32_t (&v)[N], int k, int low, Sums &sh) {
@@ -553,7 +559,19 @@ __global__ __launch_bounds__(kT) void sample_part_kernel(const Job j) {
             }
 #pragma unroll
             for (int n = 0; n < kRound; ++n) w[kHeld + n] = order_key(most[n]);
-            const uint32_t t = block_kth(w, lim.k, 0, sh);
+            uint32_t t = block_kth(w, lim.k, 0, sh);
+            if (t <= kNothing) {  // fewer vectors than k: the k-th largest of the new tokens themselves
+                t = 0;
+                for (int bit = 31; bit >= 0; --bit) {
+                    const float f = key_value(t | 1u << bit);
+                    int n = 0;
+#pragma unroll
+                    for (int i = 0; i < kRound; ++i)
+#pragma unroll
+                        for (int v = 0; v < kV; ++v) n += __builtin_popcountll(__ballot(u[i][v] >= f));
+                    if (block_count(n, sh, bit) >= lim.k) t |= 1u << bit;
+                }
+            }
             from = t > kNothing ? fmaxf(from, key_value(t)) : from;
             if (threadIdx.x == 0) sh.listed = 0;
             lds_barrier();
@@ -746,19 +764,38 @@ __global__ __launch_bounds__(kT) void sample_row_kernel(const Job j) {
     const s3d8_sample_args &a = j.a;
     const int64_t r = blockIdx.x;
     const R row(a, r);
-    const Limits lim(a, r);
+    Limits lim(a, r);
     // (asked for before any of it is used)
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, tops = j.parts * j.groups;
     const int64_t at0 = r * j.parts;
     uint32_t count = 0, some[256 / 64] = {};
-    if (j.counts && lim.listed()) {
+    if (!j.direct && j.counts && lim.listed()) {
         if (lane < j.parts) count = global(j.counts)[at0 + lane];
         if (wave == 0 && tops <= 256)
 #pragma unroll
             for (int i = 0; i < 256 / 64; ++i)
                 if (i * 64 + lane < tops) some[i] = global(j.tops)[at0 * j.groups + i * 64 + lane];
     }
-    const uint64_t first = first_place(j, r);
+    uint64_t first;
+    int n = 0, bits = 0;  // tokens in sh.list, bits in which their places differ
+    if (j.direct) {  // all tokens of the row but those of -infinity
+        if (threadIdx.x == 0) sh.listed = 0;
+        lds_barrier();
+        first = ~0ull;
+        row.each([&](int i, float l) {
+            const uint32_t key = order_key(l);
+            if (key <= kNothing) return;
+            const uint64_t x = place(key, i);
+            first = min(first, x);
+            sh.list[atomicAdd(&sh.listed, 1)] = x;
+        });
+        first = smallest(first, sh);
+        n = sh.listed;
+        bits = kOrderBits;
+        if (lim.k == 0) lim.k = kListed;
+    } else {
+        first = first_place(j, r);
+    }
     if (first == ~0ull || lim.greedy) {
         if (threadIdx.x == 0) {
             global(a.token)[r] = first == ~0ull ? -1 : (int32_t)place_index(first);
@@ -776,12 +813,13 @@ __global__ __launch_bounds__(kT) void sample_row_kernel(const Job j) {
     auto by_place = [](uint64_t p) { return p; };
     uint64_t total;
 
-    if (lim.listed()) {
+    bool fits = j.direct;
+    if (!j.direct && lim.listed()) {
         // `from`: the k-th largest of the parts' tops, as k tokens are at least that (0: too few
         // tops). What the parts listed from there on: each wave takes some parts' lists, two
         // loads a lane of four lists on their way at once.
         uint32_t from = 0;
-        bool fits = !__ballot(count == kTooMany);
+        fits = !__ballot(count == kTooMany);
         constexpr int kWaves = kT / 64;
         if (tops > 256) {
             uint32_t w[kTops / kT];
@@ -799,7 +837,6 @@ __global__ __launch_bounds__(kT) void sample_row_kernel(const Job j) {
         }
         if (threadIdx.x == 0) sh.listed = 0;
         lds_barrier();
-        int bits = 0;  // those in which the places differ
         if (fits) {
             // the lists in pieces of 64 tokens, piece by piece of each part in turn: four of a wave's are
             // on their way at once
@@ -828,7 +865,7 @@ __global__ __launch_bounds__(kT) void sample_row_kernel(const Job j) {
             }
         }
         lds_barrier();
-        int n = sh.listed;
+        n = sh.listed;
         if (fits && n > kListed) {  // the k-th place by the lists themselves
             auto go = [&](auto f) {
                 for (int p = wave; p < j.parts; p += kWaves)
@@ -845,91 +882,92 @@ __global__ __launch_bounds__(kT) void sample_row_kernel(const Job j) {
             lds_barrier();
             n = sh.listed;
         }
-        if (fits && n <= kFewTokens) {
-            // few: each thread compares its token with all of them, by place for what is kept, then by index
-            uint64_t p = ~0ull, w = 0;
-            if ((int)threadIdx.x < n) {
-                p = sh.list[threadIdx.x];
-                w = weight(place_key(p));
+    }
+    if (fits && n <= kFewTokens) {
+        // few: each thread compares its token with all of them, by place for what is kept, then by index
+        uint64_t p = ~0ull, w = 0;
+        if ((int)threadIdx.x < n) {
+            p = sh.list[threadIdx.x];
+            w = weight(place_key(p));
+        }
+        int at = (int)threadIdx.x < n ? (int)threadIdx.x : -1;
+        for (int pass = 0; pass < 2; ++pass) {
+            if (at >= 0) sh.few[at] = make_ulonglong2(p, w);
+            if (threadIdx.x < kBatch - 1 && n + threadIdx.x < kFewTokens) sh.few[n + threadIdx.x] = make_ulonglong2(~0ull, 0);
+            if (pass) total = sum_of(w, sh);
+            lds_barrier();
+            uint64_t before = 0;
+            const int rank = at >= 0 ? preceding(sh, n, p, before) : kListed;
+            if (pass) {
+                const uint64_t left = target(u, total);
+                if (at >= 0 && before < left && left <= before + w) answer((uint32_t)p, w, total);
+                return;
             }
-            int at = (int)threadIdx.x < n ? (int)threadIdx.x : -1;
-            for (int pass = 0; pass < 2; ++pass) {
-                if (at >= 0) sh.few[at] = make_ulonglong2(p, w);
-                if (threadIdx.x < kBatch - 1 && n + threadIdx.x < kFewTokens) sh.few[n + threadIdx.x] = make_ulonglong2(~0ull, 0);
-                if (pass) total = sum_of(w, sh);
-                lds_barrier();
-                uint64_t before = 0;
-                const int rank = at >= 0 ? preceding(sh, n, p, before) : kListed;
-                if (pass) {
-                    const uint64_t left = target(u, total);
-                    if (at >= 0 && before < left && left <= before + w) answer((uint32_t)p, w, total);
+            bool kept = rank < lim.k;
+            if (lim.top_p < 1.0f) {
+                const uint64_t sum = sum_of(kept ? w : 0, sh);
+                kept = kept && before < lim.end(sum);
+            }
+            if (!kept || w < least) w = 0;
+            p = place_index(p);
+            if (threadIdx.x == 0) sh.listed = 0;
+            lds_barrier();
+            at = w ? atomicAdd(&sh.listed, 1) : -1;
+            lds_barrier();
+            n = sh.listed;
+        }
+    }
+    if (fits) {
+        bits = kOrderBits - (int)smallest((uint64_t)(kOrderBits - bits), sh);
+        // top-k, top-p, the token: one piece of code, so that it is fetched once
+        uint64_t end = ~0ull;
+        for (int stage = 0; stage < 3; ++stage) {
+            if (stage == 0 ? n <= lim.k : stage == 1 && !(lim.top_p < 1.0f)) {
+                if (stage == 0) lds_barrier();
+            } else {
+                const uint64_t found = reach<false, true>(
+                    sh, stage == 2 ? kIndexBits : bits, stage == 2 ? 0 : first >> bits,
+                    [&](auto f) {
+                        for (int i = threadIdx.x; i < n; i += kT) f(i);
+                    },
+                    [&](int i) { return stage == 2 ? place_index(sh.list[i]) : sh.list[i]; },
+                    [&](int i) -> uint64_t {
+                        if (stage == 0) return 1;
+                        const uint64_t w = sh.weights[i];
+                        return stage == 1 || (sh.list[i] <= end && w >= least) ? w : 0;
+                    },
+                    [&](uint64_t s) { return stage == 0 ? (uint64_t)lim.k : stage == 1 ? lim.end(s) : target(u, s); },
+                    total);
+                if (stage == 2) {
+                    for (int i = threadIdx.x; i < n; i += kT)
+                        if (place_index(sh.list[i]) == found) answer((uint32_t)found, sh.weights[i], total);
                     return;
                 }
-                bool kept = rank < lim.k;
-                if (lim.top_p < 1.0f) {
-                    const uint64_t sum = sum_of(kept ? w : 0, sh);
-                    kept = kept && before < lim.end(sum);
+                end = found;
+            }
+            if (stage == 0) {  // those kept, with their weights
+                uint64_t held[kListed / kT];
+#pragma unroll
+                for (int i = 0; i < kListed / kT; ++i) {
+                    const int at = i * kT + threadIdx.x;
+                    held[i] = at < n ? sh.list[at] : ~0ull;
                 }
-                if (!kept || w < least) w = 0;
-                p = place_index(p);
                 if (threadIdx.x == 0) sh.listed = 0;
                 lds_barrier();
-                at = w ? atomicAdd(&sh.listed, 1) : -1;
+#pragma unroll
+                for (int i = 0; i < kListed / kT; ++i)
+                    if (held[i] != ~0ull && held[i] <= end) {
+                        const int at = atomicAdd(&sh.listed, 1);
+                        sh.list[at] = held[i];
+                        sh.weights[at] = weight(place_key(held[i]));
+                    }
                 lds_barrier();
                 n = sh.listed;
+                end = ~0ull;
             }
         }
-        if (fits) {
-            bits = kOrderBits - (int)smallest((uint64_t)(kOrderBits - bits), sh);
-            // top-k, top-p, the token: one piece of code, so that it is fetched once
-            uint64_t end = ~0ull;
-            for (int stage = 0; stage < 3; ++stage) {
-                if (stage == 0 ? n <= lim.k : stage == 1 && !(lim.top_p < 1.0f)) {
-                    if (stage == 0) lds_barrier();
-                } else {
-                    const uint64_t found = reach<false, true>(
-                        sh, stage == 2 ? kIndexBits : bits, stage == 2 ? 0 : first >> bits,
-                        [&](auto f) {
-                            for (int i = threadIdx.x; i < n; i += kT) f(i);
-                        },
-                        [&](int i) { return stage == 2 ? place_index(sh.list[i]) : sh.list[i]; },
-                        [&](int i) -> uint64_t {
-                            if (stage == 0) return 1;
-                            const uint64_t w = sh.weights[i];
-                            return stage == 1 || (sh.list[i] <= end && w >= least) ? w : 0;
-                        },
-                        [&](uint64_t s) { return stage == 0 ? (uint64_t)lim.k : stage == 1 ? lim.end(s) : target(u, s); },
-                        total);
-                    if (stage == 2) {
-                        for (int i = threadIdx.x; i < n; i += kT)
-                            if (place_index(sh.list[i]) == found) answer((uint32_t)found, sh.weights[i], total);
-                        return;
-                    }
-                    end = found;
-                }
-                if (stage == 0) {  // those kept, with their weights
-                    uint64_t held[kListed / kT];
-#pragma unroll
-                    for (int i = 0; i < kListed / kT; ++i) {
-                        const int at = i * kT + threadIdx.x;
-                        held[i] = at < n ? sh.list[at] : ~0ull;
-                    }
-                    if (threadIdx.x == 0) sh.listed = 0;
-                    lds_barrier();
-#pragma unroll
-                    for (int i = 0; i < kListed / kT; ++i)
-                        if (held[i] != ~0ull && held[i] <= end) {
-                            const int at = atomicAdd(&sh.listed, 1);
-                            sh.list[at] = held[i];
-                            sh.weights[at] = weight(place_key(held[i]));
-                        }
-                    lds_barrier();
-                    n = sh.listed;
-                    end = ~0ull;
-                }
-            }
-        }
-    } else if (lim.binned()) {
+    }
+    if (!j.direct && lim.binned()) {
         const int last = (int)global(j.ends)[2 * r];
         const uint32_t n = last < kBins ? j.steps[r] : 0;
         if (n <= kListed) {
@@ -1027,7 +1065,7 @@ __global__ __launch_bounds__(kT) void sample_row_kernel(const Job j) {
 
 struct Plan {
     int64_t rows, parts, cuts, segments, groups;
-    bool lists, bins, top_p;
+    bool direct, lists, bins, top_p;
     int64_t first, counts, lists_at, tops, bins_at, step, sums, ends, steps, bytes;
 };
 
@@ -1037,11 +1075,12 @@ Plan plan(const s3d8_sample_args &a, int cus) {
     p.rows = std::min(a.M, kRowsAtOnce);
     const int64_t vectors = a.V / (a.type == S3D8_ROWS_BF16 ? 8 : 4) + 2;
     p.segments = (vectors + kT - 1) / kT;
+    const bool one_k = !a.top_k, k_on = a.top_k_all > 0 && a.top_k_all < a.V;
     // (candidates are the fewer the larger a part is beside k: 1000 of 128256 tokens 101 us with 32 parts)
-    const int64_t most = a.top_k || a.top_k_all <= 0 ? kMaxParts : std::max<int64_t>(4, a.V / (16 * (int64_t)a.top_k_all));
+    const int64_t most = !one_k || !k_on ? kMaxParts : std::max<int64_t>(4, a.V / (16 * (int64_t)a.top_k_all));
     p.parts = std::max<int64_t>(1, std::min<int64_t>({(p.segments + kRound - 1) / kRound, 4 * cus / p.rows, kMaxParts, most}));
     p.cuts = std::max<int64_t>(1, std::min<int64_t>(p.segments, 4 * cus / p.rows));
-    const bool one_k = !a.top_k, k_on = a.top_k_all > 0 && a.top_k_all < a.V;
+    p.direct = a.V <= kListed;
     p.lists = !one_k || (k_on && a.top_k_all <= kMaxTopK);
     p.bins = !one_k || !k_on;
     // four times as many tops as tokens that are kept, so that hardly more than those are at least the k-th of them
@@ -1049,6 +1088,7 @@ Plan plan(const s3d8_sample_args &a, int cus) {
     static_assert(kMaxParts * 8 <= 256, "");
     for (p.groups = 256; p.groups > 8 && p.groups * p.parts > tops;) p.groups /= 2;
     p.top_p = a.top_p || a.top_p_all < 1.0f;
+    if (p.direct) return p;
     int64_t at = 0;
     auto room = [&](int64_t bytes) {
         const int64_t here = at;
@@ -1079,9 +1119,9 @@ int check_sizes(const s3d8_sample_args &a) {
 template <bool kBF>
 void launch(const Job &j, const Plan &p, int64_t rows, hipStream_t stream) {
     const dim3 each((unsigned)(rows * p.parts)), cut((unsigned)(rows * p.cuts)), threads(kT);
-    hipLaunchKernelGGL(sample_part_kernel<kBF>, each, threads, 0, stream, j);
-    if (p.bins && p.top_p) hipLaunchKernelGGL(sample_bins_kernel<kBF>, cut, threads, 0, stream, j);
-    if (p.bins) hipLaunchKernelGGL(sample_step_kernel<kBF>, cut, threads, 0, stream, j);
+    if (!p.direct) hipLaunchKernelGGL(sample_part_kernel<kBF>, each, threads, 0, stream, j);
+    if (!p.direct && p.bins && p.top_p) hipLaunchKernelGGL(sample_bins_kernel<kBF>, cut, threads, 0, stream, j);
+    if (!p.direct && p.bins) hipLaunchKernelGGL(sample_step_kernel<kBF>, cut, threads, 0, stream, j);
     hipLaunchKernelGGL(sample_row_kernel<kBF>, dim3((unsigned)rows), threads, 0, stream, j);
 }
 
@@ -1117,7 +1157,7 @@ int32_t s3d8_sample(const s3d8_sample_args *args, void *stream) {
     rc = s3d8::check_device(&cus);
     if (rc) return rc;
     const Plan p = plan(a, cus);
-    if (!a.workspace || a.workspace_bytes < p.bytes)
+    if (p.bytes > 0 && (!a.workspace || a.workspace_bytes < p.bytes))
         return s3d8::fail(S3D8_ERR_INVALID_ARG, "workspace smaller than s3d8_sample_workspace_bytes");
     char *const ws = static_cast<char *>(a.workspace);
     for (int64_t r = 0; r < a.M; r += p.rows) {
@@ -1131,6 +1171,7 @@ int32_t s3d8_sample(const s3d8_sample_args *args, void *stream) {
         if (a.min_p) j.a.min_p += r;
         j.a.token += r;
         if (a.prob) j.a.prob += r;
+        j.direct = p.direct;
         j.parts = (int)p.parts;
         j.cuts = (int)p.cuts;
         j.segments = (int)p.segments;
