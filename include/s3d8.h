@@ -626,10 +626,10 @@ typedef struct s3d8_head_rope_args {
  * The angle and its reduction are in 64 bits, every other step in fp32.  D even, at
  * most 256; rotary_dim even, at most D, 0 for none (a weight is then needed); strides at
  * least a head's size (of what has more than one row or head); pointers aligned to an
- * element.  Where D, rotary_dim and strides are multiples of 8, 8 and 4 and pointers
- * aligned to 4 elements, four pairs are loaded at a time, else one.  At most 524288
- * tokens and 4096 heads of each kind; squares summed within fp32's range; outputs other
- * than the input itself must not overlap inputs.
+ * element.  A lane loads n pairs at a time, of 8 (bf16 input only), 4, 2 and 1 the most for
+ * which D and rotary_dim are multiples of 2 n and strides and pointers of n elements.  At
+ * most 524288 tokens, 4096 heads of each kind and 2^26 heads of all tokens; squares summed
+ * within fp32's range; outputs other than the input itself must not overlap inputs.
  * Errors: INVALID_ARG, SHAPE, ALIGN, DEVICE, HIP. */
 int32_t s3d8_head_rope(const s3d8_head_rope_args *args, void *stream);
 
@@ -656,8 +656,8 @@ typedef struct s3d8_cross_attention_args {
  * which the first kv_lens[b] exist.  Query head h reads key head h / (heads / kv_heads):
  *   o = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale * q . k_j), over the keys j < kv_lens[b]
  *   that the mask lets the query see; 0 where there are none.
- * Products, sums and exponentials in fp32 (a running maximum taken off), p rounded to
- * bf16 where it is multiplied with v; o rounded to bf16.  With xq and xs also the codes that
+ * Products, sums and exponentials in fp32 (a running maximum taken off); p is rounded to bf16,
+ * in the sum as where it is multiplied with v; o rounded to bf16.  With xq and xs also the codes that
  * s3d8_quant_act makes of the rows of o, for the output projection.
  *   D            a multiple of 16, at most 128; heads a multiple of kv_heads.
  *   strides      multiples of 8, k_row and v_row at least D and below 2^23 where Lk > 1;

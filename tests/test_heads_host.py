@@ -71,7 +71,7 @@ def rope_args(**kw):
     (dict(q=None), 1), (dict(q_out=None), 1), (dict(k=None), 1), (dict(k_out=None), 1), (dict(k_heads=0), 1),
     (dict(k=None, k_out=None, k_heads=0, k_weight=A16), 1), (dict(M=0), 1), (dict(D=0), 1), (dict(q_heads=-1), 1),
     (dict(rotary_dim=-2), 1), (dict(D=63), 2), (dict(D=258, rotary_dim=64), 2), (dict(rotary_dim=66), 2), (dict(rotary_dim=31), 2),
-    (dict(M=(1 << 19) + 1), 2), (dict(q_heads=4097), 2), (dict(positions=None), 1), (dict(frequencies=None), 1),
+    (dict(M=(1 << 19) + 1), 2), (dict(q_heads=4097), 2), (dict(M=1 << 19, q_heads=127), 2), (dict(positions=None), 1), (dict(frequencies=None), 1),
     (dict(rotary_dim=0), 1), (dict(in_type=2), 1), (dict(out_type=3), 1), (dict(eps=0.0), 1), (dict(eps=float("nan")), 1),
     (dict(factor=float("inf")), 1), (dict(factor=float("nan")), 1), (dict(q_row=63), 1), (dict(k_out_head=32), 1),
     (dict(k_row=-128), 1), (dict(q_row=1 << 41), 1), (dict(q=A16 + 1), 3), (dict(q_out=A16 + 2, out_type=0), 3),

@@ -21,6 +21,7 @@ namespace {
 
 constexpr int kMaxHead = 256;
 constexpr int64_t kMaxTokens = 1 << 19;
+constexpr int64_t kMaxHeads = 1 << 26;     // of all tokens
 constexpr int64_t kMaxStride = int64_t(1) << 40;
 constexpr int kThreads = 256;
 constexpr int kHeads = 2;       // heads that a group of lanes takes, where there are many
@@ -340,6 +341,8 @@ int32_t s3d8_head_rope(const s3d8_head_rope_args *args, void *stream) {
         return s3d8::fail(S3D8_ERR_SHAPE, "rotary_dim must be even and at most the head's size");
     if (a.M > kMaxTokens || a.q_heads > 4096 || a.k_heads > 4096)
         return s3d8::fail(S3D8_ERR_SHAPE, "more than 524288 tokens or 4096 heads are not supported");
+    // (a workgroup takes 8 heads or more where there are many: 2^31 threads at most)
+    if (a.M * (a.q_heads + a.k_heads) > kMaxHeads) return s3d8::fail(S3D8_ERR_SHAPE, "more than 2^26 heads are not supported");
     if (a.rotary_dim && (!a.positions || !a.frequencies))
         return s3d8::fail(S3D8_ERR_INVALID_ARG, "rotary_dim needs positions and frequencies");
     if (!a.rotary_dim && !a.q_weight && !a.k_weight)
