@@ -1,4 +1,26 @@
-// Attention of query tokens to an encoder's states, for gfx950.
+// Attention of query tokens to an encoder's states, for gfx950: with p_j = exp(scale q.k_j)
+//   o = sum_j p_j v_j / sum_j p_j
+// in one pass over the keys, with a running maximum taken off the scores.
+//
+// The query tokens and heads that read one key head are the rows of one problem, so each key
+// and value is fetched once for all of them, and an 8-fold group decodes at the cost of one head.
+// Scores are computed transposed, S = K Q^T, in 32 x 32 x 16 products: a row's scores are
+// then in the registers of two lanes, its maximum and sum need one step between lanes, and
+// the rounded p are the operand of O^T = V^T P^T as they stand; LDS transposes the values as it reads
+// them.  Keys and values go from memory to LDS without registers, two blocks of each in
+// turn.  p is rounded to bf16, the type of the product with v; the sum takes the rounded p, so
+// that the weights of the values add up to 1.  Scores, maximum, sums and o are fp32.
+//
+//   mask  the mask as bits, 64 keys a word (6.9 us for 2048 x 6404 bytes)
+//   attn  tiles of rows, each over all keys or a part of them
+//   join  the parts' sums
+//
+// Few rows are bound by the reading of keys and values: 8 sequences of one token, 32 heads on 8 of 128,
+// 38 thousand states in all, 157 MB: 37 us, 4.3 TB/s (a copy reaches 5.1).  Many rows are bound by the
+// matrix products and the exponentials beside them, of which each takes a SIMD about as
+// long: 2048 tokens on 6404 states, 215 GFLOP: 205 us, 1.05 PFLOP/s (a large product by itself 1.28);
+// vector instructions in a product's shadow are not free (a 32 x 32 product 36 ticks, six fmas
+// 33, both together 50).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -85,7 +107,12 @@ __device__ __forceinline__ void visible_sum(const Attn &a, int64_t q_at, const u
 }
 
 // A workgroup of kR x kK waves: kR over rows, 32 each; kK over keys, each on every kK-th block of
-// the split's keys with tiles in LDS of its own, joined at the end.  KB keys in a block.
+// the split's keys with tiles in LDS of its own, joined at the end.  KB keys in a block.  LDS and
+// registers hold two workgroups on a CU, two waves a SIMD, so that one wave's vector work runs beside
+// the other's products: 64 rows a wave and one wave a SIMD took 260 us where this takes 205
+// (2048 tokens on 6404 states), three waves a SIMD spill.  The blocks that no row of a tile sees are left out
+// of the wave's list before the loop: a branch around them in the loop keeps the next block's
+// scores from being computed beside this block's exponentials, and spilled (1540 us).
 template <int NK, int ND, int kR, int kK, int KB>
 __global__ __launch_bounds__(64 * kR * kK, 2) void attn_kernel(const Attn a) {
     constexpr int Dp = 32 * ND;      // entries of a row in LDS

@@ -1,11 +1,15 @@
 // Query and key heads between their projections and attention, for gfx950: the RMS
 // norm of each head and its rotary position, queries and keys in one launch.
 //
-// A head is read once into the registers of 8 to 64 lanes, its squares are summed
-// there, and it is written once.  Angles are position * frequency in 64 bits, reduced
-// to a part of a turn before anything is rounded to fp32, so that far positions keep
-// their phase; a workgroup computes cosine and sine once per token and pair and
-// takes them from LDS for all of the token's heads.
+// A head x becomes n = (x r) w, r = 1 / sqrt(mean(x^2) + eps), and pairs (a, b) of n become
+// (a c - b s, b c + a s).  It is read once into the registers of 8 to 64 lanes, its squares are
+// summed there, and it is written once: memory bounds it (8192 tokens of 40 heads of 128, bf16, 168
+// MB: 34 us, 4.9 TB/s; a copy reaches 5.1), and with few tokens the launch (one token 3.4 us).
+// Lanes take up to eight pairs, 16 bytes of either side at once for bf16 and for fp32 values.  Angles are
+// position * frequency in 64 bits, reduced to a part of a turn before anything is rounded
+// to fp32, so that far positions keep their phase; a workgroup computes cosine and sine
+// once per token and pair and takes them, like the weights, from LDS for all of the token's
+// heads (2048 tokens of 40 heads: 11.8 us; with the weights in registers 18.6).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -24,7 +28,7 @@ constexpr int64_t kMaxTokens = 1 << 19;
 constexpr int64_t kMaxHeads = 1 << 26;     // of all tokens
 constexpr int64_t kMaxStride = int64_t(1) << 40;
 constexpr int kThreads = 256;
-constexpr int kHeads = 2;       // heads that a group of lanes takes, where there are many
+constexpr int64_t kCosines = 32 << 10;  // bytes of LDS
 
 // Cosine and sine of `angle` radians, each times `factor`, as fp32.  The angle goes to
 // turns and their fraction in 64 bits, from there to the nearest quarter turn and a
@@ -372,12 +376,20 @@ int32_t s3d8_head_rope(const s3d8_head_rope_args *args, void *stream) {
     int lanes = 0;
     const HeadRopeFn fn =
         a.in_type == S3D8_ROWS_BF16 ? head_rope_build<true>(pairs, a.D, lanes) : head_rope_build<false>(pairs, a.D, lanes);
-    // A head a group while that does not fill the device eight times over, else kHeads.
-    const int64_t groups = kThreads / lanes, all = a.q_heads + a.k_heads, total = a.M * all;
-    const int64_t heads = groups * (total >= groups * cus * 8 ? kHeads : 1);
-    const int64_t tokens = (heads + all - 2) / all + 1;  // that so many heads in a row can belong to
+    // Heads that a group of lanes takes in turn, by how often one for each would fill the device: with
+    // more, the next head is on its way while one is turned, and a token's cosines serve more
+    // heads, but fewer workgroups share the work.  With 1, 2 and 4, in us: 512 tokens of 40 heads of 128
+    // (2.5 times) 5.2, 6.2, 8.0; 1601 of 32 heads of 80 (6.3) 8.1, 7.2, 8.7; 2048 of 40 (10) 12.8, 11.8, 12.4;
+    // 8192 of 40 (40) 43.2, 37.6, 34.2.
+    const int64_t groups = kThreads / lanes, all = a.q_heads + a.k_heads, total = a.M * all, full = total / (groups * cus);
+    int64_t heads, cosines;
+    for (int64_t each = full >= 20 ? 4 : full >= 6 ? 2 : 1;; each /= 2) {
+        heads = groups * each;
+        cosines = ((heads + all - 2) / all + 1) * (a.rotary_dim / 2) * (int64_t)sizeof(float2);  // of the tokens they are of
+        if (each == 1 || cosines <= kCosines) break;
+    }
     hipLaunchKernelGGL(fn, dim3((unsigned)((total + heads - 1) / heads)), dim3(kThreads),
-                       (size_t)(tokens * (a.rotary_dim / 2) * sizeof(float2)), (hipStream_t)stream, a, (int)heads);
+                       (size_t)cosines, (hipStream_t)stream, a, (int)heads);
     return s3d8::launch_status();
 }
 
