@@ -844,13 +844,16 @@ def head_rope(q, k=None, positions=None, rope=None, *, q_weight=None, k_weight=N
         strides += (0, 0)
     if q_out is None:
         q_out = torch.empty(M, H, D, dtype=dtype, device=dev)
-    strides += _heads(q_out, "q_out", dtype, (M, H, D), dev)
-    if k is not None:
-        if k_out is None:
-            k_out = torch.empty(M, Hk, D, dtype=dtype, device=dev)
-        strides += _heads(k_out, "k_out", dtype, (M, Hk, D), dev)
+        strides += (H * D, D)
     else:
+        strides += _heads(q_out, "q_out", dtype, (M, H, D), dev)
+    if k is None:
         strides += (0, 0)
+    elif k_out is None:
+        k_out = torch.empty(M, Hk, D, dtype=dtype, device=dev)
+        strides += (Hk * D, D)
+    else:
+        strides += _heads(k_out, "k_out", dtype, (M, Hk, D), dev)
     if q_weight is not None:
         _dev_check(q_weight, torch.float32, "q_weight", dev, numel=D)
     if k_weight is not None:
@@ -917,8 +920,8 @@ def cross_attention(q, k, v, *, kv_lens=None, mask=None, scale=None, out: str = 
         raise ValueError(f"k and v must be [{B} or 1][Lk][kv_heads][{D}], got {tuple(k.shape)} and {tuple(v.shape)}")
     shared = Bk == 1 and B > 1
     strides = []
-    for t in (q, k, v):
-        strides += [s if n > 1 else 0 for s, n in zip(t.stride()[:3], t.shape)]
+    for (seq, row, head, _), n in ((q.stride(), q.shape), (k.stride(), k.shape), (v.stride(), v.shape)):
+        strides += (seq if n[0] > 1 else 0, row if n[1] > 1 else 0, head if n[2] > 1 else 0)
     if kv_lens is not None:
         _dev_check(kv_lens, torch.int32, "kv_lens", dev, numel=Bk)
     mask_seq = mask_row = 0

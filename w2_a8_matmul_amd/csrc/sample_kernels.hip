@@ -1,19 +1,28 @@
-// The choice of the next token from rows of logits, for gfx950.
+// The choice of the next token from rows of logits, for gfx950: of the tokens that top-k, top-p
+// and min-p keep, the one at which the running sum of the weights W(i) = exp((l_i - max l) / T), in the
+// order of the index, passes u times their sum.
 //
 // Weights are whole numbers (2^44 times the exponential, rounded), so that sums of them do
 // not depend on their order: workgroups add them with atomics as they come, and the token is
 // the same on every run.  A row is cut into parts, so that few rows still fill the device:
 //   part  the largest logit of each part; with a top-k of at most 1024 also the part's
 //         candidates, in one read of the logits (below);
-//   bins  without such a top-k: sums of the weights by the logit's distance from the largest, in
+//   bins  without a top-k: sums of the weights by the logit's distance from the largest, in
 //         steps of a 64th of temperature, and so the step in which top-p ends;
 //   step  the tokens of that step, and the kept weight of each segment of the row;
 //   row   the rest for one row: the exact end of top-k and top-p among the few that are left,
 //         min-p, and the token at the random number, in the list of candidates or in the one segment
 //         that holds it.
-// With a top-k alone the launches are `part` and `row`.  Rows for which a list is too short
-// (a top-k over 1024, thousands of equal logits) are done by `row` alone, digit by digit of
-// the tokens' order, in up to a dozen reads of the row.
+// With a top-k alone the launches are `part` and `row`; a vocabulary of at most 3584 tokens is listed
+// by `row` itself, which is then the only one.  Rows for which a list is too short (a top-k over
+// 1024, thousands of equal logits) are done by `row` alone, digit by digit of the tokens'
+// order, in up to a dozen reads of the row (464 us for 5000 of one row's 128256 tokens).
+//
+// Many rows with a top-k are bound by the one read: 512 rows of 128256 fp32, 263 MB, k = 50: `part` 73 to
+// 82 us (51 without the lists, 5.1 TB/s as a copy), `row` 13.  Without a top-k `bins` and `step` are bound by
+// the exponentials in 64 bits, one a token: 138 and 172 us beside the 42 of `part`.  Few rows are bound
+// by the chain of steps in one workgroup, each of which waits for the last: one row, k = 50: 8 us
+// each of `part` and `row`; 8 rows of bf16, top-p: 4.6, 8.9, 11.8 and 16.3.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -1076,10 +1085,14 @@ Plan plan(const s3d8_sample_args &a, int cus) {
     const int64_t vectors = a.V / (a.type == S3D8_ROWS_BF16 ? 8 : 4) + 2;
     p.segments = (vectors + kT - 1) / kT;
     const bool one_k = !a.top_k, k_on = a.top_k_all > 0 && a.top_k_all < a.V;
-    // (candidates are the fewer the larger a part is beside k: 1000 of 128256 tokens 101 us with 32 parts)
+    // Parts: of kRound segments at least, so that all of a thread's loads are on their way at once; four
+    // workgroups for every CU (eight: 47 us for 40 with 128 rows, k = 50); and at least 16 k tokens, as the
+    // candidates are the fewer the larger a part is beside k (k = 1000 of one row: 101 us in 32 parts, 50 in 8).
     const int64_t most = !one_k || !k_on ? kMaxParts : std::max<int64_t>(4, a.V / (16 * (int64_t)a.top_k_all));
     p.parts = std::max<int64_t>(1, std::min<int64_t>({(p.segments + kRound - 1) / kRound, 4 * cus / p.rows, kMaxParts, most}));
+    // (the launches that take every weight have work for smaller parts: a segment at least)
     p.cuts = std::max<int64_t>(1, std::min<int64_t>(p.segments, 4 * cus / p.rows));
+    // (V = 19 to 3500: 17 to 29 us, through the parts 15 to 45)
     p.direct = a.V <= kListed;
     p.lists = !one_k || (k_on && a.top_k_all <= kMaxTopK);
     p.bins = !one_k || !k_on;
