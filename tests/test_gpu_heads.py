@@ -325,7 +325,7 @@ def check_sample(gpu, logits, u, T, k, p, mp, dtype=F32):
         assert abs(float(prob[m]) - share) <= 2.0 ** -24 * share * 1.01 + 2.0 ** -43
 
 
-@pytest.mark.parametrize("V", [1, 2, 7, 64, 1000, 3584, 3585, 5003, 40001])
+@pytest.mark.parametrize("V", [1, 2, 7, 64, 128, 129, 300, 512, 513, 1000, 1024, 1025, 3584, 3585, 5003, 40001])
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_sample(gpu, V, dtype):
     g = gen(8300, V)

@@ -22,7 +22,7 @@
 // 82 us (51 without the lists, 5.1 TB/s as a copy), `row` 13.  Without a top-k `bins` and `step` are bound by
 // the exponentials in 64 bits, one a token: 138 and 172 us beside the 42 of `part`.  Few rows are bound
 // by the chain of steps in one workgroup, each of which waits for the last: one row, k = 50: 8 us
-// each of `part` and `row`; 8 rows of bf16, top-p: 4.6, 8.9, 11.8 and 16.3.
+// each of `part` and `row`.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -49,7 +49,8 @@ constexpr uint32_t kNothing = 0x007FFFFFu;   // order_key(-infinity)
 constexpr uint32_t kTooMany = ~0u;
 constexpr int kMaxParts = 32;
 constexpr int kTops = 4096;                  // tops of a row that are looked at
-constexpr int kFewTokens = kT;               // tokens that are compared with one another
+constexpr int kFewest = 128;                 // tokens that are compared with one another
+constexpr int kFewTokens = 2 * kT;           // tokens that are sorted
 
 // fp32 values as whole numbers that order like them (-0 as 0, NaN as -infinity).
 __device__ __forceinline__ uint32_t order_key(float l) {
@@ -237,7 +238,7 @@ struct Sums {
 struct Shared : Sums {
     union {
         uint64_t bins[kBins];
-        ulonglong2 few[kFewTokens];  // place and weight
+        ulonglong2 few[kFewest];  // place and weight
     };
     uint64_t list[kListed];
     uint64_t weights[kListed];
@@ -386,8 +387,9 @@ __device__ __forceinline__ uint64_t reach(Shared &sh, int bits, uint64_t prefix,
     return prefix;
 }
 
-// Of at most kFewTokens tokens (sh.few, filled up with all ones to a multiple of kBatch), a thread
-// each: how many precede p in the order, and their weight.
+// Of at most kFewest tokens (sh.few, filled up with all ones to a multiple of kBatch), a thread
+// each: how many precede p in the order, and their weight.  (What is read from LDS grows with the square: 434
+// tokens 12 us; 60 take 1.2, sorted 2.3.)
 constexpr int kBatch = 8;
 __device__ __forceinline__ int preceding(const Shared &sh, int n, uint64_t p, uint64_t &weight) {
     int rank = 0;
@@ -410,6 +412,69 @@ __device__ __forceinline__ uint64_t sum_of(uint64_t v, Sums &sh) {
     uint64_t total;
     scan(v, sh, total);
     return total;
+}
+
+// The smaller (low) or the larger of a lane's value and that of the lane kApart from it (lane ^ kApart).
+template <int kApart>
+__device__ __forceinline__ uint64_t of_two(uint64_t x, bool low) {
+    const uint32_t lo = (uint32_t)x, hi = (uint32_t)(x >> 32);
+    uint64_t y;
+    if constexpr (kApart == 32) {
+        const auto l = __builtin_amdgcn_permlane32_swap(lo, lo, false, false), h = __builtin_amdgcn_permlane32_swap(hi, hi, false, false);
+        x = (uint64_t)h[0] << 32 | l[0];
+        y = (uint64_t)h[1] << 32 | l[1];
+    } else if constexpr (kApart == 16) {
+        const auto l = __builtin_amdgcn_permlane16_swap(lo, lo, false, false), h = __builtin_amdgcn_permlane16_swap(hi, hi, false, false);
+        x = (uint64_t)h[0] << 32 | l[0];
+        y = (uint64_t)h[1] << 32 | l[1];
+    } else {
+        auto moved = [](uint32_t v) {
+            constexpr int kCtrl = kApart == 8 ? 0x128 : kApart == 4 ? 0x141 : kApart == 2 ? 0x4E : 0xB1;
+            v = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kCtrl, 0xF, 0xF, false);
+            // (4: the lanes of 8 turned round, then those of 4)
+            return kApart == 4 ? (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x1B, 0xF, 0xF, false) : v;
+        };
+        y = (uint64_t)moved(hi) << 32 | moved(lo);
+    }
+    return (x < y) == low ? x : y;
+}
+// Sorts the workgroup's numbers, of which the first n places (place i of x[0] in thread i, place kT + i of x[1])
+// may hold others than all ones: bitonic, between lanes by moves of registers, further apart through
+// sh.list.  (33 rows of 5003 tokens, k = 200: a call 21 us, with all compared with all 25.5; 8 bf16 rows with top-p
+// 39 us and 45.5; through LDS alone the sort of 1024 took 9 us, digit by digit is faster.)
+__device__ __forceinline__ void sort(uint64_t (&x)[2], int n, Shared &sh) {
+    const int i = threadIdx.x;
+    const bool two = n > kT;
+    for (int level = 2; level / 2 < n; level *= 2) {
+        const bool up[2] = {(i & level) == 0, ((i + kT) & level) == 0};
+        auto each = [&](auto step) {
+            x[0] = step(x[0], up[0]);
+            if (two) x[1] = step(x[1], up[1]);
+        };
+        if (level == 2 * kT) {
+            const uint64_t low = min(x[0], x[1]);
+            x[1] = max(x[0], x[1]);
+            x[0] = low;
+        }
+        for (int apart = min(level, kT) / 2; apart >= 64; apart /= 2) {
+            sh.list[i] = x[0];
+            if (two) sh.list[kT + i] = x[1];
+            lds_barrier();
+            const uint64_t y[2] = {sh.list[i ^ apart], two ? sh.list[kT + (i ^ apart)] : 0};
+            lds_barrier();
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if (e == 0 || two) x[e] = (x[e] < y[e]) == (((i & apart) == 0) == up[e]) ? x[e] : y[e];
+        }
+        if (__builtin_amdgcn_readfirstlane(i) >= 2 * n) continue;  // (a wave of no place of the next power of two)
+        auto low = [&](int apart, bool up) { return ((i & apart) == 0) == up; };
+        if (level >= 64) each([&](uint64_t v, bool up) { return of_two<32>(v, low(32, up)); });
+        if (level >= 32) each([&](uint64_t v, bool up) { return of_two<16>(v, low(16, up)); });
+        if (level >= 16) each([&](uint64_t v, bool up) { return of_two<8>(v, low(8, up)); });
+        if (level >= 8) each([&](uint64_t v, bool up) { return of_two<4>(v, low(4, up)); });
+        if (level >= 4) each([&](uint64_t v, bool up) { return of_two<2>(v, low(2, up)); });
+        each([&](uint64_t v, bool up) { return of_two<1>(v, low(1, up)); });
+    }
 }
 
 // --------------------------------------------------------------- part
@@ -787,19 +852,22 @@ __global__ __launch_bounds__(kT) void sample_row_kernel(const Job j) {
     }
     uint64_t first;
     int n = 0, bits = 0;  // tokens in sh.list, bits in which their places differ
-    if (j.direct) {  // all tokens of the row but those of -infinity
-        if (threadIdx.x == 0) sh.listed = 0;
-        lds_barrier();
+    if (j.direct) {  // all tokens of the row
+        constexpr int kMine = kListed / kT;
+        float l[kMine];
+#pragma unroll
+        for (int q = 0; q < kMine; ++q) l[q] = row.one(min(q * kT + (int)threadIdx.x, row.V - 1));
         first = ~0ull;
-        row.each([&](int i, float l) {
-            const uint32_t key = order_key(l);
-            if (key <= kNothing) return;
-            const uint64_t x = place(key, i);
-            first = min(first, x);
-            sh.list[atomicAdd(&sh.listed, 1)] = x;
-        });
+#pragma unroll
+        for (int q = 0; q < kMine; ++q) {
+            const int i = q * kT + threadIdx.x;
+            if (i >= row.V) break;
+            const uint32_t key = order_key(l[q]);
+            sh.list[i] = place(key, i);
+            if (key > kNothing) first = min(first, sh.list[i]);
+        }
         first = smallest(first, sh);
-        n = sh.listed;
+        n = row.V;
         bits = kOrderBits;
         if (lim.k == 0) lim.k = kListed;
     } else {
@@ -892,8 +960,8 @@ __global__ __launch_bounds__(kT) void sample_row_kernel(const Job j) {
             n = sh.listed;
         }
     }
-    if (fits && n <= kFewTokens) {
-        // few: each thread compares its token with all of them, by place for what is kept, then by index
+    if (fits && n <= kFewest) {
+        // fewest: each thread compares its token with all of them, by place for what is kept, then by index
         uint64_t p = ~0ull, w = 0;
         if ((int)threadIdx.x < n) {
             p = sh.list[threadIdx.x];
@@ -902,7 +970,7 @@ __global__ __launch_bounds__(kT) void sample_row_kernel(const Job j) {
         int at = (int)threadIdx.x < n ? (int)threadIdx.x : -1;
         for (int pass = 0; pass < 2; ++pass) {
             if (at >= 0) sh.few[at] = make_ulonglong2(p, w);
-            if (threadIdx.x < kBatch - 1 && n + threadIdx.x < kFewTokens) sh.few[n + threadIdx.x] = make_ulonglong2(~0ull, 0);
+            if (threadIdx.x < kBatch - 1 && n + threadIdx.x < kFewest) sh.few[n + threadIdx.x] = make_ulonglong2(~0ull, 0);
             if (pass) total = sum_of(w, sh);
             lds_barrier();
             uint64_t before = 0;
@@ -924,6 +992,48 @@ __global__ __launch_bounds__(kT) void sample_row_kernel(const Job j) {
             at = w ? atomicAdd(&sh.listed, 1) : -1;
             lds_barrier();
             n = sh.listed;
+        }
+    }
+    // those of the list at this thread's places
+    auto listed = [&](uint64_t(&x)[2], int n) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) x[e] = e * kT + (int)threadIdx.x < n ? sh.list[e * kT + threadIdx.x] : ~0ull;
+    };
+    // the weights of the first `most` of n sorted tokens, and the sums before them
+    auto weigh = [&](const uint64_t(&x)[2], int n, int most, bool by_index, uint64_t(&w)[2], uint64_t(&before)[2]) {
+        total = 0;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            w[e] = before[e] = 0;
+            if (e * kT >= n) break;
+            if (e * kT + (int)threadIdx.x < most) w[e] = weight(by_index ? (uint32_t)x[e] : place_key(x[e]));
+            uint64_t sum;
+            before[e] = total + scan(w[e], sh, sum);
+            total += sum;
+        }
+    };
+    if (fits && n <= kFewTokens) {
+        // few: sorted by place for what is kept, the first of them, then by index
+        uint64_t x[2], w[2], before[2];
+        listed(x, n);
+        for (int pass = 0; pass < 2; ++pass) {
+            sort(x, n, sh);
+            weigh(x, n, pass ? n : min(n, lim.k), pass, w, before);
+            const uint64_t left = pass ? target(u, total) : lim.top_p < 1.0f ? lim.end(total) : ~0ull;
+            uint64_t out = kFewTokens;  // the first place that is not kept
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                if (pass) {
+                    if (before[e] < left && left <= before[e] + w[e]) answer((uint32_t)(x[e] >> 32), w[e], total);
+                } else if (w[e] && w[e] >= least && before[e] < left) {
+                    x[e] = (uint64_t)place_index(x[e]) << 32 | place_key(x[e]);
+                } else {
+                    x[e] = ~0ull;
+                    out = min(out, (uint64_t)(e * kT + threadIdx.x));
+                }
+            }
+            if (pass) return;
+            n = (int)smallest(out, sh);
         }
     }
     if (fits) {
@@ -988,17 +1098,15 @@ __global__ __launch_bounds__(kT) void sample_row_kernel(const Job j) {
             };
             uint64_t end = ~0ull;
             if (n && n <= kFewTokens) {
-                uint64_t p = ~0ull, w = 0, before;
-                if (threadIdx.x < n) {
-                    p = sh.list[threadIdx.x];
-                    w = weight(place_key(p));
-                }
-                if (threadIdx.x < n + kBatch - 1 && threadIdx.x < kFewTokens) sh.few[threadIdx.x] = make_ulonglong2(p, w);
-                __syncthreads();
                 const uint64_t left = global(j.ends)[2 * r + 1];
-                if (threadIdx.x < n) {
-                    preceding(sh, n, p, before);
-                    if (before < left && left <= before + w) sh.one = p;
+                uint64_t x[2], w[2], before[2];
+                listed(x, n);
+                sort(x, n, sh);
+                weigh(x, n, n, false, w, before);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    if (before[e] < left && left <= before[e] + w[e]) sh.one = x[e];
+                    if (e * kT + threadIdx.x < n) sh.list[e * kT + threadIdx.x] = x[e];
                 }
                 __syncthreads();
                 end = sh.one;

@@ -22,9 +22,10 @@ the bytes moved do not depend on the values.
 With ``block``, the operators around the linear layers instead: each call of
 ``block_calls()`` CALLS times, over enough copies of its operands that none is
 still in a cache, one after the other in that order; with a part of a label
-after it, only the calls whose label holds it.
+after it, only the calls whose label holds it.  With ``heads``, those on heads and
+logits, ``head_calls()``.
 
-Usage: python -m w2_a8_matmul_amd.profile_run [block [PART]]   (from the repository root)
+Usage: python -m w2_a8_matmul_amd.profile_run [block|heads [PART]]   (from the repository root)
 """
 from __future__ import annotations
 
@@ -98,19 +99,74 @@ def block_calls():
     ]
 
 
-def block(part: str = "") -> None:
+def head_calls():
+    """The same of head_rope, cross_attention and sample."""
+    import torch
+
+    import w2_a8_matmul_amd as s3d8
+
+    dev = torch.device("cuda:0")
+    bf, f32 = torch.bfloat16, torch.float32
+
+    def rope(M, H, Hk, D, dtype, norm=True, out="bf16"):
+        def make():
+            x = torch.randn(M, (H + 2 * Hk) * D, device=dev).to(dtype)
+            handle = s3d8.Rope(D, 500000.0, scaling="llama3", factor=8.0, original_length=8192)
+            w = 1 + 0.1 * torch.randn(D, device=dev) if norm else None
+            q, k = x[:, :H * D].view(M, H, D), x[:, H * D:(H + Hk) * D].view(M, Hk, D)
+            pos = torch.arange(M, device=dev)
+            return lambda: s3d8.head_rope(q, k, pos, handle, q_weight=w, k_weight=w, out=out)
+        label = f"head_rope {M} x ({H} + {Hk}) x {D}, {dtype}{', norm' if norm else ''}, {out}".replace("torch.", "")
+        return label, M * (H + Hk) * D * (dtype.itemsize + (2 if out == "bf16" else 4)), make
+
+    def attention(B, Lq, Lk, H, Hk, D, lens=False, shared=False, mask=False):
+        def make():
+            n = 1 if shared else B
+            q, k, v = (torch.randn(b, L, h, D, device=dev).to(bf) for b, L, h in ((B, Lq, H), (n, Lk, Hk), (n, Lk, Hk)))
+            ls = torch.linspace(Lk // 2, Lk, B, device=dev).to(torch.int32) if lens else None
+            m = None
+            if mask:  # four images, each seen by the tokens after it
+                starts = torch.tensor([0.05, 0.15, 0.3, 0.45], device=dev) * Lq
+                m = (torch.arange(Lq, device=dev)[:, None] >= starts).repeat_interleave(-(-Lk // 4), 1)[None, :, :Lk].contiguous()
+            return lambda: s3d8.cross_attention(q, k, v, kv_lens=ls, mask=m)
+        label = (f"cross_attention {B} x {Lq} on {Lk}, {H} on {Hk} x {D}{', lengths from a half' if lens else ''}"
+                 f"{', shared states' if shared else ''}{', mask of four images' if mask else ''}")
+        return label, 4 * (1 if shared else B) * Lk * Hk * D + 4 * B * Lq * H * D + mask * Lq * Lk, make
+
+    def sample(M, V, dtype, **limits):
+        def make():
+            l = torch.randn(M, V, device=dev) * 2
+            at = torch.rand(M, V, device=dev) < 40 / V
+            l = torch.where(at, l + 8 * torch.rand(M, V, device=dev), l).to(dtype)
+            u = torch.rand(M, device=dev)
+            return lambda: s3d8.sample(l, u, temperature=0.9, **limits)
+        label = f"sample {M} x {V}, {dtype}, {', '.join(f'{k} {v}' for k, v in limits.items())}".replace("torch.", "")
+        return label, M * V * dtype.itemsize, make
+
+    return [
+        rope(1, 32, 8, 128, f32, norm=False), rope(77, 16, 4, 80, bf, out="f32"), rope(2048, 32, 8, 128, bf), rope(8192, 32, 8, 128, bf),
+        attention(1, 1, 1601, 32, 8, 128), attention(8, 1, 6404, 32, 8, 128, lens=True),
+        attention(16, 1, 6404, 32, 8, 128, shared=True), attention(1, 1601, 1601, 16, 16, 80),
+        attention(1, 2048, 6404, 32, 8, 128), attention(1, 2048, 6404, 32, 8, 128, mask=True),
+        sample(1, 128256, f32, top_k=50, top_p=0.9), sample(8, 128256, bf, top_p=0.95),
+        sample(33, 5003, f32, top_k=200, top_p=0.8, min_p=0.05), sample(512, 128256, f32, top_k=50, top_p=0.95, min_p=0.01),
+        sample(512, 128256, f32, top_p=0.95), sample(1, 128256, f32, top_k=1000, top_p=0.9), sample(1, 1000, f32, top_k=50, top_p=0.9),
+    ]
+
+
+def block(part: str = "", calls=block_calls) -> None:
     import torch
 
     torch.manual_seed(1)
-    for label, nbytes, make in block_calls():
+    for label, nbytes, make in calls():
         if part not in label:
             continue
-        calls = [make() for _ in range(max(1, min(CALLS, -(-_CACHES // nbytes))))]
+        copies = [make() for _ in range(max(1, min(CALLS, -(-_CACHES // nbytes))))]
         torch.cuda.synchronize()
         for i in range(CALLS):
-            calls[i % len(calls)]()
+            copies[i % len(copies)]()
         torch.cuda.synchronize()
-        print(f"[profile_run] {CALLS} x {label} ({len(calls)} copies)", flush=True)
+        print(f"[profile_run] {CALLS} x {label} ({len(copies)} copies)", flush=True)
 
 
 def main() -> None:
@@ -204,7 +260,7 @@ def main() -> None:
 
 
 if __name__ == "__main__":
-    if sys.argv[1:2] == ["block"]:
-        block(*sys.argv[2:3])
+    if sys.argv[1:2] in (["block"], ["heads"]):
+        block("".join(sys.argv[2:3]), block_calls if sys.argv[1] == "block" else head_calls)
     else:
         main()
