@@ -667,8 +667,9 @@ typedef struct s3d8_cross_attention_args {
  *                a query is not in its sum, whatever it holds.
  *   workspace    s3d8_cross_attention_workspace_bytes(args, CU count) bytes, 16-B aligned; NULL
  *                where that is 0.  It holds nothing between calls.
+ *   o            16-B aligned, like xq; must not overlap q, k or v.
  *   At most 65535 sequences, 2^24 tokens and keys each, 4096 heads, and B Lq heads at most
- *   2^30; with xq at most 524288 rows, of at most 65536 entries; o, xq 16-B aligned.
+ *   2^30; with xq at most 524288 rows, of at most 65536 entries.
  * Errors: INVALID_ARG, SHAPE, ALIGN, DEVICE, HIP. */
 int32_t s3d8_cross_attention(const s3d8_cross_attention_args *args, void *stream);
 

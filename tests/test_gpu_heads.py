@@ -547,3 +547,53 @@ def test_heads_run_together_on_a_stream_and_in_a_graph(gpu):
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(held[name], r[name]) for name in r)
+
+
+def test_heads_calls_at_once_and_two_graphs(gpu):
+    """Calls whose keys are split and rows cut, so that they have workspaces: on two streams at once and as two graphs
+    replayed at once, the bits of each by itself."""
+    g = gen(8900)
+    B, Lk, V = 3, 1000, 20011
+    sets = []
+    for _ in range(2):
+        q, k, v = states(g, gpu, B, 1, Lk, 8, 2, 64)
+        mask = dev(g.random((B, 1, Lk)) < 0.5, gpu)
+        logits, u = dev(g.standard_normal((B, V)).astype(np.float32) * 3, gpu), dev(g.random(B, dtype=np.float32), gpu)
+        sets.append((q, k, v, mask, logits, u))
+
+    def run(q, k, v, mask, logits, u):
+        return (s3d8.cross_attention(q, k, v), s3d8.cross_attention(q, k, v, mask=mask), *s3d8.sample(logits, u, top_p=0.9),
+                *s3d8.sample(logits, u, top_k=50, min_p=0.01))
+
+    def same(a, b):
+        assert all(torch.equal(x, y) for x, y in zip(a, b, strict=True))
+
+    want = [run(*s) for s in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(5):
+        for n, stream in enumerate(streams):
+            with torch.cuda.stream(stream):
+                got[n].append(run(*sets[n]))
+    torch.cuda.synchronize()
+    for n in range(2):
+        for r in got[n]:
+            same(r, want[n])
+
+    graphs, held = [torch.cuda.CUDAGraph() for _ in sets], []
+    for graph, s in zip(graphs, sets):
+        with torch.cuda.graph(graph):
+            held.append(run(*s))
+    for _ in range(3):
+        for r in held:
+            for t in r:
+                t.zero_()
+        torch.cuda.synchronize()
+        for graph, stream in zip(graphs, streams):
+            with torch.cuda.stream(stream):
+                graph.replay()
+        torch.cuda.synchronize()
+        for r, w in zip(held, want):
+            same(r, w)
+        same(run(*sets[0]), want[0])

@@ -986,7 +986,7 @@ def sample(logits, u, *, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, token=N
         else:
             pointers.append(0)
             numbers.append(x)
-    numbers[1] = min(int(numbers[1]), 0x7FFFFFFF)
+    numbers[1] = max(-1, min(int(numbers[1]), 0x7FFFFFFF))
     if token is None:
         token = torch.empty(M, dtype=torch.int32, device=dev)
     else:
