@@ -114,8 +114,8 @@ struct Weights {
     uint32_t top;
     double m, t, rt;
     __device__ __forceinline__ Weights(uint32_t top, const Limits &l) : top(top), m((double)key_value(top)), t(l.t), rt(l.rt) {}
-    __device__ __forceinline__ double exponent(uint32_t key) const {  // NaN where l is infinite
-        const double d = (double)key_value(key) - m, x = d * rt;
+    __device__ __forceinline__ double exponent(float l) const {  // NaN where l is infinite
+        const double d = (double)l - m, x = d * rt;
         return __builtin_fma(__builtin_fma(-x, t, d), rt, x);
     }
     __device__ __forceinline__ uint64_t of(double x) const {
@@ -126,14 +126,21 @@ struct Weights {
         return (uint64_t)__double_as_longlong(__builtin_fma(s, e.less_one, s) + 0x1p52) & ((1ull << 52) - 1);
     }
     __device__ __forceinline__ uint64_t operator()(uint32_t key) const {
-        return key == top ? 1ull << 44 : key <= kNothing ? 0 : of(exponent(key));
+        return key == top ? 1ull << 44 : key <= kNothing ? 0 : of(exponent(key_value(key)));
     }
-    // the same, and the bin of the distance from the largest logit
-    __device__ __forceinline__ int bin(uint32_t key, double &x) const {
-        x = key == top ? 0.0 : key <= kNothing ? -1e300 : exponent(key);
+    // the same of a logit, and the bin of the distance from the largest one (the last: no weight, NaN too)
+    __device__ __forceinline__ int bin(float l, double &x) const {
+        x = (double)l == m ? 0.0 : exponent(l);
         return x > -(double)kBins / kSteps ? min((int)(x * -(double)kSteps), kBins - 1) : kBins - 1;
     }
-    __device__ __forceinline__ uint64_t at(uint32_t key, double x) const { return key == top ? 1ull << 44 : of(x); }
+    __device__ __forceinline__ uint64_t at(float l, double x) const { return (double)l == m ? 1ull << 44 : of(x); }
+    // Logits below this one are in bins past `last`, and those of the last bin have no weight: 2^44 exp(-32) is
+    // less than half. One bin and 2^-20 of the value are left for rounding.
+    __device__ __forceinline__ float cut(int last) const {
+        const double c = m - t * (double)(min(last, kBins) + 2) * (1.0 / kSteps);
+        const float f = (float)(c - __builtin_fabs(c) * 0x1p-20);
+        return f == f ? f : -INFINITY;
+    }
 };
 
 // A row of logits as slots of 16 aligned bytes: slot 0 what comes before the first of them, slots 1
@@ -712,6 +719,7 @@ __global__ __launch_bounds__(kT) void sample_bins_kernel(const Job j) {
     const uint64_t first = first_place(j, r);
     if (!lim.binned() || !(lim.top_p < 1.0f) || first == ~0ull) return;
     const Weights weight(place_key(first), lim);
+    const float cut = weight.cut(kBins);
     for (int i = threadIdx.x; i < kBins; i += kT) bins[i] = 0;
     __syncthreads();
     for (int s = begin; s < end; s += kRound) {
@@ -723,10 +731,11 @@ __global__ __launch_bounds__(kT) void sample_bins_kernel(const Job j) {
             if (s + n >= end) break;
 #pragma unroll
             for (int v = 0; v < R::kV; ++v) {
-                const uint32_t key = order_key(u[n][v]);
+                const float l = u[n][v];
+                if (!(l >= cut)) continue;
                 double x;
-                const int b = weight.bin(key, x);
-                const uint64_t w = weight.at(key, x);
+                const int b = weight.bin(l, x);
+                const uint64_t w = weight.at(l, x);
                 if (w) atomicAdd((unsigned long long *)&bins[b], (unsigned long long)w);
             }
         }
@@ -771,6 +780,7 @@ __global__ __launch_bounds__(kT) void sample_step_kernel(const Job j) {
         }
     }
     if (part == 0 && threadIdx.x == 0) global(j.ends)[2 * r] = last;
+    const float cut = weight.cut(last);
     for (int s = begin; s < end; s += kRound) {
 #pragma unroll
         for (int n = 0; n < kRound; ++n) u[n] = next[n];
@@ -782,12 +792,13 @@ __global__ __launch_bounds__(kT) void sample_step_kernel(const Job j) {
             if (s + n >= end) break;
 #pragma unroll
             for (int v = 0; v < R::kV; ++v) {
-                const uint32_t key = order_key(u[n][v]);
+                const float l = u[n][v];
+                if (!(l >= cut)) continue;
                 double x;
-                const int b = weight.bin(key, x);
-                if (b > last || key <= kNothing) continue;
+                const int b = weight.bin(l, x);
+                if (b > last) continue;
                 if (b == last) {
-                    const uint64_t p = place(key, row.index((s + n) * kT + threadIdx.x) + v);
+                    const uint64_t p = place(order_key(l), row.index((s + n) * kT + threadIdx.x) + v);
                     const int here = atomicAdd(&sh.listed, 1);
                     if (here < kStepHere) {
                         sh.step[here] = p;
@@ -796,7 +807,7 @@ __global__ __launch_bounds__(kT) void sample_step_kernel(const Job j) {
                         if (at < kListed) global(j.step)[r * kListed + at] = p;
                     }
                 } else {
-                    const uint64_t w = weight.at(key, x);
+                    const uint64_t w = weight.at(l, x);
                     if (w >= least) sum[n] += w;
                 }
             }
@@ -1137,11 +1148,10 @@ __global__ __launch_bounds__(kT) void sample_row_kernel(const Job j) {
             uint64_t w[R::kV], mine = 0;
 #pragma unroll
             for (int i = 0; i < R::kV; ++i) {
-                const uint32_t key = order_key(v[i]);
                 double x;
-                const int b = weight.bin(key, x);
-                const bool in = key > kNothing && (b < last || (b == last && place(key, row.index(slot) + i) <= end));
-                w[i] = in ? weight.at(key, x) : 0;
+                const int b = weight.bin(v[i], x);
+                const bool in = b < last || (b == last && place(order_key(v[i]), row.index(slot) + i) <= end);
+                w[i] = in ? weight.at(v[i], x) : 0;
                 if (w[i] < least) w[i] = 0;
                 mine += w[i];
             }
