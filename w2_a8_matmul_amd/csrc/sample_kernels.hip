@@ -20,7 +20,7 @@
 //
 // Many rows with a top-k are bound by the one read: 512 rows of 128256 fp32, 263 MB, k = 50: `part` 73 to
 // 82 us (51 without the lists, 5.1 TB/s as a copy), `row` 13.  Without a top-k `bins` and `step` are bound by
-// the exponentials in 64 bits, one a token: 138 and 172 us beside the 42 of `part`.  Few rows are bound
+// the exponentials in 64 bits, one a token: 111 and 146 us beside the 50 of `part`.  Few rows are bound
 // by the chain of steps in one workgroup, each of which waits for the last: one row, k = 50: 8 us
 // each of `part` and `row`.
 #include <hip/hip_runtime.h>
