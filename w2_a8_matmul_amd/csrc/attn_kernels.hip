@@ -169,10 +169,9 @@ __global__ __launch_bounds__(64 * kR * kK, 2) void attn_kernel(const Attn a) {
     auto copy_values = [&](int block, int slot) { copy(vp, a.v_row, block, tiles[wk][1][slot], voff); };
 
     // the mask's bits of a block, of 64 keys a word
-    auto load_word = [&](int64_t at, int block) {
-        const uint64_t w = global(a.words)[at + block * KB / kKeys * a.word_block];
-        return KB == kKeys ? w : w >> (block * KB % kKeys);
-    };
+    // (shifted where they are used, a step later: a shift at the load waits for it)
+    auto load_word = [&](int64_t at, int block) { return global(a.words)[at + block * KB / kKeys * a.word_block]; };
+    auto bits_of = [&](uint64_t word, int block) { return word >> (block * KB % kKeys); };  // the block's: the first KB
     constexpr uint64_t kAll = KB == 64 ? ~0ull : (1ull << (KB % 64)) - 1;
 
     // With a mask, the blocks that any row of the tile sees, by the words of the tile's tokens: a lane a
@@ -189,7 +188,7 @@ __global__ __launch_bounds__(64 * kR * kK, 2) void attn_kernel(const Attn a) {
 #pragma unroll 4
             for (int t = t0 + wave; t <= t1; t += kR * kK)
                 any |= load_word((a.shared ? t / a.Lq : seq) * a.word_seq + (a.shared ? t % a.Lq : t) * a.word_row, block);
-            const uint64_t bits = __ballot((any & kAll) != 0 && n + lane < count);
+            const uint64_t bits = __ballot((bits_of(any, block) & kAll) != 0 && n + lane < count);
             if (lane == 0) atomicOr((unsigned long long *)&seen[n / 64], (unsigned long long)bits);
         }
         __syncthreads();
@@ -240,7 +239,7 @@ __global__ __launch_bounds__(64 * kR * kK, 2) void attn_kernel(const Attn a) {
         }
         return __builtin_bit_cast(bf8, two);
     };
-    auto word_of = [&](int block) { return a.words && block < end ? load_word(word_at, block) & kAll : kAll; };
+    auto word_of = [&](int block) { return a.words && block < end ? load_word(word_at, block) : ~0ull; };
     auto inside = [&](int block) {  // the bits of the keys that exist
         const int n = block < end ? len - block * KB : 0;
         return n < KB ? (1ull << max(n, 0)) - 1 : kAll;
@@ -278,7 +277,7 @@ __global__ __launch_bounds__(64 * kR * kK, 2) void attn_kernel(const Attn a) {
         auto step = [&](int n, int slot, f16v(&s)[KT], f16v(&t)[KT]) {
             const int later = block_at(n + 2), other = slot ^ 1;
             wait_vmcnt_barrier<0>();
-            const uint64_t bits = word & inside(block);
+            const uint64_t bits = bits_of(word, block) & inside(block);
             word = next_word;
             next_word = word_of(later);
             copy_keys(later, slot);  // this block's keys were read a step ago, the last one's values too
