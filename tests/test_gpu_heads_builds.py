@@ -111,6 +111,45 @@ def test_cross_attention_mask_of_more_blocks_than_are_listed(gpu, Lq, Lk):
     close(o[:, some], want, bound)
 
 
+@pytest.mark.parametrize("B,Lq,Lk,H,Hk,D,shared", [
+    (1, 1, 1601, 32, 8, 128, False), (2, 140, 300, 4, 2, 80, False), (2, 33, 129, 4, 4, 48, False), (5, 20, 333, 8, 2, 96, True),
+    (20, 129, 133, 8, 8, 64, False), (9, 65, 191, 48, 16, 80, False), (17, 129, 200, 16, 16, 96, False),
+    (5, 200, 257, 32, 8, 128, False), (33, 1, 300, 32, 8, 128, False), (11, 500, 210, 8, 8, 64, True)])
+def test_cross_attention_values_that_are_hidden_leave_the_bits(gpu, B, Lq, Lk, H, Hk, D, shared):
+    """Infinities and NaN in values that a row does not see: the bits of a call with zeros there, in every build.  A row
+    that sees some has their sum in their entry, and its other entries as they were."""
+    g = gen(9040, B, Lq, Lk, D)
+    q, k, v = states(g, gpu, B, Lq, Lk, H, Hk, D, Bk=1 if shared else None)
+    mask = g.random((B, Lq, Lk)) < 0.6
+    hidden = [3, 40, 41, Lk // 2, Lk - 9]
+    mask[:, :, hidden] = False
+    lens = np.full(1 if shared else B, Lk, np.int32)
+    lens[-1] = Lk - 5
+    inf, nan = float("inf"), float("nan")
+    dirty_k, dirty_v, v = k.clone(), v.clone(), v.clone()
+    dirty_k[:, hidden], dirty_k[-1, Lk - 5:] = nan, inf
+    v[:, hidden], v[-1, Lk - 5:] = 0, 0
+    dirty_v[:, hidden[0]], dirty_v[:, hidden[1:3]], dirty_v[:, hidden[3:]], dirty_v[-1, Lk - 5:] = inf, -inf, nan, nan
+    extra = np.zeros((B, Lq, D))
+    for key, entry, x in [(5, 0, inf), (6, 1, -inf), (7, 2, nan), (8, 3, inf), (Lk - 10, 3, -inf), (60, D - 1, inf),
+                          (61, D - 1, inf), (9, 4, -inf), (10, 4, -inf), (2, 5, nan), (1, 5, inf)]:
+        v[:, key, -1, entry], dirty_v[:, key, -1, entry] = 0, x
+        with np.errstate(invalid="ignore"):
+            extra[:, :, entry] += np.where(mask[:, :, key], x, 0)
+    kw = dict(kv_lens=dev(lens, gpu), mask=dev(mask, gpu))
+    want = s3d8.cross_attention(q, k, v, **kw)
+    want[:, :, -(H // Hk):] += dev(extra, gpu, BF16)[:, :, None]
+    got = s3d8.cross_attention(q, dirty_k, dirty_v, **kw)
+    lost = torch.isnan(want)
+    assert torch.equal(torch.isnan(got), lost)
+    assert torch.equal(got[~lost], want[~lost])
+    q[0, Lq // 2, 0] = nan  # a row of its own
+    again = s3d8.cross_attention(q, dirty_k, dirty_v, **kw)
+    assert torch.isnan(again[0, Lq // 2, 0]).all()
+    again[0, Lq // 2, 0] = got[0, Lq // 2, 0]
+    assert torch.equal(torch.isnan(again), lost) and torch.equal(again[~lost], got[~lost])
+
+
 # ------------------------------------------------------------------ head_rope
 @pytest.mark.parametrize("M,H,Hk,D,rot,layout,norm,dtype,out", [
     # two heads a group of lanes: heads that fill the device 6 to 20 times

@@ -82,28 +82,22 @@ __device__ __forceinline__ float halves_max(float x) {
     return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 
-// sum_j p_j v_j of one row over the keys from `begin` to `end` that it sees: entries
-// `lane` and `lane` + 64.
-__device__ __forceinline__ void visible_sum(const Attn &a, int64_t q_at, const uint16_t *kp, const uint16_t *vp, int64_t word_at,
-                                         float most, int begin, int end, float (&e)[2]) {
-    const int lane = threadIdx.x & 63;
-    const uint64_t *words = a.words + word_at;
-    float q[2];
+// Of two bf16 numbers in a word: those that are finite, and a code of each of the others, 1 for
+// infinity, 32 for minus infinity and 1024 for NaN: sums of 16 codes tell which were among them.
+__device__ __forceinline__ void take_apart(uint32_t w, uint32_t &finite, uint32_t &codes) {
+    finite = codes = 0;
 #pragma unroll
-    for (int n = 0; n < 2; ++n) q[n] = lane + 64 * n < a.D ? bf16_to_f32(a.q[q_at + lane + 64 * n]) : 0.0f;
-    for (int key = begin; key < end; ++key) {
-        if (!(words[(key / kKeys) * a.word_block] >> (key % kKeys) & 1)) continue;
-        float s = 0.0f;
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-            if (lane + 64 * n < a.D) s = __builtin_fmaf(q[n], bf16_to_f32(kp[key * a.k_row + lane + 64 * n]), s);
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) s += __shfl_xor(s, o);
-        const float p = (float)(__bf16)__builtin_amdgcn_exp2f(__builtin_fmaf(s, a.scale, -most));
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-            if (lane + 64 * n < a.D) e[n] = __builtin_fmaf(p, bf16_to_f32(vp[key * a.v_row + lane + 64 * n]), e[n]);
+    for (int n = 0; n < 32; n += 16) {
+        const uint32_t x = w >> n & 0xFFFFu;
+        const bool is = (x & 0x7F80u) != 0x7F80u;
+        finite |= (is ? x : 0) << n;
+        codes |= (is ? 0 : x & 0x7Fu ? 0x4480u : x & 0x8000u ? 0x4200u : 0x3F80u) << n;
     }
+}
+__device__ __forceinline__ float with_codes(float x, int codes) {
+    if (codes == 0) return x;
+    const bool above = codes & 31, below = codes >> 5;  // (NaN: below, and not minus infinity alone)
+    return x + (codes >> 10 || (above && below) ? NAN : above ? INFINITY : -INFINITY);
 }
 
 // A workgroup of kR x kK waves: kR over rows, 32 each; kK over keys, each on every kK-th block of
@@ -124,6 +118,7 @@ __global__ __launch_bounds__(64 * kR * kK, 2) void attn_kernel(const Attn a) {
     __shared__ __attribute__((aligned(1024))) uint4 tiles[kK][2][2][kTile];  // keys and values, two blocks of each
     __shared__ uint64_t seen[kListed / 64];
     __shared__ uint16_t list[kListed];
+    __shared__ int again;  // sums are formed twice
 
     const int lane = threadIdx.x & 63, col = lane & 31, h = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), wr = wave % kR, wk = wave / kR;
@@ -257,6 +252,7 @@ __global__ __launch_bounds__(64 * kR * kK, 2) void attn_kernel(const Attn a) {
     // scores of the next block are computed: their products run beside the exponentials, and the
     // largest of them is found beside the products with the values.
     const int steps = (count + kK - 1) / kK;
+    if (threadIdx.x == 0) again = 0;  // (read after the steps' barriers)
     if (steps > 0) {
         int block = block_at(0), next = block_at(1);
         uint64_t word = word_of(block), next_word = word_of(next);
@@ -349,30 +345,101 @@ __global__ __launch_bounds__(64 * kR * kK, 2) void attn_kernel(const Attn a) {
         }
         wait_vmcnt_barrier<0>();  // the last steps' copies have landed before LDS is used again or let go
     }
-    if (a.words) {
-        // A hidden key has p = 0, but the product with an infinite or NaN value of it is NaN. Rows that
-        // are not finite are summed again, one by one, over what they see.
+    if (a.words && steps > 0) {
+        // A hidden key has p = 0, but the product with an infinite or NaN value of it is NaN. Sums that are
+        // not finite are formed again over the same p, from the finite values, and by a product of the
+        // keys that a row sees with codes of the other values, which of those are among them: the bits are
+        // those of a call whose hidden values are 0. (A row whose scores have a NaN is NaN: it stays.) One step
+        // after the other, copies a step ahead: 1.0 ms in all where a mask of images on 2048 x 6404 takes 0.2.
         float z = 0.0f;
 #pragma unroll
         for (int d = 0; d < ND; ++d)
 #pragma unroll
             for (int r = 0; r < 16; ++r) z = __builtin_fmaf(acc[d][r], 0.0f, z);
-        uint64_t bad = __ballot(z != z);
-        bad = (bad | bad >> 32) & 0xFFFFFFFFull;
-        while (bad) {
-            const int lost = __builtin_ctzll(bad);
-            bad &= bad - 1;
-            float e[2] = {0.0f, 0.0f};
-            for (int n = 0, block; (block = block_at(n)) < end; ++n)
-                visible_sum(a, __shfl((long long)q_at, lost), kp, vp, __shfl((long long)word_at, lost), __shfl(most, lost),
-                            block * KB, min((block + 1) * KB, len), e);
+        uint64_t lost = __ballot(z != z && row < a.R);
+        const uint64_t none = __ballot(sum != sum);
+        lost = (lost | lost >> 32) & ~(none | none >> 32) & 0xFFFFFFFFull;
+        if (lost && lane == 0) again = 1;
+        __syncthreads();
+        if (again) {  // (the workgroup's: its waves share tiles)
+            const bool mine = lost >> col & 1;
 #pragma unroll
             for (int d = 0; d < ND; ++d)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const float x = __shfl(e[d / 2], (32 * d + 8 * (r / 4) + 4 * h + r % 4) & 63);
-                    if (col == lost) acc[d][r] = x;
+                for (int r = 0; r < 16; ++r) acc[d][r] = mine ? 0.0f : acc[d][r];
+            float top = -FLT_MAX;  // the running maximum as it was
+            copy_keys(block_at(0), 0);
+            copy_values(block_at(0), 0);
+            for (int n = 0; n < steps; ++n) {
+                const int slot = n & 1, block = block_at(n), next = block_at(n + 1);
+                const uint64_t bits = bits_of(word_of(block), block) & inside(block);
+                wait_vmcnt_barrier<0>();
+                copy_keys(next, slot ^ 1);  // read by all a step ago
+                copy_values(next, slot ^ 1);
+                if (!lost) continue;
+                f16v s[KT];
+#pragma unroll
+                for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) s[kt][r] = 0.0f;
+#pragma unroll
+                for (int i = 0; i < kScores; ++i)
+                    s[i % KT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(key_operand(slot, i), qf[i / KT], s[i % KT], 0, 0, 0);
+                // (the bits of register r, and of the one after it)
+                auto sees = [&](int kt, int r) { return (uint32_t)(bits >> (4 * h + 32 * kt)) >> (8 * (r / 4) + r % 4); };
+#pragma unroll
+                for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) s[kt][r] = sees(kt, r) & 1 ? s[kt][r] : -INFINITY;
+                float m = halves_max(most_of(s)) * a.scale;
+                if (__ballot(m > top + kSlack)) {
+                    m = fmaxf(top, m);
+                    const float f = mine ? __builtin_amdgcn_exp2f(top - m) : 1.0f;
+                    top = m;
+#pragma unroll
+                    for (int d = 0; d < ND; ++d)
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) acc[d][r] *= f;
                 }
+                // p, and 1 for a key that is seen: of the lost rows, the others' sums stay
+                uint32_t pf[KB / 4], one[KB / 4];
+#pragma unroll
+                for (int e = 0; e < KB / 4; ++e) {
+                    bf2 two;
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+                        two[x] = (__bf16)__builtin_amdgcn_exp2f(__builtin_fmaf(s[e / 8][2 * (e % 8) + x], a.scale, -top));
+                    const uint32_t which = sees(e / 8, 2 * (e % 8));
+                    pf[e] = mine ? __builtin_bit_cast(uint32_t, two) : 0;
+                    one[e] = mine ? (which & 1) * 0x3F80u | (which >> 1 & 1) * 0x3F800000u : 0;
+                }
+#pragma unroll
+                for (int i = 0; i < kSums; ++i) {
+                    const int e = i / ND * 4;
+                    const v4u v = __builtin_bit_cast(v4u, value_operand(slot, i));
+                    v4u finite, codes;
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        uint32_t f, c;
+                        take_apart(v[x], f, c);
+                        finite[x] = f;
+                        codes[x] = c;
+                    }
+                    acc[i % ND] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                        __builtin_bit_cast(bf8, finite), __builtin_bit_cast(bf8, make_uint4(pf[e], pf[e + 1], pf[e + 2], pf[e + 3])),
+                        acc[i % ND], 0, 0, 0);
+                    if (!__ballot((codes[0] | codes[1] | codes[2] | codes[3]) != 0)) continue;
+                    f16v among;
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) among[r] = 0.0f;
+                    among = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                        __builtin_bit_cast(bf8, codes), __builtin_bit_cast(bf8, make_uint4(one[e], one[e + 1], one[e + 2], one[e + 3])),
+                        among, 0, 0, 0);
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) acc[i % ND][r] = with_codes(acc[i % ND][r], (int)among[r]);
+                }
+            }
+            wait_vmcnt_barrier<0>();
         }
     }
     sum += __shfl_xor(sum, 32);
