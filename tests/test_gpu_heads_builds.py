@@ -192,6 +192,33 @@ def test_head_rope_cosines_past_their_room(gpu):
     close(y[dev(some, gpu)], want, bound)
 
 
+def test_head_rope_cosine_and_sine(gpu):
+    """Cosine and sine themselves, as the turned pair (1, 0), in units of 2^-25, half a step of a value from 1/2 to 1.
+
+    The rest x of at most an eighth of a turn is off by 1, its square z by 1.  Cosine: sin(x) <= 0.71 of the one and
+    half of the other, the last sum's rounding 1, that of its factor (from 1/4 to 1/2, a half) times z <= 0.62, and less
+    than 0.06 of what comes before: 2.6.  Sine: cos(x) <= 1 of x, the last rounding 1, z times x/6 <= 0.14, z x (half a unit)
+    times 1/6, its factor (a quarter) times x^3 <= 0.49, the series' rest 0.06: 2.5.  Near an eighth of a turn the mean of 65536
+    errors is that of the coefficients, 2^-30 times z^2 <= 0.39, and six times 2^-25 / sqrt(65536) at most: 2^-29.8."""
+    D, M = 256, 512
+    g = gen(9120)
+    rope, q = s3d8.Rope(D, device=gpu), torch.zeros(M, 1, D, device=gpu)
+    q[..., :D // 2] = 1
+
+    def turned(angles):  # [M][D / 2]: a call a row, its angles as frequencies
+        both = []
+        for row in angles:
+            rope.frequencies = dev(row, gpu)
+            both.append(s3d8.head_rope(q[:1], positions=torch.ones(1, dtype=torch.int64, device=gpu), rope=rope, out="f32"))
+        y = host(torch.cat(both))[:, 0]
+        return y[:, :D // 2] - np.cos(angles), y[:, D // 2:] - np.sin(angles)
+
+    for angles in (g.uniform(-20, 20, (M, D // 2)), np.pi / 4 * np.arange(-M * D // 4, M * D // 4).reshape(M, D // 2)):
+        c, s = turned(angles)
+        assert np.abs(c).max() <= 2.6 * 2.0 ** -25 and np.abs(s).max() <= 2.6 * 2.0 ** -25  # (either is either, by quarters)
+    assert abs(turned(g.uniform(0.7, np.pi / 4, (M, D // 2)))[0].mean()) <= 2.0 ** -29.8
+
+
 # ------------------------------------------------------------------ sample
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("top_k,top_p", [("rows", "rows"), (0, "rows"), (0, 1.0), (30, 0.9)])
