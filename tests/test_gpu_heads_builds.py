@@ -295,3 +295,31 @@ def test_sample_limits_outside_their_range_in_parts(gpu):
             want, share = ref.sample(logits[m], fine_u[m], fine_T[m], k[m], p[m], mp[m])
             assert int(token[m]) == want, m
             assert abs(float(prob[m]) - share) <= 2.0 ** -24 * share * 1.01 + 2.0 ** -43
+
+
+# ------------------------------------------------------------------ buffers for results
+def test_buffers_of_another_shape_are_refused(gpu):
+    """A buffer with as many elements in another order of the dimensions would be filled in the wrong places; one with
+    neighbouring dimensions joined takes the same bytes."""
+    g = gen(9300)
+    B, Lq, Lk, H, D, M = 2, 3, 20, 4, 32, 6
+    q, k, v = states(g, gpu, B, Lq, Lk, H, 2, D)
+    want = s3d8.cross_attention(q, k, v)
+    for shape in [(B, H, Lq, D), (Lq, B, H, D), (B, Lq, D, H), (B * Lq * 2, H * D // 2), (B, Lq * 2, H, D // 2)]:
+        o = torch.full(shape, 7.0, dtype=BF16, device=gpu)
+        with pytest.raises(ValueError):
+            s3d8.cross_attention(q, k, v, o=o)
+        assert (o == 7).all()
+    for shape in [(B, Lq, H * D), (B * Lq, H * D), (B * Lq, H, D), (B * Lq * H * D,)]:
+        o = torch.empty(shape, dtype=BF16, device=gpu)
+        assert s3d8.cross_attention(q, k, v, o=o) is o and torch.equal(o.view(q.shape), want)
+    logits, u = dev(g.standard_normal((M, 50)).astype(np.float32), gpu), dev(g.random(M, dtype=np.float32), gpu)
+    token, prob = s3d8.sample(logits, u)
+    for bad in [(2, 3), (3, 2)]:
+        with pytest.raises(ValueError):
+            s3d8.sample(logits, u, token=torch.empty(bad, dtype=torch.int32, device=gpu))
+        with pytest.raises(ValueError):
+            s3d8.sample(logits, u, prob=torch.empty(bad, dtype=F32, device=gpu))
+    column = torch.empty(M, 1, dtype=torch.int32, device=gpu)
+    assert s3d8.sample(logits, u, token=column)[0] is column and torch.equal(column[:, 0], token)
+    assert s3d8.sample(logits, u, token=token, prob=prob)[0] is token

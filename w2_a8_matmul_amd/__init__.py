@@ -26,6 +26,7 @@ frequencies), ``cross_attention`` (attention to an encoder's states) and
 from __future__ import annotations
 
 import ctypes
+import math
 
 import numpy as np
 
@@ -889,6 +890,19 @@ def _workspace(name, dev, key, args) -> int:
     return nbytes
 
 
+def _result(t, dtype, name, dev, shape):
+    """A caller's buffer for a result of ``shape``, or of that shape with neighbouring dimensions joined: another
+    order of the dimensions has as many elements, but not in these places."""
+    _dev_check(t, dtype, name, dev, numel=math.prod(shape))
+    left = [n for n in shape if n != 1]
+    for n in t.shape:
+        size = 1
+        while size < n and left:
+            size *= left.pop(0)
+        if size != n:
+            raise ValueError(f"{name} must be {list(shape)}, or that with neighbouring dimensions joined, got {tuple(t.shape)}")
+
+
 def cross_attention(q, k, v, *, kv_lens=None, mask=None, scale=None, out: str = "bf16", o=None, xq=None, xs=None):
     """Attention of query tokens to an encoder's states (see s3d8_cross_attention).
 
@@ -896,7 +910,8 @@ def cross_attention(q, k, v, *, kv_lens=None, mask=None, scale=None, out: str = 
     states that all sequences share; any strides that are multiples of 8, the entries of
     a head in a row.  ``kv_lens``: int32 [B] ([1] if shared), the states of each sequence
     (all Lk without).  ``mask``: bool [B or 1][Lq or 1][Lk], true where a token sees a
-    state.  A token that sees none has 0.  ``scale``: 1 / sqrt(D) unless given.
+    state.  A token that sees none has 0.  ``scale``: 1 / sqrt(D) unless given.  ``o`` takes the
+    result (also as [B][Lq][heads D] or [B Lq][heads D]; not over q, k or v).
 
     Returns o bf16 [B][Lq][heads][D], or its INT8 codes and scales for the output
     projection (xq [B Lq][heads D], xs [B Lq]) with ``out="codes"``."""
@@ -940,7 +955,7 @@ def cross_attention(q, k, v, *, kv_lens=None, mask=None, scale=None, out: str = 
     if o is None:
         o = torch.empty(B, Lq, H, D, dtype=bf16, device=dev)
     else:
-        _dev_check(o, bf16, "o", dev, numel=B * Lq * H * D)
+        _result(o, bf16, "o", dev, (B, Lq, H, D))
     if out == "codes":
         xq, xs = _codes_out(xq, xs, B * Lq, H * D, dev)
     elif xq is not None or xs is not None:
@@ -964,6 +979,7 @@ def sample(logits, u, *, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, token=N
     ``logits``: fp32 or bf16 [M][V], rows contiguous, any distance apart; ``u``: fp32 [M],
     uniform from [0, 1); ``temperature`` (0: the largest logit), ``top_k`` (0: all), ``top_p``
     (1: all), ``min_p`` (0: all): a number, or a device tensor [M] (fp32, ``top_k`` int32).
+    ``token``, ``prob``: buffers [M] for the results.
 
     Returns (token int32 [M], prob fp32 [M]), the probability among the tokens kept;
     -1 and 0 for a row of -infinity."""
@@ -990,11 +1006,11 @@ def sample(logits, u, *, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, token=N
     if token is None:
         token = torch.empty(M, dtype=torch.int32, device=dev)
     else:
-        _dev_check(token, torch.int32, "token", dev, numel=M)
+        _result(token, torch.int32, "token", dev, (M,))
     if prob is None:
         prob = torch.empty(M, dtype=torch.float32, device=dev)
     else:
-        _dev_check(prob, torch.float32, "prob", dev, numel=M)
+        _result(prob, torch.float32, "prob", dev, (M,))
     tail = (M, V, logits.stride(0) if M > 1 else V, *numbers, t)
     # what the workspace's size depends on
     nbytes = _workspace("s3d8_sample_workspace_bytes", dev, (M, V, t, numbers[1], pointers[1] != 0, pointers[2] != 0),
