@@ -16,9 +16,9 @@
 //   join  the parts' sums
 //
 // Few rows are bound by the reading of keys and values: 8 sequences of one token, 32 heads on 8 of 128,
-// 38 thousand states in all, 157 MB: 37 us, 4.3 TB/s (a copy reaches 5.1).  Many rows are bound by the
+// 38 thousand states in all, 157 MB: 36 to 38 us, 4.1 to 4.4 TB/s (a copy reaches 5.1).  Many rows are bound by the
 // matrix products and the exponentials beside them, of which each takes a SIMD about as
-// long: 2048 tokens on 6404 states, 215 GFLOP: 205 us, 1.05 PFLOP/s (a large product by itself 1.28);
+// long: 2048 tokens on 6404 states, 215 GFLOP: 201 to 205 us, 1.05 PFLOP/s (a large product by itself 1.28);
 // vector instructions in a product's shadow are not free (a 32 x 32 product 36 ticks, six fmas
 // 33, both together 50).
 #include <hip/hip_runtime.h>

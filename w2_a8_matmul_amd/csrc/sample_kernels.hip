@@ -18,8 +18,8 @@
 // 1024, thousands of equal logits) are done by `row` alone, digit by digit of the tokens'
 // order, in up to a dozen reads of the row (464 us for 5000 of one row's 128256 tokens).
 //
-// Many rows with a top-k are bound by the one read: 512 rows of 128256 fp32, 263 MB, k = 50: `part` 73 to
-// 82 us (51 without the lists, 5.1 TB/s as a copy), `row` 13.  Without a top-k `bins` and `step` are bound by
+// Many rows with a top-k are bound by the one read: 512 rows of 128256 fp32, 263 MB, k = 50: `part` 70 to
+// 74 us (51 without the lists, 5.1 TB/s as a copy), `row` 12.  Without a top-k `bins` and `step` are bound by
 // the exponentials in 64 bits, one a token: 111 and 146 us beside the 50 of `part`.  Few rows are bound
 // by the chain of steps in one workgroup, each of which waits for the last: one row, k = 50: 8 us
 // each of `part` and `row`.

@@ -108,18 +108,19 @@ def head_calls():
     dev = torch.device("cuda:0")
     bf, f32 = torch.bfloat16, torch.float32
 
-    def rope(M, H, Hk, D, dtype, norm=True, out="bf16"):
+    def rope(M, H, Hk, D, dtype, norm=True, out="bf16", position=True):
         def make():
             x = torch.randn(M, (H + 2 * Hk) * D, device=dev).to(dtype)
             handle = s3d8.Rope(D, 500000.0, scaling="llama3", factor=8.0, original_length=8192)
             w = 1 + 0.1 * torch.randn(D, device=dev) if norm else None
             q, k = x[:, :H * D].view(M, H, D), x[:, H * D:(H + Hk) * D].view(M, Hk, D)
-            pos = torch.arange(M, device=dev)
-            return lambda: s3d8.head_rope(q, k, pos, handle, q_weight=w, k_weight=w, out=out)
-        label = f"head_rope {M} x ({H} + {Hk}) x {D}, {dtype}{', norm' if norm else ''}, {out}".replace("torch.", "")
+            pos = torch.arange(M, device=dev) if position else None
+            return lambda: s3d8.head_rope(q, k, pos, handle if position else None, q_weight=w, k_weight=w, out=out)
+        label = f"head_rope {M} x ({H} + {Hk}) x {D}, {dtype}{', norm' if norm else ''}{'' if position else ' alone'}, {out}"
+        label = label.replace("torch.", "")
         return label, M * (H + Hk) * D * (dtype.itemsize + (2 if out == "bf16" else 4)), make
 
-    def attention(B, Lq, Lk, H, Hk, D, lens=False, shared=False, mask=False):
+    def attention(B, Lq, Lk, H, Hk, D, lens=False, shared=False, mask=False, out="bf16", lost=False):
         def make():
             n = 1 if shared else B
             q, k, v = (torch.randn(b, L, h, D, device=dev).to(bf) for b, L, h in ((B, Lq, H), (n, Lk, Hk), (n, Lk, Hk)))
@@ -128,19 +129,23 @@ def head_calls():
             if mask:  # four images, each seen by the tokens after it
                 starts = torch.tensor([0.05, 0.15, 0.3, 0.45], device=dev) * Lq
                 m = (torch.arange(Lq, device=dev)[:, None] >= starts).repeat_interleave(-(-Lk // 4), 1)[None, :, :Lk].contiguous()
-            return lambda: s3d8.cross_attention(q, k, v, kv_lens=ls, mask=m)
+            if lost:  # a value of the first image, which most tokens see
+                v[:, 0, :, 0] = float("inf")
+            return lambda: s3d8.cross_attention(q, k, v, kv_lens=ls, mask=m, out=out)
         label = (f"cross_attention {B} x {Lq} on {Lk}, {H} on {Hk} x {D}{', lengths from a half' if lens else ''}"
-                 f"{', shared states' if shared else ''}{', mask of four images' if mask else ''}")
+                 f"{', shared states' if shared else ''}{', mask of four images' if mask else ''}"
+                 f"{', an infinite value' if lost else ''}{', codes' if out == 'codes' else ''}")
         return label, 4 * (1 if shared else B) * Lk * Hk * D + 4 * B * Lq * H * D + mask * Lq * Lk, make
 
-    def sample(M, V, dtype, **limits):
+    def sample(M, V, dtype, temperature=0.9, **limits):
         def make():
             l = torch.randn(M, V, device=dev) * 2
             at = torch.rand(M, V, device=dev) < 40 / V
             l = torch.where(at, l + 8 * torch.rand(M, V, device=dev), l).to(dtype)
             u = torch.rand(M, device=dev)
-            return lambda: s3d8.sample(l, u, temperature=0.9, **limits)
-        label = f"sample {M} x {V}, {dtype}, {', '.join(f'{k} {v}' for k, v in limits.items())}".replace("torch.", "")
+            return lambda: s3d8.sample(l, u, temperature=temperature, **limits)
+        label = ", ".join([f"sample {M} x {V}", str(dtype), f"temperature {temperature}", *(f"{k} {v}" for k, v in limits.items())])
+        label = label.replace("torch.", "")
         return label, M * V * dtype.itemsize, make
 
     return [
@@ -151,6 +156,10 @@ def head_calls():
         sample(1, 128256, f32, top_k=50, top_p=0.9), sample(8, 128256, bf, top_p=0.95),
         sample(33, 5003, f32, top_k=200, top_p=0.8, min_p=0.05), sample(512, 128256, f32, top_k=50, top_p=0.95, min_p=0.01),
         sample(512, 128256, f32, top_p=0.95), sample(1, 128256, f32, top_k=1000, top_p=0.9), sample(1, 1000, f32, top_k=50, top_p=0.9),
+        sample(512, 128256, f32), sample(512, 128256, f32, temperature=0.0), sample(1, 128256, f32, temperature=0.0),
+        rope(2048, 32, 8, 128, bf, position=False), attention(1, 1, 1601, 32, 8, 128, out="codes"),
+        attention(1, 2048, 6404, 32, 8, 128, out="codes"), attention(1, 2048, 6404, 32, 8, 128, mask=True, lost=True),
+        attention(33, 1, 1601, 32, 8, 128),
     ]
 
 
